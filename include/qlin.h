@@ -437,6 +437,164 @@ int qlin_stream_copy(const void *src, void *dst, int64_t nbytes, void *stream);
 int qlin_mfma_ceiling(const int8_t *frags, int32_t *out, int workgroups, int iters,
                       void *stream);
 
+/* ------------------------------------------------- around the projection */
+
+/*
+ * RMS norm with the residual's addition and INT8 rows as its output: what
+ * stands between one projection of a model and the next.
+ *
+ *   x, residual  [rows, cols], dtype QLIN_F32 or QLIN_BF16 (both the same);
+ *                residual may be NULL.
+ *   gamma        [cols] fp32.
+ *   h            [rows, cols] output of x's type: rnd(x + residual), the
+ *                residual stream that goes on; NULL exactly when residual is
+ *                (the stream is then x itself).  May be x or residual.
+ *   q, s         [rows, cols] int8 and [rows] fp32 outputs: the codes and
+ *                scales, as qlin_quantize_rows defines them, of
+ *                rotate((h * rstd) * gamma), for the products.
+ *   rstd         [rows] fp32 output, 1 / sqrt(mean(h^2) + eps), which
+ *                qlin_rmsnorm_bwd takes.
+ *   y            [rows, cols] bf16 output or NULL: the values s * q that the
+ *                codes stand for, for float layers beside the projection (in
+ *                the rotated basis where had_block is set).
+ * Sums are fp32; the order is fixed.  A row of h whose sum of squares, or
+ * whose normalized values, are not finite gets s = NaN and q = 0, so that
+ * every product of it is NaN.  eps > 0 and finite.  rows >= 0; cols in
+ * [16, QLIN_MAX_ROW], a multiple of 16; had_block as in qlin_quantize_rows.
+ */
+int qlin_rmsnorm_quant(const void *x, const void *residual, int dtype, int64_t rows, int64_t cols,
+                       const float *gamma, float eps, int had_block, void *h, int8_t *q, float *s,
+                       float *rstd, void *y, void *stream);
+
+/*
+ * Backward of the norm (straight through the quantizer and the rotation: dn
+ * is the gradient of the unrotated normalized values, which is what the dX
+ * product with its rotation gives).
+ *
+ *   dn     [rows, cols], dn_dtype fp32 or bf16.
+ *   h      [rows, cols] of type dtype, rstd [rows]: as the forward left them.
+ *   dres   [rows, cols] of type dtype or NULL: the gradient that reaches h
+ *          from the residual stream.
+ *   dh     [rows, cols] output of type dtype: dres + rstd (g - xh mean(g xh))
+ *          with g = dn gamma, xh = h rstd; the gradient of x and of the
+ *          residual.  May be dres.
+ *   dgamma [cols] fp32 output: the sum over rows of dn xh (zeros for no rows).
+ * workspace: qlin_rmsnorm_bwd_ws_bytes(rows, cols) bytes, any contents.
+ */
+int qlin_rmsnorm_bwd(const void *dn, int dn_dtype, const void *h, const void *dres, int dtype,
+                     const float *rstd, const float *gamma, int64_t rows, int64_t cols, void *dh,
+                     float *dgamma, void *workspace, size_t ws_bytes, void *stream);
+size_t qlin_rmsnorm_bwd_ws_bytes(int64_t rows, int64_t cols);
+
+/*
+ * Low-rank adapters of many requests beside one shared projection.  Token m
+ * has the adapter ids[m]; an id outside [0, L) means none.  With x^ = sx qx,
+ * the values of the projection's own INT8 input:
+ *
+ *   u = scale[id] (x^ A[id]^T)                     [M, R]
+ *   y = sx sw (qx . qw^T) + bias + u B[id]^T       [M, N]
+ *
+ *   a      [L, R, K], b [L, N, R], both w_dtype fp32 or bf16.  A is held in
+ *          the basis of the codes: where they are rotated, A's rows are too
+ *          (qlin_hadamard), as the projection's weight rows are.
+ *   scale  [L] fp32, ids [M] int32.
+ *   u      [M, R] fp32 output, which the backward call takes.
+ * R is a multiple of 8 in [8, QLIN_MAX_RANK] (fill smaller ranks up with
+ * zeros); 1 <= L; M <= QLIN_MAX_ADAPTER_ROWS.  The projection's own part is
+ * exactly qlin_product_ws's; the adapter's part is summed in fp32 from
+ * operands kept to their 24 bits.  Any M, a single token too.
+ * workspace: qlin_adapter_fwd_ws_bytes bytes, zero-filled before its first use
+ * (every call leaves it ready for the next; calls that share one must not
+ * overlap in time).
+ */
+#define QLIN_MAX_RANK 128
+#define QLIN_MAX_ADAPTERS 1023          /* of the grouped and backward calls */
+#define QLIN_MAX_ADAPTER_ROWS 1048560
+int qlin_adapter_fwd(const int8_t *qx, const float *sx, const int8_t *qw, const float *sw,
+                     const float *bias, const void *a, const void *b, int w_dtype,
+                     const float *scale, const int32_t *ids, int64_t M, int64_t N, int64_t K,
+                     int64_t L, int64_t R, float *u, float *y, void *workspace, size_t ws_bytes,
+                     void *stream);
+size_t qlin_adapter_fwd_ws_bytes(int64_t M, int64_t N, int64_t K, int64_t L, int64_t R);
+
+/*
+ * The tokens grouped by adapter, for qlin_adapter_bwd: a batch's plan, made
+ * once for all its layers.  order [M] int32 lists the tokens adapter by
+ * adapter, each one's in their own order, those without an adapter last;
+ * start [L + 1] int32: adapter l's are order[start[l]] .. order[start[l + 1] - 1].
+ * L <= QLIN_MAX_ADAPTERS.
+ */
+int qlin_adapter_group(const int32_t *ids, int64_t M, int64_t L, int32_t *order, int32_t *start,
+                       void *stream);
+
+/*
+ * Backward of qlin_adapter_fwd with a frozen projection:
+ *
+ *   v  = scale[id] (dY B[id])                                       [M, R]
+ *   dx = rotate(sg1 (qg1 . qw) + v A[id])                           [M, K]
+ *   da[l] = sum over l's tokens of v^T x^, db[l] = the same of dY^T u, fp32,
+ *           [L, R, K] and [L, N, R], zeros for an adapter without tokens
+ *
+ *   dy     [M, N] fp32 or bf16 (dy_dtype); qg1, sg1: its codes as the dX
+ *          product takes them (qlin_quantize_rows of dY with prescale sw).
+ *   u      as the forward call gave it; order and start as qlin_adapter_group
+ *          gave them for the same ids.
+ *   dx     may be NULL (then qg1, sg1 and qw may be too): adapter gradients only.
+ * The sums over tokens are fp32, in a fixed order.  Limits as in the forward
+ * call, L <= QLIN_MAX_ADAPTERS; had_block as in qlin_bwd_dx.
+ * workspace: qlin_adapter_bwd_ws_bytes bytes, zero-filled before its first use.
+ */
+int qlin_adapter_bwd(const void *dy, int dy_dtype, const int8_t *qg1, const float *sg1,
+                     const int8_t *qw, const int8_t *qx, const float *sx, const float *u,
+                     const void *a, const void *b, int w_dtype, const float *scale,
+                     const int32_t *ids, const int32_t *order, const int32_t *start, int64_t M,
+                     int64_t N, int64_t K, int64_t L, int64_t R, int had_block, float *dx,
+                     float *da, float *db, void *workspace, size_t ws_bytes, void *stream);
+size_t qlin_adapter_bwd_ws_bytes(int64_t M, int64_t N, int64_t K, int64_t L, int64_t R);
+
+/*
+ * AdamW (decoupled weight decay, bias-corrected moments) over a list of float
+ * tensors in one launch.  A plan is made once from the tensors' addresses:
+ * qlin_adamw_tensors_plan checks the list and writes qlin_adamw_tensors_plan_bytes
+ * bytes to `image` (host memory), which the caller copies to the device
+ * (16-byte aligned) and hands to every step.
+ *
+ *   p [numel] fp32 or bf16, updated in place; g [numel] fp32 or bf16.
+ *   state_bits 32: m, v [numel] fp32, the moments; scales NULL.
+ *   state_bits 8:  m, v [numel] e4m3 codes with scales m_scale, v_scale
+ *                  [ceil(numel / 256)] fp32, one per 256 elements: m's values
+ *                  and the ROOT of the second moment's; zeros to start with.
+ *   index0         index of the tensor's first element in the rounding's
+ *                  uniforms, a multiple of 8: ranges that do not overlap give
+ *                  every element its own.
+ *   weight_decay   >= 0, per tensor.
+ *
+ *   m' = b1 m + (1 - b1) g, v' = b2 v + (1 - b2) g^2,
+ *   p' = p (1 - lr wd) - lr / (1 - b1^t) m' / (sqrt(v') / sqrt(1 - b2^t) + eps)
+ *
+ * in fp32.  8-bit blocks are scaled so that the largest value becomes 448; m
+ * is rounded to nearest, the root stochastically and never from above zero to
+ * zero; bf16 parameters are rounded stochastically.  The uniforms are Philox
+ * 4x32-10 with key seed and counter (index >> 3, step), as in qlin_sgd_requant,
+ * with the counter's top bit set for the parameters.  A block whose largest
+ * value is below 2^-100 holds zeros; one with a NaN has a NaN scale.
+ */
+typedef struct qlin_tensor {
+    void *p;
+    const void *g;
+    void *m, *v;
+    float *m_scale, *v_scale;
+    int64_t numel, index0;
+    float weight_decay;
+    int p_dtype, g_dtype, state_bits;
+} qlin_tensor;
+int64_t qlin_adamw_tensors_chunks(const qlin_tensor *tensors, int64_t count);
+size_t qlin_adamw_tensors_plan_bytes(const qlin_tensor *tensors, int64_t count);
+int qlin_adamw_tensors_plan(const qlin_tensor *tensors, int64_t count, void *image,
+                            size_t image_bytes);
+int qlin_adamw_tensors(const void *image, int64_t count, int64_t chunks, double lr, double beta1,
+                       double beta2, double eps, uint64_t seed, uint64_t step, void *stream);
+
 #ifdef __cplusplus
 }
 #endif

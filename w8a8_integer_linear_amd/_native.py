@@ -6,6 +6,7 @@ the C ABI, and a nonzero status raises QlinError.  Every step of the layer runs
 in the library's HIP kernels; there is no fallback.
 """
 import ctypes
+import functools
 import os
 
 import torch
@@ -17,10 +18,22 @@ QLIN_OK, QLIN_EINVAL, QLIN_EUNSUPPORTED, QLIN_EDEVICE = 0, 1, 2, 3
 QLIN_F32, QLIN_BF16 = 0, 1
 QLIN_OP_FWD, QLIN_OP_DX, QLIN_OP_DW = 0, 1, 2
 MAX_CONTRACTION = 131071
+MAX_RANK, MAX_ADAPTERS = 128, 1023
 
 # Exported symbols and their C signatures (kept in step with include/qlin.h).
 _vp, _i64, _i32, _f32, _u64 = (ctypes.c_void_p, ctypes.c_int64, ctypes.c_int, ctypes.c_float,
                                ctypes.c_uint64)
+_f64, _size = ctypes.c_double, ctypes.c_size_t
+
+
+class TensorDesc(ctypes.Structure):
+    """qlin_tensor of include/qlin.h."""
+    _fields_ = [("p", _vp), ("g", _vp), ("m", _vp), ("v", _vp), ("m_scale", _vp),
+                ("v_scale", _vp), ("numel", _i64), ("index0", _i64), ("weight_decay", _f32),
+                ("p_dtype", _i32), ("g_dtype", _i32), ("state_bits", _i32)]
+
+
+_tensors = ctypes.POINTER(TensorDesc)
 SIGNATURES = {
     "qlin_status_string": ([_i32], ctypes.c_char_p),
     "qlin_abi_version": ([], _i32),
@@ -47,6 +60,22 @@ SIGNATURES = {
     "qlin_product_noalloc": ([_i32, _vp, _vp, _vp, _vp, _vp, _i64, _i64, _i64, _i32, _vp, _vp],
                              _i32),
     "qlin_mfma_ceiling": ([_vp, _vp, _i32, _i32, _vp], _i32),
+    "qlin_rmsnorm_quant": ([_vp, _vp, _i32, _i64, _i64, _vp, _f32, _i32, _vp, _vp, _vp, _vp, _vp,
+                            _vp], _i32),
+    "qlin_rmsnorm_bwd": ([_vp, _i32, _vp, _vp, _i32, _vp, _vp, _i64, _i64, _vp, _vp, _vp, _size,
+                          _vp], _i32),
+    "qlin_rmsnorm_bwd_ws_bytes": ([_i64, _i64], _size),
+    "qlin_adapter_fwd": ([_vp] * 7 + [_i32, _vp, _vp] + [_i64] * 5 + [_vp, _vp, _vp, _size, _vp],
+                         _i32),
+    "qlin_adapter_fwd_ws_bytes": ([_i64] * 5, _size),
+    "qlin_adapter_group": ([_vp, _i64, _i64, _vp, _vp, _vp], _i32),
+    "qlin_adapter_bwd": ([_vp, _i32] + [_vp] * 8 + [_i32] + [_vp] * 4 + [_i64] * 5
+                         + [_i32, _vp, _vp, _vp, _vp, _size, _vp], _i32),
+    "qlin_adapter_bwd_ws_bytes": ([_i64] * 5, _size),
+    "qlin_adamw_tensors_chunks": ([_tensors, _i64], _i64),
+    "qlin_adamw_tensors_plan_bytes": ([_tensors, _i64], _size),
+    "qlin_adamw_tensors_plan": ([_tensors, _i64, _vp, _size], _i32),
+    "qlin_adamw_tensors": ([_vp, _i64, _i64, _f64, _f64, _f64, _f64, _u64, _u64, _vp], _i32),
 }
 MFMA_CEILING_FRAG_BYTES = 24 * 1024
 NOALLOC_SCRATCH_BYTES = 4096 + 160 * 262144
@@ -380,3 +409,231 @@ def qlin_mfma_ceiling(frags, out, workgroups, iters, stream=None):
     _check("qlin_mfma_ceiling", lib().qlin_mfma_ceiling(_ptr(frags), _ptr(out), int(workgroups),
                                                         int(iters), _stream(stream)))
     return out
+
+
+# ------------------------------------------------- around the projection
+
+def _on_stream(f):
+    """Runs f inside its `stream` argument's context, so that what it allocates
+    (outputs, a workspace) is allocated, cleared and freed in that stream's order."""
+    @functools.wraps(f)
+    def call(*args, stream=None, **kw):
+        if stream is None:
+            return f(*args, **kw)
+        with torch.cuda.stream(stream):
+            return f(*args, stream=stream, **kw)
+    return call
+
+
+def _workspace(workspace, need, like, zero):
+    """A call's workspace: the caller's, or a fresh one."""
+    if workspace is None:
+        make = torch.zeros if zero else torch.empty
+        return make(need, dtype=torch.uint8, device=like.device) if need else None
+    return _need(workspace, "workspace", torch.uint8)
+
+
+def _bytes(workspace):
+    return 0 if workspace is None else workspace.numel()
+
+
+@_on_stream
+def qlin_rmsnorm_quant(x, gamma, eps, residual=None, had_block=0, h=None, q=None, s=None,
+                       rstd=None, y=None, want_y=False, stream=None):
+    """RMS norm of h = x + residual with INT8 rows as its output.  Returns
+    (q, s, h, rstd, y): h is x itself without a residual, y (bf16 values of the
+    codes) None unless given or wanted."""
+    rows, cols = x.shape
+    _need(x, "x", x.dtype)
+    code = _dtype_code(x)
+    _need(gamma, "gamma", torch.float32, (cols,))
+    if residual is not None:
+        _need(residual, "residual", x.dtype, (rows, cols))
+        h = _empty((rows, cols), x.dtype, x) if h is None else _need(h, "h", x.dtype, (rows, cols))
+    q = _empty((rows, cols), torch.int8, x) if q is None else _need(q, "q", torch.int8, (rows, cols))
+    s = _empty((rows,), torch.float32, x) if s is None else _need(s, "s", torch.float32, (rows,))
+    rstd = (_empty((rows,), torch.float32, x) if rstd is None
+            else _need(rstd, "rstd", torch.float32, (rows,)))
+    if y is None and want_y:
+        y = _empty((rows, cols), torch.bfloat16, x)
+    _opt(y, "y", torch.bfloat16, (rows, cols))
+    _check("qlin_rmsnorm_quant", lib().qlin_rmsnorm_quant(
+        _ptr(x), _ptr(residual), code, rows, cols, _ptr(gamma), float(eps), int(had_block),
+        None if residual is None else _ptr(h), _ptr(q), _ptr(s), _ptr(rstd), _ptr(y),
+        _stream(stream)))
+    return q, s, x if residual is None else h, rstd, y
+
+
+def qlin_rmsnorm_bwd_ws_bytes(rows, cols):
+    return int(lib().qlin_rmsnorm_bwd_ws_bytes(int(rows), int(cols)))
+
+
+@_on_stream
+def qlin_rmsnorm_bwd(dn, h, rstd, gamma, dres=None, dh=None, dgamma=None, workspace=None,
+                     stream=None):
+    """Backward of the norm.  Returns (dh, dgamma)."""
+    rows, cols = h.shape
+    _need(dn, "dn", dn.dtype, (rows, cols))
+    _need(h, "h", h.dtype)
+    dn_code, code = _dtype_code(dn), _dtype_code(h)
+    _need(rstd, "rstd", torch.float32, (rows,))
+    _need(gamma, "gamma", torch.float32, (cols,))
+    _opt(dres, "dres", h.dtype, (rows, cols))
+    dh = _empty((rows, cols), h.dtype, h) if dh is None else _need(dh, "dh", h.dtype, (rows, cols))
+    dgamma = (_empty((cols,), torch.float32, h) if dgamma is None
+              else _need(dgamma, "dgamma", torch.float32, (cols,)))
+    workspace = _workspace(workspace, qlin_rmsnorm_bwd_ws_bytes(rows, cols), h, zero=False)
+    _check("qlin_rmsnorm_bwd", lib().qlin_rmsnorm_bwd(
+        _ptr(dn), dn_code, _ptr(h), _ptr(dres), code, _ptr(rstd), _ptr(gamma), rows, cols,
+        _ptr(dh), _ptr(dgamma), _ptr(workspace), _bytes(workspace), _stream(stream)))
+    return dh, dgamma
+
+
+def _adapters(a, b, scale, ids, M, N, K):
+    L, R = a.shape[:2]
+    _need(a, "a", a.dtype, (L, R, K))
+    _need(b, "b", a.dtype, (L, N, R))
+    _need(scale, "scale", torch.float32, (L,))
+    _need(ids, "ids", torch.int32, (M,))
+    return L, R, _dtype_code(a)
+
+
+def qlin_adapter_fwd_ws_bytes(M, N, K, L, R):
+    return int(lib().qlin_adapter_fwd_ws_bytes(int(M), int(N), int(K), int(L), int(R)))
+
+
+@_on_stream
+def qlin_adapter_fwd(qx, sx, qw, sw, a, b, scale, ids, bias=None, y=None, u=None, workspace=None,
+                     stream=None):
+    """The shared projection with each token's adapter.  Returns (y, u)."""
+    M, K = qx.shape
+    N = qw.shape[0]
+    _need(qx, "qx", torch.int8)
+    _need(qw, "qw", torch.int8, (N, K))
+    _need(sx, "sx", torch.float32, (M,))
+    _need(sw, "sw", torch.float32, (N,))
+    _opt(bias, "bias", torch.float32, (N,))
+    L, R, code = _adapters(a, b, scale, ids, M, N, K)
+    y = _empty((M, N), torch.float32, qx) if y is None else _need(y, "y", torch.float32, (M, N))
+    u = _empty((M, R), torch.float32, qx) if u is None else _need(u, "u", torch.float32, (M, R))
+    workspace = _workspace(workspace, 0 if workspace is not None else
+                           qlin_adapter_fwd_ws_bytes(M, N, K, L, R), qx, zero=True)
+    _check("qlin_adapter_fwd", lib().qlin_adapter_fwd(
+        _ptr(qx), _ptr(sx), _ptr(qw), _ptr(sw), _ptr(bias), _ptr(a), _ptr(b), code, _ptr(scale),
+        _ptr(ids), M, N, K, L, R, _ptr(u), _ptr(y), _ptr(workspace), _bytes(workspace),
+        _stream(stream)))
+    return y, u
+
+
+@_on_stream
+def qlin_adapter_group(ids, L, order=None, start=None, stream=None):
+    """Tokens grouped by adapter, for qlin_adapter_bwd.  Returns (order, start)."""
+    M, = ids.shape
+    L = int(L)
+    _need(ids, "ids", torch.int32)
+    order = (_empty((M,), torch.int32, ids) if order is None
+             else _need(order, "order", torch.int32, (M,)))
+    start = (_empty((L + 1,), torch.int32, ids) if start is None
+             else _need(start, "start", torch.int32, (L + 1,)))
+    _check("qlin_adapter_group", lib().qlin_adapter_group(
+        _ptr(ids), M, L, _ptr(order), _ptr(start), _stream(stream)))
+    return order, start
+
+
+def qlin_adapter_bwd_ws_bytes(M, N, K, L, R):
+    return int(lib().qlin_adapter_bwd_ws_bytes(int(M), int(N), int(K), int(L), int(R)))
+
+
+@_on_stream
+def qlin_adapter_bwd(dy, qg1, sg1, qw, qx, sx, u, a, b, scale, ids, order, start, had_block=0,
+                     dx=None, da=None, db=None, workspace=None, want_dx=True, stream=None):
+    """Input and adapter gradients of qlin_adapter_fwd with a frozen projection.
+    Returns (dx, da, db); dx is None with want_dx=False."""
+    M, N = dy.shape
+    K = qx.shape[1]
+    _need(dy, "dy", dy.dtype)
+    dy_code = _dtype_code(dy)
+    _need(qx, "qx", torch.int8, (M, K))
+    _need(sx, "sx", torch.float32, (M,))
+    L, R, code = _adapters(a, b, scale, ids, M, N, K)
+    _need(u, "u", torch.float32, (M, R))
+    _need(order, "order", torch.int32, (M,))
+    _need(start, "start", torch.int32, (L + 1,))
+    if want_dx:
+        _need(qg1, "qg1", torch.int8, (M, N))
+        _need(sg1, "sg1", torch.float32, (M,))
+        _need(qw, "qw", torch.int8, (N, K))
+        dx = (_empty((M, K), torch.float32, dy) if dx is None
+              else _need(dx, "dx", torch.float32, (M, K)))
+    else:
+        qg1 = sg1 = qw = dx = None
+    da = (_empty((L, R, K), torch.float32, dy) if da is None
+          else _need(da, "da", torch.float32, (L, R, K)))
+    db = (_empty((L, N, R), torch.float32, dy) if db is None
+          else _need(db, "db", torch.float32, (L, N, R)))
+    workspace = _workspace(workspace, 0 if workspace is not None else
+                           qlin_adapter_bwd_ws_bytes(M, N, K, L, R), dy, zero=True)
+    _check("qlin_adapter_bwd", lib().qlin_adapter_bwd(
+        _ptr(dy), dy_code, _ptr(qg1), _ptr(sg1), _ptr(qw), _ptr(qx), _ptr(sx), _ptr(u), _ptr(a),
+        _ptr(b), code, _ptr(scale), _ptr(ids), _ptr(order), _ptr(start), M, N, K, L, R,
+        int(had_block), _ptr(dx), _ptr(da), _ptr(db), _ptr(workspace), _bytes(workspace),
+        _stream(stream)))
+    return dx, da, db
+
+
+class AdamWPlan:
+    """The device image of a list of tensors (qlin_adamw_tensors_plan); holds
+    the tensors, whose addresses are in the image."""
+
+    def __init__(self, image, count, chunks, tensors):
+        self.image, self.count, self.chunks, self.tensors = image, count, chunks, tensors
+
+
+def qlin_adamw_tensors_plan(tensors):
+    """A plan for qlin_adamw_tensors.  tensors: a list of dicts with p and g
+    (fp32 or bf16, of one shape), m and v (both fp32 of that shape, or both
+    float8_e4m3fn with m_scale and v_scale, fp32 of one value per 256
+    elements), weight_decay (0.0) and index0 (by default, tensors follow one
+    another at multiples of 256)."""
+    tensors = [dict(t) for t in tensors]
+    descs = (TensorDesc * max(1, len(tensors)))()
+    at, device = 0, None
+    for d, t in zip(descs, tensors):
+        p, n = t["p"], t["p"].numel()
+        _need(p, "p", p.dtype)
+        _need(t["g"], "g", t["g"].dtype, p.shape)
+        eight = t["m"].dtype == torch.float8_e4m3fn
+        for name in ("m", "v"):
+            _need(t[name], name, torch.float8_e4m3fn if eight else torch.float32, p.shape)
+            if eight:
+                _need(t.get(name + "_scale"), name + "_scale", torch.float32, (-(-n // 256),))
+            elif t.get(name + "_scale") is not None:
+                raise ValueError(f"{name}_scale belongs to 8-bit moments")
+        if device is None:
+            device = p.device
+        if any(t[k].device != device for k in ("p", "g", "m", "v")):
+            raise ValueError("the tensors are on different devices")
+        t.setdefault("index0", at)
+        at = t["index0"] + -(-n // 256) * 256
+        d.p, d.g, d.m, d.v = (t[k].data_ptr() for k in ("p", "g", "m", "v"))
+        if eight:
+            d.m_scale, d.v_scale = t["m_scale"].data_ptr(), t["v_scale"].data_ptr()
+        d.numel, d.index0, d.weight_decay = n, t["index0"], t.get("weight_decay", 0.0)
+        d.p_dtype, d.g_dtype, d.state_bits = _dtype_code(p), _dtype_code(t["g"]), 8 if eight else 32
+    n = len(tensors)
+    size = int(lib().qlin_adamw_tensors_plan_bytes(descs, n))
+    image = torch.zeros(max(size, 1), dtype=torch.uint8)
+    _check("qlin_adamw_tensors_plan", lib().qlin_adamw_tensors_plan(
+        descs, n, ctypes.c_void_p(image.data_ptr()), size))
+    chunks = int(lib().qlin_adamw_tensors_chunks(descs, n))
+    return AdamWPlan(image.to(device) if chunks else None, n, chunks, tensors)
+
+
+@_on_stream
+def qlin_adamw_tensors(plan, lr, beta1, beta2, eps, seed, step, stream=None):
+    """One AdamW step over the plan's tensors, in place (step >= 1)."""
+    if stream is not None and plan.image is not None:
+        plan.image.record_stream(stream)    # the plan may be dropped before the step has run
+    _check("qlin_adamw_tensors", lib().qlin_adamw_tensors(
+        _ptr(plan.image), plan.count, plan.chunks, lr, beta1, beta2, eps, int(seed), int(step),
+        _stream(stream)))

@@ -106,4 +106,48 @@ void launch_adamw_requant(int8_t *qw, float *sw, const float *dw, float *m, floa
                           int64_t K, const AdamConsts &k, uint64_t seed, uint64_t step,
                           float *bias, const float *db, float *bm, float *bv, hipStream_t st);
 
+// RMS norm with the residual's addition and INT8 rows as its output, and its
+// backward pass (norm.hip).  part holds rmsnorm_bwd_parts(rows, cols) rows of
+// cols floats.
+void launch_rmsnorm_quant(const void *x, const void *res, bool bf16, int64_t rows, int64_t cols,
+                          const float *gamma, float eps, int had, float cb, void *h, int8_t *q,
+                          float *s, float *rstd, void *y, hipStream_t st);
+int rmsnorm_bwd_parts(int64_t rows, int64_t cols);
+void launch_rmsnorm_bwd(const void *dn, bool dn_bf16, const void *h, const void *dres, bool bf16,
+                        const float *rstd, const float *gamma, int64_t rows, int64_t cols, void *dh,
+                        float *dgamma, float *part, hipStream_t st);
+
+// AdamW over the tensors of a device image (tensors.hpp, adamw.hip).
+struct AdamTensorConsts {
+    float b1, b2, eps, a1, a2, c1, c2, lr;
+};
+void launch_adamw_tensors(const void *image, int64_t count, int64_t chunks, const AdamTensorConsts &k,
+                          uint64_t seed, uint64_t step, hipStream_t st);
+
+// Low-rank adapters beside a projection (adapter.hip).  a [L, R, K] and b
+// [L, N, R] are fp32 or bf16; ids [M] names each token's adapter.
+constexpr int kMaxAdapters = 1023;
+struct AdapterArgs {
+    const void *a, *b;
+    bool bf16;
+    const float *scale;
+    const int32_t *ids;
+    int64_t M, N, K;
+    int L, R;
+};
+// u = scale x^ A^T, then y += u B^T.
+void launch_adapter_fwd(const AdapterArgs &g, const int8_t *qx, const float *sx, float *u, float *y,
+                        hipStream_t st);
+void launch_adapter_group(const int32_t *ids, int64_t M, int L, int32_t *order, int32_t *start,
+                          hipStream_t st);
+// Backward, with a workspace of adapter_bwd_bytes: v = scale dY B (kept in
+// the workspace), dx += v A, then both adapter gradients.
+size_t adapter_bwd_bytes(int64_t M, int64_t N, int64_t K, int64_t L, int64_t R);
+void launch_adapter_bwd_v(const AdapterArgs &g, const void *dy, bool dy_bf16, void *ws,
+                          hipStream_t st);
+void launch_adapter_bwd_dx(const AdapterArgs &g, float *dx, void *ws, hipStream_t st);
+void launch_adapter_bwd_w(const AdapterArgs &g, const void *dy, bool dy_bf16, const int8_t *qx,
+                          const float *sx, const float *u, const int32_t *order,
+                          const int32_t *start, float *da, float *db, void *ws, hipStream_t st);
+
 } // namespace qlin

@@ -6,34 +6,11 @@
 // the rounding.  AdamW reads and writes its fp32 moments in the same pass.
 #include "common.hpp"
 #include "launch.hpp"
+#include "philox.hpp"
 
 namespace qlin {
 
 namespace {
-
-// Philox-4x32-10 (Salmon, Moraes, Dror, Shaw, SC'11): per round, words 0 and
-// 2 are multiplied by the round multipliers with full 64-bit products; the
-// new counter is (hi(M1*c2) ^ c1 ^ k0, lo(M1*c2), hi(M0*c0) ^ c3 ^ k1,
-// lo(M0*c0)); the key advances by the Weyl constants between rounds.
-__device__ __forceinline__ void philox4x32_10(uint32_t c[4], uint32_t k0, uint32_t k1)
-{
-#pragma unroll
-    for (int r = 0; r < 10; r++) {
-        if (r > 0) {
-            k0 += 0x9E3779B9u;
-            k1 += 0xBB67AE85u;
-        }
-        const uint64_t p0 = (uint64_t)0xD2511F53u * c[0];
-        const uint64_t p1 = (uint64_t)0xCD9E8D57u * c[2];
-        // Three-input exclusive or in one instruction (truth table 0x96).
-        const uint32_t n0 = __builtin_amdgcn_bitop3_b32((uint32_t)(p1 >> 32), c[1], k0, 0x96);
-        const uint32_t n2 = __builtin_amdgcn_bitop3_b32((uint32_t)(p0 >> 32), c[3], k1, 0x96);
-        c[1] = (uint32_t)p1;
-        c[3] = (uint32_t)p0;
-        c[0] = n0;
-        c[2] = n2;
-    }
-}
 
 // AdamW state and step constants (computed on the host, each rounded once
 // from double): a1 = 1 - b1, a2 = 1 - b2, c1 = lr / (1 - b1^t),
