@@ -19,6 +19,8 @@
 // A chunk of 4096 elements is one workgroup's work; a lane holds two runs of
 // eight elements, and 16 lanes a block of 256, whose absmax is found with four
 // DPP steps.  One read and one write of each array: the HBM traffic bounds it.
+#include <type_traits>
+
 #include "common.hpp"
 #include "launch.hpp"
 #include "lowp.hpp"
@@ -65,36 +67,123 @@ __device__ __forceinline__ i32x2 pack_e4m3x8(const float v[8])
     return w;
 }
 
-// t in [0, 448] rounded to an e4m3 value, up with the probability that r16 /
-// 2^16 gives: r16 is added below the last kept mantissa bit, then the rest is
-// cut off.  Values below 2^-6 are e4m3 subnormals, multiples of 2^-9: adding
-// 2^-6 gives them that last bit.
-__device__ __forceinline__ float stochastic_e4m3(float t, uint32_t r16)
+// Eight values t in [0, 448] as e4m3 codes, each rounded up with the
+// probability that its place between two codes gives: the conversion adds the
+// uniform r16 / 2^16 (seed = r16 << 16) below the last kept bit and cuts off.
+// A value above zero gets at least the smallest code, 2^-9: the median of t,
+// 2^-9 and 2^100 t is 0 for 0, 2^-9 below 2^-9 and t above.
+__device__ __forceinline__ i32x2 stochastic_e4m3x8(const float t[8], const uint32_t x[4])
 {
-    const float low = t < 0x1p-6f ? 0x1p-6f : 0.0f;
-    const uint32_t bits = (__float_as_uint(t + low) + (r16 << 4)) & ~0xFFFFFu;
-    const float near = __uint_as_float(bits) - low;
-    return t > 0.0f ? fmaxf(near, 0x1p-9f) : near;
+    i32x2 w = {0, 0};
+#pragma unroll
+    for (int h = 0; h < 2; h++) {
+        int c = 0;
+        auto put = [&](auto E) {
+            constexpr int e = decltype(E)::value;
+            const float v = t[4 * h + e];
+            const uint32_t word = x[2 * h + e / 2];
+            const uint32_t seed = e % 2 ? word & 0xFFFF0000u : word << 16;
+            c = __builtin_amdgcn_cvt_sr_fp8_f32(
+                __builtin_amdgcn_fmed3f(v, 0x1p-9f, v * 0x1p100f), (int)seed, c, e);
+        };
+        put(std::integral_constant<int, 0>{});
+        put(std::integral_constant<int, 1>{});
+        put(std::integral_constant<int, 2>{});
+        put(std::integral_constant<int, 3>{});
+        w[h] = c;
+    }
+    return w;
 }
 
-// The 16-bit uniforms of the eight elements from index 8 blk.
+// The 16-bit uniforms of the eight elements from index 8 blk, two per word.
 __device__ __forceinline__ void uniforms8(const StepArgs &a, uint64_t blk, uint32_t stream,
-                                          uint32_t r[8])
+                                          uint32_t x[4])
 {
-    uint32_t x[4] = {(uint32_t)blk, (uint32_t)(blk >> 32), a.step_lo, a.step_hi + stream};
+    x[0] = (uint32_t)blk;
+    x[1] = (uint32_t)(blk >> 32);
+    x[2] = a.step_lo;
+    x[3] = a.step_hi + stream;
     philox4x32_10(x, a.seed_lo, a.seed_hi);
+}
+
+// Eight floats as bf16, rounded stochastically with the uniforms x; infinities
+// and NaN (which adding to the bits would turn into one another) as they are.
+__device__ __forceinline__ i32x4 stochastic_bf16x8(const float v[8], const uint32_t x[4])
+{
+    float top = 0.0f;
 #pragma unroll
     for (int e = 0; e < 8; e++)
-        r[e] = (x[e >> 1] >> (16 * (e & 1))) & 0xFFFFu;
+        top = max_nan(top, __builtin_fabsf(v[e]));
+    const bool finite = top < __builtin_inff();
+    i32x4 w;
+#pragma unroll
+    for (int e = 0; e < 4; e++) {
+        uint32_t lo = __float_as_uint(v[2 * e]) + (x[e] & 0xFFFFu);
+        uint32_t hi = __float_as_uint(v[2 * e + 1]) + (x[e] >> 16);
+        if (!finite) {
+            lo = __builtin_fabsf(v[2 * e]) < __builtin_inff() ? lo : __float_as_uint(v[2 * e]);
+            hi = __builtin_fabsf(v[2 * e + 1]) < __builtin_inff() ? hi : __float_as_uint(v[2 * e + 1]);
+            // a NaN stays one when its low half is cut off
+            lo |= v[2 * e] != v[2 * e] ? 0x400000u : 0u;
+            hi |= v[2 * e + 1] != v[2 * e + 1] ? 0x400000u : 0u;
+        }
+        w[e] = (int)__builtin_amdgcn_perm(hi, lo, 0x07060302u);
+    }
+    return w;
+}
+
+// sqrt(v) within half an ulp and a relative 2^-46, for every v of a lane in
+// [2^-96, 2^96]: the hardware's reciprocal root and one correction of s = v y
+// by (v - s^2) y / 2 (eight issue slots against seventeen for the correctly
+// rounded root).  Other values take the correctly rounded root.
+template <int N> __device__ __forceinline__ void roots(const float v[N], float r[N])
+{
+    float lo = v[0], hi = v[0];
+#pragma unroll
+    for (int e = 1; e < N; e++) {
+        lo = fminf(lo, v[e]);
+        hi = fmaxf(hi, v[e]);
+    }
+    if (lo >= 0x1p-96f && hi <= 0x1p96f) {
+#pragma unroll
+        for (int e = 0; e < N; e++) {
+            const float y = __builtin_amdgcn_rsqf(v[e]), s = v[e] * y;
+            r[e] = __builtin_fmaf(__builtin_fmaf(-s, s, v[e]), 0.5f * y, s);
+        }
+    } else {
+#pragma unroll
+        for (int e = 0; e < N; e++)
+            r[e] = __builtin_sqrtf(v[e]);
+    }
+}
+
+// Global memory at a pointer that was itself read from memory (the compiler
+// would take it for a generic one and use flat accesses).
+template <typename T> __device__ __forceinline__ T gload(const void *p, int64_t byte)
+{
+    typedef const __attribute__((address_space(1))) T *G;
+    return *(G)(uintptr_t)(static_cast<const char *>(p) + byte);
+}
+template <typename T> __device__ __forceinline__ void gstore(void *p, int64_t byte, T v)
+{
+    typedef __attribute__((address_space(1))) T *G;
+    *(G)(uintptr_t)(static_cast<char *>(p) + byte) = v;
 }
 
 // Eight elements from 'idx' of an fp32 or bf16 array of n; those past its end
-// read as zeros.
-template <bool BF16>
-__device__ __forceinline__ void load8_tail(const void *p, int64_t idx, int64_t n, float v[8])
+// read as zeros.  WHOLE: there are none.
+template <bool BF16, bool WHOLE>
+__device__ __forceinline__ void load_eight(const void *p, int64_t idx, int64_t n, float v[8])
 {
-    if (idx + 8 <= n) {
-        load8<BF16>(p, idx, v);
+    if (WHOLE || idx + 8 <= n) {
+        Raw8<BF16> r;
+        if constexpr (BF16) {
+            r.w = gload<i32x4>(p, idx * 2);
+        } else {
+            r.a = gload<f32x4>(p, idx * 4);
+            r.b = gload<f32x4>(p, idx * 4 + 16);
+        }
+        unpack8<BF16>(r, v);
         return;
     }
 #pragma unroll
@@ -102,24 +191,57 @@ __device__ __forceinline__ void load8_tail(const void *p, int64_t idx, int64_t n
         v[e] = 0.0f;
         if (idx + e < n) {
             if constexpr (BF16)
-                v[e] = bf16_lo(static_cast<const uint16_t *>(p)[idx + e]);
+                v[e] = bf16_lo(gload<uint16_t>(p, (idx + e) * 2));
             else
-                v[e] = static_cast<const float *>(p)[idx + e];
+                v[e] = gload<float>(p, (idx + e) * 4);
         }
     }
 }
 
-template <typename T>
-__device__ __forceinline__ void store_tail(T *p, int64_t idx, int64_t n, const T v[8])
+template <bool WHOLE>
+__device__ __forceinline__ void store_eight(void *p, int64_t idx, int64_t n, const float v[8])
 {
+    if (WHOLE || idx + 8 <= n) {
+        gstore(p, idx * 4, f32x4{v[0], v[1], v[2], v[3]});
+        gstore(p, idx * 4 + 16, f32x4{v[4], v[5], v[6], v[7]});
+        return;
+    }
 #pragma unroll
     for (int e = 0; e < 8; e++)
         if (idx + e < n)
-            p[idx + e] = v[e];
+            gstore(p, (idx + e) * 4, v[e]);
 }
 
-template <bool PB, bool GB, bool S8>
-__device__ void step_chunk(const StepArgs &a, const TensorEntry &t, int64_t c0)
+// Eight one-byte codes.
+template <bool WHOLE>
+__device__ __forceinline__ i32x2 load_codes(const void *p, int64_t idx, int64_t n)
+{
+    if (WHOLE || idx + 8 <= n)
+        return gload<i32x2>(p, idx);
+    i32x2 w = {0, 0};
+#pragma unroll
+    for (int e = 0; e < 8; e++)
+        if (idx + e < n)
+            w[e / 4] |= gload<uint8_t>(p, idx + e) << (8 * (e % 4));
+    return w;
+}
+
+template <bool WHOLE>
+__device__ __forceinline__ void store_codes(void *p, int64_t idx, int64_t n, i32x2 w)
+{
+    if (WHOLE || idx + 8 <= n) {
+        gstore(p, idx, w);
+        return;
+    }
+#pragma unroll
+    for (int e = 0; e < 8; e++)
+        if (idx + e < n)
+            gstore(p, idx + e, (uint8_t)((uint32_t)w[e / 4] >> (8 * (e % 4))));
+}
+
+// WHOLE: the chunk ends before the tensor does, so nothing is checked.
+template <bool PB, bool GB, bool S8, bool WHOLE>
+__device__ __forceinline__ void step_chunk(const StepArgs &a, const TensorEntry &t, int64_t c0)
 {
     constexpr int kRuns = 2;            // of eight elements per lane
     const int64_t n = t.numel;
@@ -127,57 +249,59 @@ __device__ void step_chunk(const StepArgs &a, const TensorEntry &t, int64_t c0)
     // Lane l of 16 holds elements 8 l .. 8 l + 7 and 128 + 8 l .. of its block.
     const int64_t at = c0 + (threadIdx.x / 16) * kStateBlock + (threadIdx.x % 16) * 8;
     const int64_t blk = at / kStateBlock;
-    if (at >= n && !S8)
+    const bool live = WHOLE || blk * kStateBlock < n;
+    if (!live)                          // (all 16 lanes of a block agree)
         return;
     float p[kRuns][8], g[kRuns][8], m[kRuns][8], v[kRuns][8];
+    i32x2 wm[kRuns], wv[kRuns];
     float sm = 0.0f, sv = 0.0f;
-    if (S8 && blk * kStateBlock < n) {
-        sm = t.ms[blk];
-        sv = t.vs[blk];
+    if constexpr (S8) {
+        sm = gload<float>(t.ms, blk * 4);
+        sv = gload<float>(t.vs, blk * 4);
     }
 #pragma unroll
     for (int k = 0; k < kRuns; k++) {
         const int64_t i = at + 128 * k;
-        load8_tail<PB>(t.p, i, n, p[k]);
-        load8_tail<GB>(t.g, i, n, g[k]);
+        load_eight<PB, WHOLE>(t.p, i, n, p[k]);
+        load_eight<GB, WHOLE>(t.g, i, n, g[k]);
         if constexpr (S8) {
-            i32x2 wm = {0, 0}, wv = {0, 0};
-            if (i + 8 <= n) {
-                wm = *reinterpret_cast<const i32x2 *>(static_cast<const uint8_t *>(t.m) + i);
-                wv = *reinterpret_cast<const i32x2 *>(static_cast<const uint8_t *>(t.v) + i);
-            } else {
-#pragma unroll
-                for (int e = 0; e < 8; e++)
-                    if (i + e < n) {
-                        wm[e / 4] |= static_cast<const uint8_t *>(t.m)[i + e] << (8 * (e % 4));
-                        wv[e / 4] |= static_cast<const uint8_t *>(t.v)[i + e] << (8 * (e % 4));
-                    }
-            }
-            unpack_e4m3x8(wm, m[k]);
-            unpack_e4m3x8(wv, v[k]);
+            wm[k] = load_codes<WHOLE>(t.m, i, n);
+            wv[k] = load_codes<WHOLE>(t.v, i, n);
         } else {
-            load8_tail<false>(t.m, i, n, m[k]);
-            load8_tail<false>(t.v, i, n, v[k]);
+            load_eight<false, WHOLE>(t.m, i, n, m[k]);
+            load_eight<false, WHOLE>(t.v, i, n, v[k]);
         }
     }
     float am = 0.0f, av = 0.0f;
 #pragma unroll
     for (int k = 0; k < kRuns; k++) {
+        if constexpr (S8) {
+            unpack_e4m3x8(wm[k], m[k]);
+            unpack_e4m3x8(wv[k], v[k]);
+#pragma unroll
+            for (int e = 0; e < 8; e++) {
+                m[k][e] = m[k][e] * sm;
+                v[k][e] = v[k][e] * sv;
+                v[k][e] = v[k][e] * v[k][e];
+            }
+        }
+        float r[8];
 #pragma unroll
         for (int e = 0; e < 8; e++) {
-            if constexpr (S8) {
-                m[k][e] = m[k][e] * sm;
-                const float r = v[k][e] * sv;
-                v[k][e] = r * r;
-            }
             m[k][e] = a.b1 * m[k][e] + a.a1 * g[k][e];
             v[k][e] = a.b2 * v[k][e] + (a.a2 * g[k][e]) * g[k][e];
-            const float r = __builtin_sqrtf(v[k][e]);
-            p[k][e] = p[k][e] * decay - a.c1 * (m[k][e] / __builtin_fmaf(r, a.c2, a.eps));
+        }
+        roots<8>(v[k], r);
+#pragma unroll
+        for (int e = 0; e < 8; e++) {
+            // (The quotient within about two ulps: it moves p by a part in 2^22
+            // of the step.)
+            p[k][e] = p[k][e] * decay -
+                      a.c1 * (m[k][e] * __builtin_amdgcn_rcpf(__builtin_fmaf(r[e], a.c2, a.eps)));
             if constexpr (S8) {
-                v[k][e] = r;
+                v[k][e] = r[e];
                 am = max_nan(am, __builtin_fabsf(m[k][e]));
-                av = max_nan(av, r);
+                av = max_nan(av, r[e]);
             }
         }
     }
@@ -190,74 +314,59 @@ __device__ void step_chunk(const StepArgs &a, const TensorEntry &t, int64_t c0)
         const bool zm = am < kTinyBlock, zv = av < kTinyBlock;
         im = zm ? 0.0f : (1.0f / am) * kE4m3Max;
         iv = zv ? 0.0f : (1.0f / av) * kE4m3Max;
-        if (threadIdx.x % 16 == 0 && blk * kStateBlock < n) {
-            t.ms[blk] = zm ? 0.0f : am * (1.0f / kE4m3Max);
-            t.vs[blk] = zv ? 0.0f : av * (1.0f / kE4m3Max);
+        if (threadIdx.x % 16 == 0) {
+            gstore(t.ms, blk * 4, zm ? 0.0f : am * (1.0f / kE4m3Max));
+            gstore(t.vs, blk * 4, zv ? 0.0f : av * (1.0f / kE4m3Max));
         }
     }
 #pragma unroll
     for (int k = 0; k < kRuns; k++) {
         const int64_t i = at + 128 * k;
-        if (i >= n)
+        if (!WHOLE && i >= n)
             continue;
-        const bool whole = i + 8 <= n;
         const uint64_t u = (uint64_t)(t.index0 + i) >> 3;
         if constexpr (PB) {
-            uint32_t r[8];
-            uniforms8(a, u, 0x80000000u, r);
-            uint16_t o[8];
-#pragma unroll
-            for (int e = 0; e < 8; e++) {
-                const uint32_t b = __float_as_uint(p[k][e]);
-                // (Adding to an infinity's or a NaN's bits would change which it is.)
-                const bool finite = (b & 0x7F800000u) != 0x7F800000u;
-                o[e] = (uint16_t)((finite ? b + r[e] : b) >> 16);
-            }
-            uint16_t *dst = static_cast<uint16_t *>(t.p);
-            if (whole) {
-                i32x4 w;
-#pragma unroll
-                for (int e = 0; e < 4; e++)
-                    w[e] = (int)(o[2 * e] | (uint32_t)o[2 * e + 1] << 16);
-                *reinterpret_cast<i32x4 *>(dst + i) = w;
-            } else {
-                store_tail(dst, i, n, o);
-            }
-        } else if (whole) {
-            store8(static_cast<float *>(t.p), i, p[k]);
-        } else {
-            store_tail(static_cast<float *>(t.p), i, n, p[k]);
-        }
-        if constexpr (S8) {
-            uint32_t r[8];
-            uniforms8(a, u, 0u, r);
-#pragma unroll
-            for (int e = 0; e < 8; e++) {
-                // (A block with a NaN has a NaN scale; its codes do not matter.)
-                m[k][e] = fminf(fmaxf(m[k][e] * im, -kE4m3Max), kE4m3Max);
-                v[k][e] = stochastic_e4m3(fminf(v[k][e] * iv, kE4m3Max), r[e]);
-            }
-            const i32x2 wm = pack_e4m3x8(m[k]), wv = pack_e4m3x8(v[k]);
-            uint8_t *dm = static_cast<uint8_t *>(t.m), *dv = static_cast<uint8_t *>(t.v);
-            if (whole) {
-                *reinterpret_cast<i32x2 *>(dm + i) = wm;
-                *reinterpret_cast<i32x2 *>(dv + i) = wv;
+            uint32_t x[4];
+            uniforms8(a, u, 0x80000000u, x);
+            const i32x4 w = stochastic_bf16x8(p[k], x);
+            if (WHOLE || i + 8 <= n) {
+                gstore(t.p, i * 2, w);
             } else {
 #pragma unroll
                 for (int e = 0; e < 8; e++)
-                    if (i + e < n) {
-                        dm[i + e] = (uint8_t)((uint32_t)wm[e / 4] >> (8 * (e % 4)));
-                        dv[i + e] = (uint8_t)((uint32_t)wv[e / 4] >> (8 * (e % 4)));
-                    }
+                    if (i + e < n)
+                        gstore(t.p, (i + e) * 2, (uint16_t)((uint32_t)w[e / 2] >> (16 * (e % 2))));
             }
-        } else if (whole) {
-            store8(static_cast<float *>(t.m), i, m[k]);
-            store8(static_cast<float *>(t.v), i, v[k]);
         } else {
-            store_tail(static_cast<float *>(t.m), i, n, m[k]);
-            store_tail(static_cast<float *>(t.v), i, n, v[k]);
+            store_eight<WHOLE>(t.p, i, n, p[k]);
+        }
+        if constexpr (S8) {
+            // (The largest value's product with 448 / a may exceed 448 by a few
+            // ulps; both conversions still give 448.  A block with a NaN has a
+            // NaN scale, and its codes do not matter.)
+            uint32_t x[4];
+            uniforms8(a, u, 0u, x);
+#pragma unroll
+            for (int e = 0; e < 8; e++) {
+                m[k][e] = m[k][e] * im;
+                v[k][e] = v[k][e] * iv;
+            }
+            store_codes<WHOLE>(t.m, i, n, pack_e4m3x8(m[k]));
+            store_codes<WHOLE>(t.v, i, n, stochastic_e4m3x8(v[k], x));
+        } else {
+            store_eight<WHOLE>(t.m, i, n, m[k]);
+            store_eight<WHOLE>(t.v, i, n, v[k]);
         }
     }
+}
+
+template <bool PB, bool GB, bool S8>
+__device__ __forceinline__ void step_either(const StepArgs &a, const TensorEntry &t, int64_t c0)
+{
+    if (c0 + kTensorChunk <= t.numel)
+        step_chunk<PB, GB, S8, true>(a, t, c0);
+    else
+        step_chunk<PB, GB, S8, false>(a, t, c0);
 }
 
 __global__ __launch_bounds__(256) void adamw_tensors_kernel(StepArgs a)
@@ -265,14 +374,14 @@ __global__ __launch_bounds__(256) void adamw_tensors_kernel(StepArgs a)
     const TensorEntry t = a.tensors[a.chunk_tensor[blockIdx.x]];
     const int64_t c0 = ((int64_t)blockIdx.x - t.chunk0) * kTensorChunk;
     switch (t.flags) {
-    case 0: return step_chunk<false, false, false>(a, t, c0);
-    case 1: return step_chunk<true, false, false>(a, t, c0);
-    case 2: return step_chunk<false, true, false>(a, t, c0);
-    case 3: return step_chunk<true, true, false>(a, t, c0);
-    case 4: return step_chunk<false, false, true>(a, t, c0);
-    case 5: return step_chunk<true, false, true>(a, t, c0);
-    case 6: return step_chunk<false, true, true>(a, t, c0);
-    default: return step_chunk<true, true, true>(a, t, c0);
+    case 0: return step_either<false, false, false>(a, t, c0);
+    case 1: return step_either<true, false, false>(a, t, c0);
+    case 2: return step_either<false, true, false>(a, t, c0);
+    case 3: return step_either<true, true, false>(a, t, c0);
+    case 4: return step_either<false, false, true>(a, t, c0);
+    case 5: return step_either<true, false, true>(a, t, c0);
+    case 6: return step_either<false, true, true>(a, t, c0);
+    default: return step_either<true, true, true>(a, t, c0);
     }
 }
 
