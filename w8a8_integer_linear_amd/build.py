@@ -15,8 +15,8 @@ CSRC = os.path.join(HERE, "csrc")
 ROOT = os.path.dirname(HERE)
 LIB = os.path.join(HERE, "libqlin.so")
 BUILD_DIR = os.path.join(ROOT, "_build")
-SOURCES = ["api.hip", "api_around.hip", "quant.hip", "gemm.hip", "sgd.hip", "norm.hip", "adapter.hip",
-           "adamw.hip", "stream.hip", "mfma_ceiling.hip"]
+SOURCES = ["api.hip", "api_around.hip", "quant.hip", "gemm.hip", "gemm_adapter.hip", "sgd.hip",
+           "norm.hip", "adapter.hip", "adamw.hip", "stream.hip", "mfma_ceiling.hip"]
 
 ARCH = "gfx950"
 FLAGS = [

@@ -17,6 +17,7 @@
 // far from the 64-bit result as fp32 products are.)  Every lane of an accumulator belongs to one token, so the rows of a
 // 16-token block that have another adapter are dropped by a select and never
 // meet its matrices' values (a NaN in one adapter stays with its tokens).
+#include "adapter_frag.hpp"
 #include "common.hpp"
 #include "launch.hpp"
 #include "lowp.hpp"
@@ -24,105 +25,6 @@
 namespace qlin {
 
 namespace {
-
-typedef uint16_t u16x8 __attribute__((ext_vector_type(8)));
-
-enum { X_I8 = 0, X_BF16 = 1, X_F32 = 2 };
-
-// An MFMA operand: eight contraction values per lane, as one or three bf16
-// terms, each the rounded rest that the ones before it leave.
-template <int TERMS> struct Frag {
-    bf16x8 t[TERMS];
-};
-
-__device__ __forceinline__ bf16x8 zero8() { return __builtin_bit_cast(bf16x8, i32x4{0, 0, 0, 0}); }
-
-__device__ __forceinline__ bf16x8 round8(const float v[8])
-{
-    return __builtin_bit_cast(bf16x8, pack_bf16x8(v));
-}
-
-__device__ __forceinline__ Frag<3> split8(const float v[8])
-{
-    Frag<3> f;
-    float rest[8];
-#pragma unroll
-    for (int e = 0; e < 8; e++)
-        rest[e] = v[e];
-#pragma unroll
-    for (int q = 0; q < 3; q++) {
-        f.t[q] = round8(rest);
-        if (q < 2) {
-            float t[8];
-            unpack8<true>(Raw8<true>{__builtin_bit_cast(i32x4, f.t[q])}, t);
-#pragma unroll
-            for (int e = 0; e < 8; e++)
-                rest[e] = rest[e] - t[e];
-        }
-    }
-    return f;
-}
-
-constexpr int terms_of(int x) { return x == X_F32 ? 3 : 1; }
-
-// Eight consecutive elements from index idx (a multiple of 8); zeros unless ok.
-template <int X>
-__device__ __forceinline__ Frag<terms_of(X)> load_frag(const void *p, int64_t idx, bool ok)
-{
-    Frag<terms_of(X)> f;
-    if constexpr (X == X_BF16) {
-        f.t[0] = zero8();
-        if (ok)
-            f.t[0] = *reinterpret_cast<const bf16x8 *>(static_cast<const uint16_t *>(p) + idx);
-        return f;
-    } else if constexpr (X == X_I8) {
-        i32x2 w = {0, 0};
-        if (ok)
-            w = *reinterpret_cast<const i32x2 *>(static_cast<const int8_t *>(p) + idx);
-        float v[8];
-        codes_to_float(w, v);
-        f.t[0] = round8(v);
-        return f;
-    } else {
-        float v[8] = {0, 0, 0, 0, 0, 0, 0, 0};
-        if (ok)
-            load8<false>(p, idx, v);
-        return split8(v);
-    }
-}
-
-// acc += a b over the terms, the smallest first; of nine partial products of
-// two split operands, the three below 2^-24 are left out.
-template <int TA, int TB>
-__device__ __forceinline__ f32x4 mfma(const Frag<TA> &a, const Frag<TB> &b, f32x4 acc)
-{
-#pragma unroll
-    for (int d = 2; d >= 0; d--)
-#pragma unroll
-        for (int i = 0; i < TA; i++)
-            if (d - i >= 0 && d - i < TB)
-                acc = __builtin_amdgcn_mfma_f32_16x16x32_bf16(a.t[i], b.t[d - i], acc, 0, 0, 0);
-    return acc;
-}
-
-// f(id, mine) for every adapter among the wave's 16 tokens (lane l holds token
-// l % 16's id, or -1); mine: whether this lane's token has it.
-template <typename F> __device__ __forceinline__ void for_adapters(int id, F f)
-{
-    uint64_t left = __ballot(id >= 0);
-    while (left) {
-        const int cur = __builtin_amdgcn_readlane(id, (int)__builtin_ctzll(left));
-        const bool mine = id == cur;
-        f(cur, mine);
-        left &= ~__ballot(mine);
-    }
-}
-
-__device__ __forceinline__ int id_of(const int32_t *ids, int64_t m, int64_t M, int L)
-{
-    const int id = m < M ? ids[m] : -1;
-    return id >= 0 && id < L ? id : -1;
-}
 
 // ------------------------------------------------------------------ shrink
 
@@ -205,66 +107,6 @@ template <int X, bool WB> void run_shrink(const ShrinkArgs &a, hipStream_t st)
         hipLaunchKernelGGL((adapter_shrink_kernel<X, WB, 4>), grid, block, lds, st, a);
     else
         hipLaunchKernelGGL((adapter_shrink_kernel<X, WB, 8>), grid, block, lds, st, a);
-}
-
-// ------------------------------------------------------------------ expand
-
-struct ExpandArgs {
-    const float *p;         // [M, R]
-    const void *q;          // [L, C, R]
-    const int32_t *ids;
-    int64_t M, C;
-    int L, R;
-    float *out;             // [M, C], added to
-};
-
-// out[m, c] += sum_r p[m, r] q[id, c, r]: 16 tokens and 256 columns per
-// workgroup, 64 columns per wave.
-template <bool WB> __global__ __launch_bounds__(256) void adapter_expand_kernel(ExpandArgs a)
-{
-    constexpr int W = WB ? X_BF16 : X_F32;
-    const int lane = __lane_id(), w = threadIdx.x / kWave;
-    const int64_t m = (int64_t)blockIdx.y * 16 + lane % 16;
-    const int64_t c0 = (int64_t)blockIdx.x * 256 + w * 64;
-    const int64_t mc = m < a.M ? m : a.M - 1;
-    const int id = id_of(a.ids, m, a.M, a.L);
-    f32x4 acc[4] = {};
-    for_adapters(id, [&](int cur, bool mine) {
-        f32x4 t[4] = {};
-        for (int r0 = 0; r0 < a.R; r0 += 32) {
-            const int r = r0 + 8 * (lane / 16);
-            const bool ok = r < a.R;
-            const auto pf = load_frag<X_F32>(a.p, mc * a.R + r, ok);
-#pragma unroll
-            for (int b = 0; b < 4; b++) {
-                const int64_t c = c0 + 16 * b + lane % 16;
-                const auto qf = load_frag<W>(a.q, ((int64_t)cur * a.C + c) * a.R + r, ok && c < a.C);
-                t[b] = mfma(qf, pf, t[b]);
-            }
-        }
-#pragma unroll
-        for (int b = 0; b < 4; b++)
-            acc[b] = mine ? t[b] : acc[b];
-    });
-    if (id < 0)
-        return;
-#pragma unroll
-    for (int b = 0; b < 4; b++) {
-        const int64_t c = c0 + 16 * b + 4 * (lane / 16);
-        if (c < a.C) {
-            f32x4 *o = reinterpret_cast<f32x4 *>(a.out + m * a.C + c);
-            *o = *o + acc[b];
-        }
-    }
-}
-
-void run_expand(const ExpandArgs &a, bool wbf, hipStream_t st)
-{
-    const dim3 grid((unsigned)((a.C + 255) / 256), (unsigned)((a.M + 15) / 16));
-    if (wbf)
-        hipLaunchKernelGGL(adapter_expand_kernel<true>, grid, dim3(256), 0, st, a);
-    else
-        hipLaunchKernelGGL(adapter_expand_kernel<false>, grid, dim3(256), 0, st, a);
 }
 
 // --------------------------------------------------------------- transpose
@@ -552,12 +394,11 @@ __global__ __launch_bounds__(256) void adapter_sum_kernel(const float *__restric
 
 } // namespace
 
-void launch_adapter_fwd(const AdapterArgs &g, const int8_t *qx, const float *sx, float *u, float *y,
-                        hipStream_t st)
+void launch_adapter_u(const AdapterArgs &g, const int8_t *qx, const float *sx, float *u,
+                      hipStream_t st)
 {
     const ShrinkArgs s{qx, sx, g.a, g.scale, g.ids, g.M, g.K, g.L, g.R, u};
     g.bf16 ? run_shrink<X_I8, true>(s, st) : run_shrink<X_I8, false>(s, st);
-    run_expand(ExpandArgs{u, g.b, g.ids, g.M, g.N, g.L, g.R, y}, g.bf16, st);
 }
 
 void launch_adapter_group(const int32_t *ids, int64_t M, int L, int32_t *order, int32_t *start,
@@ -595,7 +436,8 @@ size_t adapter_bwd_bytes(int64_t M, int64_t N, int64_t K, int64_t L, int64_t R)
     return bwd_layout(M, N, K, L, R).end;
 }
 
-void launch_adapter_bwd_v(const AdapterArgs &g, const void *dy, bool dy_bf16, void *ws, hipStream_t st)
+AdapterEpilogue launch_adapter_bwd_v(const AdapterArgs &g, const void *dy, bool dy_bf16, void *ws,
+                                     hipStream_t st)
 {
     char *w = static_cast<char *>(ws);
     const BwdLayout o = bwd_layout(g.M, g.N, g.K, g.L, g.R);
@@ -607,15 +449,7 @@ void launch_adapter_bwd_v(const AdapterArgs &g, const void *dy, bool dy_bf16, vo
         g.bf16 ? run_shrink<X_BF16, true>(s, st) : run_shrink<X_BF16, false>(s, st);
     else
         g.bf16 ? run_shrink<X_F32, true>(s, st) : run_shrink<X_F32, false>(s, st);
-}
-
-void launch_adapter_bwd_dx(const AdapterArgs &g, float *dx, void *ws, hipStream_t st)
-{
-    char *w = static_cast<char *>(ws);
-    const BwdLayout o = bwd_layout(g.M, g.N, g.K, g.L, g.R);
-    run_expand(ExpandArgs{reinterpret_cast<const float *>(w + o.v), w + o.at, g.ids, g.M, g.K, g.L, g.R,
-                          dx},
-               g.bf16, st);
+    return AdapterEpilogue{s.out, w + o.at, g.ids, g.L, g.R, g.bf16};
 }
 
 void launch_adapter_bwd_w(const AdapterArgs &g, const void *dy, bool dy_bf16, const int8_t *qx,

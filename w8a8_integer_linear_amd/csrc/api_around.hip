@@ -174,8 +174,8 @@ int qlin_adapter_fwd(const int8_t *qx, const float *sx, const int8_t *qw, const 
     if (need)
         p.split_ws = workspace;
     const qlin::AdapterArgs g{a, b, w_dtype == QLIN_BF16, scale, ids, M, N, K, (int)L, (int)R};
-    qlin::launch_product(p, s);
-    qlin::launch_adapter_fwd(g, qx, sx, u, y, s);
+    qlin::launch_adapter_u(g, qx, sx, u, s);
+    qlin::launch_product_adapter(p, {u, b, ids, (int)L, (int)R, g.bf16}, s);
     return finish();
 }
 
@@ -242,14 +242,16 @@ int qlin_adapter_bwd(const void *dy, int dy_dtype, const int8_t *qg1, const floa
     void *aw = static_cast<char *>(workspace) + round256(pw);
     const qlin::AdapterArgs g{a, b, w_dtype == QLIN_BF16, scale, ids, M, N, K, (int)L, (int)R};
     if (any) {
-        qlin::launch_adapter_bwd_v(g, dy, dy_dtype == QLIN_BF16, aw, s);
+        const qlin::AdapterEpilogue va =
+            qlin::launch_adapter_bwd_v(g, dy, dy_dtype == QLIN_BF16, aw, s);
         if (dx) {
             qlin::ProductArgs p{QLIN_OP_DX, qg1, qw, M, N, K, sg1, nullptr, nullptr, dx, false};
             if (pw)
                 p.split_ws = workspace;
-            qlin::launch_product(p, s);
-            qlin::launch_adapter_bwd_dx(g, dx, aw, s);
-            if (had_block)
+            p.had = had_block;
+            p.had_scale = had_block ? hadamard_scale(had_block) : 1.0f;
+            qlin::launch_product_adapter(p, va, s);
+            if (had_block > 128)
                 qlin::launch_hadamard(dx, false, M, K, had_block, hadamard_scale(had_block), dx, s);
         }
     }

@@ -52,6 +52,19 @@ struct ProductArgs {
 
 void launch_product(const ProductArgs &p, hipStream_t st);
 
+// The low-rank term of a product's output row i: sum_r p[i, r] q[ids[i], j, r]
+// with p [rows, R] fp32 and q [L, cols, R] fp32 or bf16.
+struct AdapterEpilogue {
+    const float *p;
+    const void *q;
+    const int32_t *ids;
+    int L, R;
+    bool bf16;
+};
+// A forward or dX product (no workspace mode, contraction within the int32
+// bound) with that term added.
+void launch_product_adapter(const ProductArgs &p, const AdapterEpilogue &ad, hipStream_t st);
+
 // Whether the product kernels can address every operand byte of this shape
 // with their 32-bit buffer offsets (for contractions past the int32 bound,
 // those of one chunk's launch).
@@ -135,17 +148,17 @@ struct AdapterArgs {
     int64_t M, N, K;
     int L, R;
 };
-// u = scale x^ A^T, then y += u B^T.
-void launch_adapter_fwd(const AdapterArgs &g, const int8_t *qx, const float *sx, float *u, float *y,
-                        hipStream_t st);
+// u = scale x^ A^T.
+void launch_adapter_u(const AdapterArgs &g, const int8_t *qx, const float *sx, float *u,
+                      hipStream_t st);
 void launch_adapter_group(const int32_t *ids, int64_t M, int L, int32_t *order, int32_t *start,
                           hipStream_t st);
 // Backward, with a workspace of adapter_bwd_bytes: v = scale dY B (kept in
-// the workspace), dx += v A, then both adapter gradients.
+// the workspace; the result says where it and A's transpose lie, for the dX
+// product), then both adapter gradients.
 size_t adapter_bwd_bytes(int64_t M, int64_t N, int64_t K, int64_t L, int64_t R);
-void launch_adapter_bwd_v(const AdapterArgs &g, const void *dy, bool dy_bf16, void *ws,
-                          hipStream_t st);
-void launch_adapter_bwd_dx(const AdapterArgs &g, float *dx, void *ws, hipStream_t st);
+AdapterEpilogue launch_adapter_bwd_v(const AdapterArgs &g, const void *dy, bool dy_bf16, void *ws,
+                                     hipStream_t st);
 void launch_adapter_bwd_w(const AdapterArgs &g, const void *dy, bool dy_bf16, const int8_t *qx,
                           const float *sx, const float *u, const int32_t *order,
                           const int32_t *start, float *da, float *db, void *ws, hipStream_t st);
