@@ -241,21 +241,19 @@ int qlin_adapter_bwd(const void *dy, int dy_dtype, const int8_t *qg1, const floa
     const size_t pw = qlin_product_ws_bytes(QLIN_OP_DX, M, N, K);
     void *aw = static_cast<char *>(workspace) + round256(pw);
     const qlin::AdapterArgs g{a, b, w_dtype == QLIN_BF16, scale, ids, M, N, K, (int)L, (int)R};
-    if (any) {
-        const qlin::AdapterEpilogue va =
-            qlin::launch_adapter_bwd_v(g, dy, dy_dtype == QLIN_BF16, aw, s);
-        if (dx) {
-            qlin::ProductArgs p{QLIN_OP_DX, qg1, qw, M, N, K, sg1, nullptr, nullptr, dx, false};
-            if (pw)
-                p.split_ws = workspace;
-            p.had = had_block;
-            p.had_scale = had_block ? hadamard_scale(had_block) : 1.0f;
-            qlin::launch_product_adapter(p, va, s);
-            if (had_block > 128)
-                qlin::launch_hadamard(dx, false, M, K, had_block, hadamard_scale(had_block), dx, s);
-        }
+    const qlin::AdapterEpilogue va =
+        qlin::launch_adapter_bwd_v(g, dy, dy_dtype == QLIN_BF16, start, aw, s);
+    if (any && dx) {
+        qlin::ProductArgs p{QLIN_OP_DX, qg1, qw, M, N, K, sg1, nullptr, nullptr, dx, false};
+        if (pw)
+            p.split_ws = workspace;
+        p.had = had_block;
+        p.had_scale = had_block ? hadamard_scale(had_block) : 1.0f;
+        qlin::launch_product_adapter(p, va, s);
+        if (had_block > 128)
+            qlin::launch_hadamard(dx, false, M, K, had_block, hadamard_scale(had_block), dx, s);
     }
-    qlin::launch_adapter_bwd_w(g, dy, dy_dtype == QLIN_BF16, qx, sx, u, order, start, da, db, aw, s);
+    qlin::launch_adapter_bwd_w(g, dy, dy_dtype == QLIN_BF16, qx, sx, u, order, da, db, aw, s);
     return finish();
 }
 

@@ -157,10 +157,10 @@ void launch_adapter_group(const int32_t *ids, int64_t M, int L, int32_t *order, 
 // the workspace; the result says where it and A's transpose lie, for the dX
 // product), then both adapter gradients.
 size_t adapter_bwd_bytes(int64_t M, int64_t N, int64_t K, int64_t L, int64_t R);
-AdapterEpilogue launch_adapter_bwd_v(const AdapterArgs &g, const void *dy, bool dy_bf16, void *ws,
-                                     hipStream_t st);
+AdapterEpilogue launch_adapter_bwd_v(const AdapterArgs &g, const void *dy, bool dy_bf16,
+                                     const int32_t *start, void *ws, hipStream_t st);
 void launch_adapter_bwd_w(const AdapterArgs &g, const void *dy, bool dy_bf16, const int8_t *qx,
-                          const float *sx, const float *u, const int32_t *order,
-                          const int32_t *start, float *da, float *db, void *ws, hipStream_t st);
+                          const float *sx, const float *u, const int32_t *order, float *da,
+                          float *db, void *ws, hipStream_t st);
 
 } // namespace qlin
