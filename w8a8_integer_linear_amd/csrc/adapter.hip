@@ -39,178 +39,229 @@ struct ShrinkArgs {
     int64_t M, C;
     int L, R;
     float *out;             // [M, R]
+    uint16_t *terms;        // out as bf16 terms for a q of form qt
+    int qt;
 };
 
-// Sixteen consecutive elements, as they lie in memory: the unit of this
-// kernel's loads.
-template <int X> struct Raw16 {
-    static constexpr int kWords = X == X_I8 ? 1 : X == X_BF16 ? 2 : 4;
-    i32x4 w[kWords];
+// Four values of a row of out, from rank r.
+__device__ __forceinline__ void put_out(const ShrinkArgs &a, int64_t m, int r, f32x4 v)
+{
+    *reinterpret_cast<f32x4 *>(a.out + m * a.R + r) = v;
+    const float f[4] = {v[0], v[1], v[2], v[3]};
+    put_terms<4>(a.terms, a.qt, a.R, m, r, f);
+}
+
+// W of a shrink product: X_BF16 or X_F32, [L, R, C], or three bf16 terms, one
+// plane [L, R, C] after another.
+enum { W_TERMS = 3 };
+constexpr int terms_of_w(int w) { return w == X_BF16 ? 1 : 3; }
+
+// A 16-token operand's bytes in LDS: rows of kRowBytes, whose 16-byte chunk c
+// lies at position c ^ (row & 7), so that the 16 rows that a fragment read
+// takes together fall on all banks.  Rows come straight from global memory by
+// buffer loads, 1 KiB per wave instruction: chunk for chunk in memory order but
+// for that exchange, which stays within 128 bytes.
+typedef __attribute__((address_space(3))) int8_t lds_byte;
+
+template <int ROW_BYTES> struct RowTile {
+    static constexpr int kRowBytes = ROW_BYTES, kChunks = ROW_BYTES / 16;
+
+    // Instruction n (of rows * ROW_BYTES / 1024): the lane's row and byte.
+    __device__ static __forceinline__ void slot(int n, int &row, int &byte)
+    {
+        const int s = n * 64 + __lane_id();
+        row = s / kChunks;
+        byte = 16 * ((s % kChunks) ^ (row & 7));
+    }
+    __device__ static __forceinline__ i32x4 read(const lds_byte *tile, int row, int byte)
+    {
+        typedef const __attribute__((address_space(3))) i32x4 lds_i32x4;
+        return *reinterpret_cast<lds_i32x4 *>(tile + row * ROW_BYTES + 16 * ((byte / 16) ^ (row & 7)));
+    }
+    // Eight bytes.
+    __device__ static __forceinline__ i32x2 read8(const lds_byte *tile, int row, int byte)
+    {
+        typedef const __attribute__((address_space(3))) i32x2 lds_i32x2;
+        return *reinterpret_cast<lds_i32x2 *>(tile + row * ROW_BYTES + 16 * ((byte / 16) ^ (row & 7)) +
+                                              byte % 16);
+    }
 };
 
-template <int X> __device__ __forceinline__ Raw16<X> load16(const void *p, int64_t idx, bool ok)
+constexpr uint32_t kPastEnd = 0x7FFFFFF0u;      // beyond every buffer below: reads zeros
+
+__device__ __forceinline__ __amdgpu_buffer_rsrc_t buffer_of(const void *p)
+{
+    return __builtin_amdgcn_make_buffer_rsrc(const_cast<void *>(p), (short)0, (int)kPastEnd, kRsrcWord3);
+}
+
+// out[m, r] = scale xs[m] sum_c x[m, c] w[id, r, c] for 32 tokens and RB blocks of
+// 16 ranks per workgroup.  512 bytes of every token's row and w's values for
+// them are brought into LDS at a time, STAGES - 1 such stages ahead; of a
+// stage's steps of 32 contraction indexes each of four waves per token block
+// takes a quarter, and their sums are added at the end.  What bounds it is the
+// read of x.  (Fragments straight from global memory took two to three times as
+// long: neighbouring lanes hold different rows, and each was a cache access of
+// its own.)
+template <int X, int W, int RB, int STAGES>
+__global__ __launch_bounds__(512) void adapter_shrink_kernel(ShrinkArgs a)
 {
     constexpr int kSize = X == X_I8 ? 1 : X == X_BF16 ? 2 : 4;
-    Raw16<X> r;
+    constexpr int kStep = 512 / kSize;                  // contraction indexes of a stage
+    constexpr int kPlanes = W == W_TERMS ? 3 : 1, kWSize = W == X_F32 ? 4 : 2;
+    using XTile = RowTile<512>;
+    using WTile = RowTile<kStep * kWSize>;
+    constexpr int kXBytes = 32 * 512, kWBytes = 16 * RB * kPlanes * WTile::kRowBytes;
+    constexpr int kStageBytes = kXBytes + kWBytes;
+    constexpr int kXLoads = kXBytes / 1024 / 8, kWLoads = (kWBytes / 1024 + 7) / 8;
+    constexpr int kLoads = kXLoads + kWLoads;           // per wave and stage
+    static_assert(RB * 8 * kWave * 16 <= STAGES * kStageBytes, "the sums reuse the stages");
+    __shared__ __attribute__((aligned(1024))) int8_t smem[STAGES * kStageBytes];
+    const int lane = __lane_id(), w = __builtin_amdgcn_readfirstlane((int)(threadIdx.x / kWave));
+    const int tb = w % 2, quarter = w / 2, rb0 = blockIdx.y * RB * 16;
+    const int64_t m0 = (int64_t)blockIdx.x * 32;
+    const int64_t plane = (int64_t)a.L * a.R * a.C * 2;
+    const int row_bytes = (int)(a.C * kSize);
+    const __amdgpu_buffer_rsrc_t xr = buffer_of(static_cast<const int8_t *>(a.x) + m0 * row_bytes);
+    // The adapters of both token blocks (every wave goes through them all).
+    int id[2], left[2];
 #pragma unroll
-    for (int q = 0; q < Raw16<X>::kWords; q++) {
-        r.w[q] = i32x4{0, 0, 0, 0};
-        if (ok)
-            r.w[q] = *reinterpret_cast<const i32x4 *>(static_cast<const char *>(p) + idx * kSize + 16 * q);
-    }
-    return r;
-}
-
-// Elements 8 h .. 8 h + 7 of the sixteen as an MFMA operand.
-template <int X, int H> __device__ __forceinline__ Frag<terms_of(X)> frag_of(const Raw16<X> &r)
-{
-    Frag<terms_of(X)> f;
-    if constexpr (X == X_BF16) {
-        f.t[0] = __builtin_bit_cast(bf16x8, r.w[H]);
-    } else if constexpr (X == X_I8) {
-        float v[8];
-        codes_to_float(i32x2{r.w[0][2 * H], r.w[0][2 * H + 1]}, v);
-        f.t[0] = round8(v);
-    } else {
-        float v[8];
-        unpack8<false>({__builtin_bit_cast(f32x4, r.w[2 * H]), __builtin_bit_cast(f32x4, r.w[2 * H + 1])},
-                       v);
-        f = split8(v);
-    }
-    return f;
-}
-
-template <int X> __device__ __forceinline__ void floats_of(const Raw16<X> &r, float v[16])
-{
-    if constexpr (X == X_I8) {
-        codes_to_float(i32x2{r.w[0][0], r.w[0][1]}, v);
-        codes_to_float(i32x2{r.w[0][2], r.w[0][3]}, v + 8);
-    } else if constexpr (X == X_BF16) {
-        unpack8<true>({r.w[0]}, v);
-        unpack8<true>({r.w[1]}, v + 8);
-    } else {
+    for (int t = 0; t < 2; t++)
+        left[t] = id[t] = id_of(a.ids, m0 + 16 * t + lane % 16, a.M, a.L);
+    const int mine_id = tb ? id[1] : id[0];
+    const int steps = (int)((a.C + kStep - 1) / kStep);
+    f32x4 acc[RB];
 #pragma unroll
-        for (int e = 0; e < 16; e++)
-            v[e] = __builtin_bit_cast(f32x4, r.w[e / 4])[e % 4];
-    }
-}
-
-// out[m, r] = scale xs[m] sum_c x[m, c] w[id, r, c] for TB blocks of 16 tokens
-// and RB of 16 ranks per workgroup; its waves take turns along the contraction
-// and add their sums in LDS.  What bounds it is the read of x, so the loads
-// are wide: of a chunk of 128 contraction indexes each of the four lane groups
-// takes 32 in a row, a full line per row of INT8 codes, and multiplies them in
-// four steps.  (The order inside a chunk is the same for x and w, which is all
-// the product needs.)
-template <int X, int W, int TB, int RB, int WAVES>
-__global__ __launch_bounds__(WAVES *kWave) void adapter_shrink_kernel(ShrinkArgs a)
-{
-    __shared__ f32x4 red[WAVES * kWave];
-    const int lane = __lane_id(), w = threadIdx.x / kWave;
-    const int rb0 = blockIdx.y * RB * 16;
-    int64_t m[TB], row[TB];
-    int id[TB];
-#pragma unroll
-    for (int t = 0; t < TB; t++) {
-        m[t] = ((int64_t)blockIdx.x * TB + t) * 16 + lane % 16;
-        row[t] = (m[t] < a.M ? m[t] : a.M - 1) * a.C;
-        id[t] = id_of(a.ids, m[t], a.M, a.L);
-    }
-    f32x4 acc[TB][RB];
-#pragma unroll
-    for (int t = 0; t < TB; t++)
-#pragma unroll
-        for (int b = 0; b < RB; b++)
-            acc[t][b] = f32x4{0, 0, 0, 0};
-    int left[TB];
-#pragma unroll
-    for (int t = 0; t < TB; t++)
-        left[t] = id[t];
+    for (int b = 0; b < RB; b++)
+        acc[b] = f32x4{0, 0, 0, 0};
     while (true) {
         int cur = -1;
 #pragma unroll
-        for (int t = 0; t < TB; t++) {
+        for (int t = 0; t < 2; t++) {
             const uint64_t any = __ballot(left[t] >= 0);
             if (any)
                 cur = __builtin_amdgcn_readlane(left[t], (int)__builtin_ctzll(any));
         }
         if (cur < 0)
             break;
-        const int64_t wrow = ((int64_t)cur * a.R + rb0 + lane % 16) * a.C;
-        f32x4 s[TB][RB];
+        const int8_t *wbase = static_cast<const int8_t *>(a.w) + ((int64_t)cur * a.R + rb0) * a.C * kWSize;
+        auto issue = [&](int s) {
+            lds_byte *dst = (lds_byte *)smem + (s % STAGES) * kStageBytes;
+            // (Stages past the end read zeros, so that every iteration waits
+            // for the same number of loads.)
+            const int64_t k0 = (int64_t)s * kStep;
 #pragma unroll
-        for (int t = 0; t < TB; t++)
-#pragma unroll
-            for (int b = 0; b < RB; b++)
-                s[t][b] = f32x4{0, 0, 0, 0};
-        for (int64_t k0 = (int64_t)w * 128; k0 < a.C; k0 += WAVES * 128) {
-            const int64_t k = k0 + 32 * (lane / 16);
-            Raw16<X> xr[TB][2];
-            Raw16<W> wr[RB][2];
-#pragma unroll
-            for (int h = 0; h < 2; h++) {
-                const bool ok = k + 16 * h < a.C;
-#pragma unroll
-                for (int t = 0; t < TB; t++)
-                    xr[t][h] = load16<X>(a.x, row[t] + k + 16 * h, ok);
-#pragma unroll
-                for (int b = 0; b < RB; b++)
-                    wr[b][h] = load16<W>(a.w, wrow + (int64_t)16 * b * a.C + k + 16 * h,
-                                         ok && rb0 + 16 * b + lane % 16 < a.R);
+            for (int n = 0; n < kXLoads; n++) {
+                int r, byte;
+                XTile::slot(w * kXLoads + n, r, byte);
+                const bool ok = m0 + r < a.M && k0 * kSize + byte < row_bytes;
+                const uint32_t off = ok ? (uint32_t)(r * row_bytes + byte + k0 * kSize) : kPastEnd;
+                __builtin_amdgcn_raw_ptr_buffer_load_lds(
+                    xr, (__attribute__((address_space(3))) void *)(dst + (w * kXLoads + n) * 1024), 16, off,
+                    0, 0, 0);
             }
-            auto step = [&](auto H) {
-                constexpr int h = decltype(H)::value;
-                Frag<terms_of(X)> xf[TB];
 #pragma unroll
-                for (int t = 0; t < TB; t++)
-                    xf[t] = frag_of<X, h % 2>(xr[t][h / 2]);
+            for (int n = 0; n < kWLoads; n++) {
+                const int at = w * kWLoads + n;         // KiB of the stage's w
+                constexpr int kKiB = kWBytes / 1024, kPlaneKiB = kKiB / kPlanes;
+                // (A wave without a piece of its own repeats the last one.)
+                const int piece = at < kKiB ? at : kKiB - 1, p = piece / kPlaneKiB;
+                const __amdgpu_buffer_rsrc_t wr = buffer_of(wbase + p * plane);
+                int r, byte;
+                WTile::slot(piece % kPlaneKiB, r, byte);
+                const int64_t in = k0 * kWSize + byte;
+                const bool ok = rb0 + r < a.R && in < a.C * kWSize;
+                const uint32_t off = ok ? (uint32_t)(r * a.C * kWSize + in) : kPastEnd;
+                __builtin_amdgcn_raw_ptr_buffer_load_lds(
+                    wr, (__attribute__((address_space(3))) void *)(dst + kXBytes + piece * 1024), 16, off, 0,
+                    0, 0);
+            }
+        };
+        f32x4 s[RB];
+#pragma unroll
+        for (int b = 0; b < RB; b++)
+            s[b] = f32x4{0, 0, 0, 0};
+#pragma unroll
+        for (int st = 0; st < STAGES - 1; st++)
+            issue(st);
+        for (int st = 0; st < steps; st++) {
+            issue(st + STAGES - 1);
+            asm volatile("s_waitcnt vmcnt(%0)" ::"n"(kLoads *(STAGES - 1)) : "memory");
+            asm volatile("s_barrier" ::: "memory");
+            const lds_byte *xt = (const lds_byte *)smem + (st % STAGES) * kStageBytes;
+            const lds_byte *wt = xt + kXBytes;
+            constexpr int kMine = kStep / 32 / 4;       // steps of this wave
+#pragma unroll
+            for (int q = 0; q < kMine; q++) {
+                const int k = (quarter * kMine + q) * 32 + 8 * (lane / 16), row = tb * 16 + lane % 16;
+                Frag<terms_of(X)> xf;
+                if constexpr (X == X_BF16) {
+                    xf.t[0] = __builtin_bit_cast(bf16x8, XTile::read(xt, row, 2 * k));
+                } else if constexpr (X == X_I8) {
+                    float v[8];
+                    codes_to_float(XTile::read8(xt, row, k), v);
+                    xf.t[0] = round8(v);
+                } else {
+                    float v[8];
+                    unpack8<false>({__builtin_bit_cast(f32x4, XTile::read(xt, row, 4 * k)),
+                                    __builtin_bit_cast(f32x4, XTile::read(xt, row, 4 * k + 16))},
+                                   v);
+                    xf = split8(v);
+                }
 #pragma unroll
                 for (int b = 0; b < RB; b++) {
-                    const auto wf = frag_of<W, h % 2>(wr[b][h / 2]);
+                    Frag<terms_of_w(W)> wf;
+                    const int r = 16 * b + lane % 16;
+                    if constexpr (W == X_F32) {
+                        float v[8];
+                        unpack8<false>({__builtin_bit_cast(f32x4, WTile::read(wt, r, 4 * k)),
+                                        __builtin_bit_cast(f32x4, WTile::read(wt, r, 4 * k + 16))},
+                                       v);
+                        wf = split8(v);
+                    } else {
 #pragma unroll
-                    for (int t = 0; t < TB; t++)
-                        s[t][b] = mfma(wf, xf[t], s[t][b]);
+                        for (int p = 0; p < kPlanes; p++)
+                            wf.t[p] = __builtin_bit_cast(
+                                bf16x8, WTile::read(wt + p * (kWBytes / kPlanes), r, 2 * k));
+                    }
+                    s[b] = mfma(wf, xf, s[b]);
                 }
-            };
-            step(std::integral_constant<int, 0>{});
-            step(std::integral_constant<int, 1>{});
-            step(std::integral_constant<int, 2>{});
-            step(std::integral_constant<int, 3>{});
-        }
-#pragma unroll
-        for (int t = 0; t < TB; t++) {
-            const bool mine = id[t] == cur;
-            left[t] = mine ? -1 : left[t];
-#pragma unroll
-            for (int b = 0; b < RB; b++)
-                acc[t][b] = mine ? s[t][b] : acc[t][b];
-        }
-    }
-#pragma unroll
-    for (int t = 0; t < TB; t++) {
-        const float f = id[t] >= 0 ? a.scale[id[t]] * (a.xs ? a.xs[m[t]] : 1.0f) : 0.0f;
-#pragma unroll
-        for (int b = 0; b < RB; b++) {
-            if (t + b > 0)
-                __syncthreads();
-            red[threadIdx.x] = acc[t][b];
-            __syncthreads();
-            const int r = rb0 + 16 * b + 4 * (lane / 16);
-            if (w == (t * RB + b) % WAVES && m[t] < a.M && r < a.R) {
-                f32x4 s = red[lane];
-                for (int i = 1; i < WAVES; i++)
-                    s += red[i * kWave + lane];
-                *reinterpret_cast<f32x4 *>(a.out + m[t] * a.R + r) =
-                    id[t] >= 0 ? s * f : f32x4{0, 0, 0, 0};
             }
+            // Every wave has read the stage before the next issue refills it.
+            lds_barrier();
         }
+        // (The stages past the end are still landing.)
+        asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+        asm volatile("s_barrier" ::: "memory");
+#pragma unroll
+        for (int t = 0; t < 2; t++)
+            left[t] = id[t] == cur ? -1 : left[t];
+#pragma unroll
+        for (int b = 0; b < RB; b++)
+            acc[b] = mine_id == cur ? s[b] : acc[b];
+    }
+    f32x4 *red = reinterpret_cast<f32x4 *>(smem);       // [RB][8 waves][64]
+#pragma unroll
+    for (int b = 0; b < RB; b++)
+        red[(b * 8 + w) * kWave + lane] = acc[b];
+    __syncthreads();
+    const int64_t m = m0 + 16 * tb + lane % 16;
+    const float f = mine_id >= 0 ? a.scale[mine_id] * (a.xs ? a.xs[m] : 1.0f) : 0.0f;
+    const int r = rb0 + 16 * quarter + 4 * (lane / 16);
+    if (quarter < RB && m < a.M && r < a.R) {
+        f32x4 s = red[(quarter * 8 + tb) * kWave + lane];
+#pragma unroll
+        for (int q = 1; q < 4; q++)
+            s += red[(quarter * 8 + tb + 2 * q) * kWave + lane];
+        put_out(a, m, r, mine_id >= 0 ? s * f : f32x4{0, 0, 0, 0});
     }
 }
 
+// Tokens of the weight-streaming product, which does not read the terms.
+constexpr int64_t kSkinnyTokens = 16;
+
 // The same for a few tokens: one wave per token and rank, whose read of w (the
 // ranks of one token's adapter in as many waves) is what takes the time.
-template <int X, int W>
-__global__ __launch_bounds__(256) void adapter_shrink_few_kernel(ShrinkArgs a)
+template <int W> __global__ __launch_bounds__(256) void adapter_shrink_few_kernel(ShrinkArgs a)
 {
     const int lane = __lane_id();
     const int64_t at = (int64_t)blockIdx.x * 4 + threadIdx.x / kWave;
@@ -220,47 +271,139 @@ __global__ __launch_bounds__(256) void adapter_shrink_few_kernel(ShrinkArgs a)
     float s = 0.0f;
     if (id >= 0) {
         const int64_t x0 = m * a.C, w0 = ((int64_t)id * a.R + r) * a.C;
-#pragma unroll 4
-        for (int64_t k = lane * 16; k < a.C; k += kWave * 16) {
-            const auto xr = load16<X>(a.x, x0 + k, true);
-            const auto wr = load16<W>(a.w, w0 + k, true);
-            float x[16], w[16];
-            floats_of(xr, x);
-            floats_of(wr, w);
+        // Four pieces of 1024 contraction indexes are loaded at once; those past
+        // the end read the last values and do not count.
+        constexpr int kAtOnce = 4;
+        constexpr bool kBf = W == X_BF16;
+        for (int64_t k0 = lane * 16; k0 < a.C; k0 += kAtOnce * kWave * 16) {
+            i32x4 q[kAtOnce];
+            Raw8<kBf> wr[kAtOnce][2];
 #pragma unroll
-            for (int e = 0; e < 16; e++)
-                s = __builtin_fmaf(x[e], w[e], s);
+            for (int i = 0; i < kAtOnce; i++) {
+                const int64_t k = k0 + i * kWave * 16 < a.C ? k0 + i * kWave * 16 : a.C - 16;
+                q[i] = *reinterpret_cast<const i32x4 *>(static_cast<const int8_t *>(a.x) + x0 + k);
+                wr[i][0] = load_raw8<kBf>(a.w, w0 + k);
+                wr[i][1] = load_raw8<kBf>(a.w, w0 + k + 8);
+            }
+            __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+            for (int i = 0; i < kAtOnce; i++) {
+                float x[16], w[16], t = 0.0f;
+                codes_to_float(i32x2{q[i][0], q[i][1]}, x);
+                codes_to_float(i32x2{q[i][2], q[i][3]}, x + 8);
+                unpack8<kBf>(wr[i][0], w);
+                unpack8<kBf>(wr[i][1], w + 8);
+#pragma unroll
+                for (int e = 0; e < 16; e++)
+                    t = __builtin_fmaf(x[e], w[e], t);
+                s = k0 + i * kWave * 16 < a.C ? s + t : s;
+            }
         }
     }
     s = wave_all(s, [](float p, float q) { return p + q; });
-    if (lane == 0)
-        a.out[m * a.R + r] = id >= 0 ? s * (a.scale[id] * (a.xs ? a.xs[m] : 1.0f)) : 0.0f;
+    if (lane == 0) {
+        const float v = id >= 0 ? s * (a.scale[id] * (a.xs ? a.xs[m] : 1.0f)) : 0.0f;
+        a.out[m * a.R + r] = v;
+        if (a.M > kSkinnyTokens) {
+            const float f[1] = {v};
+            put_terms<1>(a.terms, a.qt, a.R, m, r, f);
+        }
+    }
 }
 
 // Most tokens of the kernel above: it reads an adapter once per token.
 constexpr int64_t kFewTokens = 32;
 
-template <int X, int W, int TB, int RB, int WAVES> void go_shrink(const ShrinkArgs &a, hipStream_t st)
+template <int X, int W, int RB> void go_shrink(const ShrinkArgs &a, hipStream_t st)
 {
-    const dim3 grid((unsigned)((a.M + 16 * TB - 1) / (16 * TB)), (unsigned)((a.R + 16 * RB - 1) / (16 * RB)));
-    hipLaunchKernelGGL((adapter_shrink_kernel<X, W, TB, RB, WAVES>), grid, dim3(WAVES * kWave), 0, st, a);
+    constexpr int kSize = X == X_I8 ? 1 : X == X_BF16 ? 2 : 4;
+    constexpr int kStage = 32 * 512 + 16 * RB * (W == W_TERMS ? 3 : 1) * (W == X_F32 ? 4 : 2) * 512 / kSize;
+    constexpr int kStages = kStage <= 26 * 1024 ? 3 : 2;
+    const dim3 grid((unsigned)((a.M + 31) / 32), (unsigned)((a.R + 16 * RB - 1) / (16 * RB)));
+    hipLaunchKernelGGL((adapter_shrink_kernel<X, W, RB, kStages>), grid, dim3(512), 0, st, a);
 }
 
-template <int X, bool WB> void run_shrink(const ShrinkArgs &a, hipStream_t st)
+template <int X, int W> void run_shrink(const ShrinkArgs &a, hipStream_t st)
 {
-    constexpr int W = WB ? X_BF16 : X_F32;
-    if (X == X_I8 && a.M <= kFewTokens) {
-        hipLaunchKernelGGL((adapter_shrink_few_kernel<X_I8, W>), dim3((unsigned)(a.M * a.R / 4)), dim3(256),
-                           0, st, a);
-        return;
+    if constexpr (X == X_I8) {
+        if (a.M <= kFewTokens) {
+            hipLaunchKernelGGL(adapter_shrink_few_kernel<W>, dim3((unsigned)(a.M * a.R / 4)), dim3(256), 0,
+                               st, a);
+            return;
+        }
     }
-    // Two token blocks share an adapter's operands; when that leaves compute
-    // units without a workgroup, one block, ranks in workgroups of their own
-    // and more waves along the contraction.
-    const int64_t blocks = (a.M + 15) / 16;
-    if (blocks >= 512)
-        return a.R <= 16 ? go_shrink<X, W, 2, 1, 4>(a, st) : go_shrink<X, W, 2, 2, 4>(a, st);
-    return a.R <= 16 || blocks < 128 ? go_shrink<X, W, 1, 1, 16>(a, st) : go_shrink<X, W, 1, 2, 8>(a, st);
+    // Ranks above 16 share x's stage where w's fits beside it, unless that
+    // leaves compute units without a workgroup.
+    if constexpr (W == X_BF16) {
+        if (a.R > 16 && a.M >= 32 * 128)
+            return go_shrink<X, W, 2>(a, st);
+    }
+    go_shrink<X, W, 1>(a, st);
+}
+
+// ------------------------------------------------------------------ expand
+
+struct ExpandArgs {
+    AdapterEpilogue ad;
+    int64_t M, C;
+    float *out;             // [M, C], added to
+};
+
+// out[m, c] += sum_r p[m, r] q[id, c, r], for products of so few tiles that
+// adding the term in their epilogues would leave it to a few compute units: 16
+// tokens and 64 columns per wave.  QT as in the epilogues: q as one bf16 term, as
+// three, or fp32.
+template <int QT> __global__ __launch_bounds__(256) void adapter_expand_kernel(ExpandArgs a)
+{
+    const int lane = __lane_id(), w = threadIdx.x / kWave, R = a.ad.R;
+    const int64_t m = (int64_t)blockIdx.y * 16 + lane % 16;
+    const int64_t c0 = (int64_t)blockIdx.x * 256 + w * 64;
+    const int id = id_of(a.ad.ids, m, a.M, a.ad.L);
+    f32x4 acc[4];
+#pragma unroll
+    for (int b = 0; b < 4; b++) {
+        const int64_t c = c0 + 16 * b + 4 * (lane / 16);
+        acc[b] = f32x4{0, 0, 0, 0};
+        if (id >= 0 && c < a.C)
+            acc[b] = *reinterpret_cast<const f32x4 *>(a.out + m * a.C + c);
+    }
+    constexpr int kTerms = QT == 0 ? 3 : 1;
+    const int length = (QT == 0 ? 1 : QT == 1 ? 3 : 6) * R, steps = terms_steps(QT, R);
+    for_adapters(id, [&](int cur, bool mine) {
+        for (int k0 = 0; k0 < length; k0 += 32) {
+            const int k = k0 + 8 * (lane / 16);
+            const bool ok = k < length;
+            int pair = 0;
+            if constexpr (QT != 0)
+                pair = (k >= R) + (k >= 2 * R) + (QT == 3 ? (k >= 3 * R) + (k >= 4 * R) + (k >= 5 * R) : 0);
+            const int r = k - pair * R + (QT == 3 ? pair_other(pair) * R : 0);
+            Frag<kTerms> pf, qf[4];
+#pragma unroll
+            for (int t = 0; t < kTerms; t++)
+                pf.t[t] = load_frag<X_BF16>(
+                    a.ad.terms, (((int64_t)blockIdx.y * steps + k0 / 32 * kTerms + t) * 64 + lane) * 8, ok).t[0];
+#pragma unroll
+            for (int b = 0; b < 4; b++) {
+                const int64_t c = c0 + 16 * b + lane % 16;
+                qf[b] = load_frag<QT == 0 ? X_F32 : X_BF16>(
+                    a.ad.q, ((int64_t)cur * a.C + c) * (QT == 3 ? 3 : 1) * R + r, ok && c < a.C);
+            }
+            __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+            for (int b = 0; b < 4; b++) {
+                const f32x4 t = mfma(qf[b], pf, acc[b]);
+                acc[b] = mine ? t : acc[b];
+            }
+        }
+    });
+    if (id < 0)
+        return;
+#pragma unroll
+    for (int b = 0; b < 4; b++) {
+        const int64_t c = c0 + 16 * b + 4 * (lane / 16);
+        if (c < a.C)
+            *reinterpret_cast<f32x4 *>(a.out + m * a.C + c) = acc[b];
+    }
 }
 
 // ------------------------------------------------------- grouping of tokens
@@ -269,7 +412,8 @@ template <int X, bool WB> void run_shrink(const ShrinkArgs &a, hipStream_t st)
 // waves counts its own run of tokens, the counts become first places (adapter
 // by adapter, and for one adapter wave by wave), and each wave places its
 // tokens 64 at a time, one adapter among them after another.  Tokens without
-// an adapter come last.
+// an adapter come last.  The reads' latency is what takes the time: a wave
+// loads 512 tokens' adapters at once.
 constexpr int kGroupWaves = 8;
 
 __global__ __launch_bounds__(kGroupWaves *kWave) void adapter_group_kernel(const int32_t *__restrict__ ids,
@@ -278,19 +422,58 @@ __global__ __launch_bounds__(kGroupWaves *kWave) void adapter_group_kernel(const
                                                                            int32_t *__restrict__ start)
 {
     __shared__ int count[kGroupWaves][kMaxAdapters + 1];
-    __shared__ int total[kMaxAdapters + 2];
+    __shared__ int total[kMaxAdapters + 1];
     const int bins = L + 1, t = threadIdx.x, w = t / kWave, lane = __lane_id();
     for (int i = t; i < kGroupWaves * bins; i += kGroupWaves * kWave)
         count[i / bins][i % bins] = 0;
     __syncthreads();
-    const int64_t per = (M + kGroupWaves - 1) / kGroupWaves;
+    const int64_t per = ((M + kGroupWaves * kWave - 1) / (kGroupWaves * kWave)) * kWave;
     const int64_t r0 = w * per < M ? w * per : M, r1 = r0 + per < M ? r0 + per : M;
-    auto bin_of = [&](int64_t m) {
-        const int id = ids[m];
-        return id >= 0 && id < L ? id : L;
+    // f(m, bin, mask, n) for each adapter among 64 tokens of the wave's run; of
+    // 512 tokens with one adapter f is called at once, with a full mask and n =
+    // 8 groups of 64.  (The eight groups go through LDS so that the loop over
+    // them stays rolled: fetching unrolled code once costs more than running
+    // it.)
+    constexpr int kAtOnce = 8;
+    __shared__ int16_t seen[kGroupWaves][kAtOnce * kWave];
+    auto for_runs = [&](auto f) {
+        for (int64_t m0 = r0; m0 < r1; m0 += kAtOnce * kWave) {
+            int b[kAtOnce];
+            bool same = true;
+#pragma unroll
+            for (int q = 0; q < kAtOnce; q++) {
+                const int64_t m = m0 + q * kWave + lane;
+                b[q] = ids[m < r1 ? m : r1 - 1];
+            }
+            __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+            for (int q = 0; q < kAtOnce; q++) {
+                const int64_t m = m0 + q * kWave + lane;
+                b[q] = m >= r1 ? -1 : b[q] >= 0 && b[q] < L ? b[q] : L;
+                seen[w][q * kWave + lane] = (int16_t)b[q];
+                same = same && b[q] == __builtin_amdgcn_readfirstlane(b[0]);
+            }
+            if (__all(same)) {
+                f(m0 + lane, __builtin_amdgcn_readfirstlane(b[0]), ~0ull, kAtOnce);
+                continue;
+            }
+#pragma unroll 1
+            for (int q = 0; q < kAtOnce; q++) {
+                const int bin = seen[w][q * kWave + lane];
+                uint64_t left = __ballot(bin >= 0);
+                while (left) {
+                    const int cur = __builtin_amdgcn_readlane(bin, (int)__builtin_ctzll(left));
+                    const uint64_t mask = __ballot(bin == cur);
+                    f(m0 + q * kWave + lane, cur, mask, 1);
+                    left &= ~mask;
+                }
+            }
+        }
     };
-    for (int64_t m = r0 + lane; m < r1; m += kWave)
-        atomicAdd(&count[w][bin_of(m)], 1);
+    for_runs([&](int64_t, int bin, uint64_t mask, int n) {
+        if (lane == 0)
+            count[w][bin] += n * __popcll(mask);
+    });
     __syncthreads();
     for (int b = t; b < bins; b += kGroupWaves * kWave) {
         int s = 0;
@@ -324,28 +507,22 @@ __global__ __launch_bounds__(kGroupWaves *kWave) void adapter_group_kernel(const
         }
     }
     __syncthreads();
-    for (int64_t m0 = r0; m0 < r1; m0 += kWave) {
-        const int64_t m = m0 + lane;
-        const int b = m < r1 ? bin_of(m) : -1;
-        uint64_t left = __ballot(b >= 0);
-        while (left) {
-            const int cur = __builtin_amdgcn_readlane(b, (int)__builtin_ctzll(left));
-            const uint64_t mask = __ballot(b == cur);
-            const int first = count[w][cur];
-            if (b == cur)
-                order[first + __popcll(mask & ((1ull << lane) - 1))] = (int32_t)m;
-            if (lane == 0)
-                count[w][cur] = first + __popcll(mask);
-            left &= ~mask;
-        }
-    }
+    for_runs([&](int64_t m, int bin, uint64_t mask, int n) {
+        const int first = count[w][bin];
+        const int at = first + __popcll(mask & ((1ull << lane) - 1));
+        for (int q = 0; q < n; q++)
+            if ((mask >> lane) & 1)
+                order[at + q * kWave] = (int32_t)m + q * kWave;
+        if (lane == 0)
+            count[w][bin] = first + n * __popcll(mask);
+    });
 }
 
 // ------------------------------------------------------- adapter gradients
 
 // The tokens of an adapter are split into slabs of kSlab; a table entry says
 // which adapter a slab has and where its tokens lie in the grouped order.
-constexpr int kSlab = 512;
+constexpr int kSlab = 256;
 
 struct Slab {
     int32_t adapter, first, rows, pad;
@@ -353,7 +530,7 @@ struct Slab {
 
 struct PrepArgs {
     const void *a, *b;      // [L, R, K], [L, N, R]
-    void *at, *bt;          // [L, K, R], [L, R, N]
+    uint16_t *at, *bt;      // [L, K, terms, R], [terms, L, R, N]
     int64_t N, K, M;
     int L, R, slabs;
     const int32_t *start;
@@ -361,41 +538,63 @@ struct PrepArgs {
     int32_t *first;         // [L + 1]: the first slab of each adapter
 };
 
-// dst [cols, rows] = src [rows, cols], one 32 x 32 tile.
-template <typename T>
-__device__ __forceinline__ void transpose_tile(const T *src, T *dst, int64_t rows, int64_t cols, int64_t r0,
+// One 32 x 32 tile of src [rows, cols] turned into dst: element (r, c) goes to
+// dst[c * pitch + r], as bf16; fp32 values as three terms, `plane` elements
+// apart.
+template <bool WB>
+__device__ __forceinline__ void transpose_tile(const void *src, int64_t s0, uint16_t *dst, int64_t rows,
+                                               int64_t cols, int64_t pitch, int64_t plane, int64_t r0,
                                                int64_t c0)
 {
-    __shared__ T tile[32][33];
+    __shared__ uint32_t tile[32][33];
     const int x = threadIdx.x % 32, y = threadIdx.x / 32;
 #pragma unroll
     for (int i = y; i < 32; i += 8)
-        if (r0 + i < rows && c0 + x < cols)
-            tile[i][x] = src[(r0 + i) * cols + c0 + x];
+        if (r0 + i < rows && c0 + x < cols) {
+            const int64_t at = s0 + (r0 + i) * cols + c0 + x;
+            if constexpr (WB)
+                tile[i][x] = static_cast<const uint16_t *>(src)[at];
+            else
+                tile[i][x] = static_cast<const uint32_t *>(src)[at];
+        }
     __syncthreads();
 #pragma unroll
     for (int i = y; i < 32; i += 8)
-        if (c0 + i < cols && r0 + x < rows)
-            dst[(c0 + i) * rows + r0 + x] = tile[x][i];
+        if (c0 + i < cols && r0 + x < rows) {
+            uint16_t *to = dst + (c0 + i) * pitch + r0 + x;
+            if constexpr (WB) {
+                *to = (uint16_t)tile[x][i];
+            } else {
+                float v = __uint_as_float(tile[x][i]);
+#pragma unroll
+                for (int q = 0; q < 3; q++) {
+                    const uint32_t t = pack_bf16x2(v, 0.0f);
+                    to[q * plane] = (uint16_t)t;
+                    v = v - bf16_lo(t);
+                }
+            }
+        }
 }
 
 // What the backward kernels need first, in one launch: B transposed for the
-// product with dY and A for dX's epilogue (both then have the contraction
-// index contiguous), and the table of slabs.  Workgroup 0 of adapter 0 makes
-// the table, 256 adapters at a time.
-template <typename T> __global__ __launch_bounds__(256) void adapter_prep_kernel(PrepArgs p)
+// product with dY, A for dX's epilogue (both then have the contraction index
+// contiguous), fp32 ones split into bf16 terms (B [3, L, R, N], A [L, K, 3, R]),
+// and the table of slabs.  Workgroup 0 of adapter 0 makes the table, 256
+// adapters at a time.
+template <bool WB> __global__ __launch_bounds__(256) void adapter_prep_kernel(PrepArgs p)
 {
+    constexpr int kTerms = WB ? 1 : 3;
     const int t = threadIdx.x;
     if (blockIdx.x > 0) {
         const int64_t rt = (p.R + 31) / 32, nt = (p.N + 31) / 32, l = blockIdx.y;
         const int64_t k = blockIdx.x - 1;
         const int64_t sb = l * p.N * p.R, sa = l * p.K * p.R;
         if (k < rt * nt)
-            transpose_tile(static_cast<const T *>(p.b) + sb, static_cast<T *>(p.bt) + sb, p.N, p.R,
-                           k / rt * 32, k % rt * 32);
+            transpose_tile<WB>(p.b, sb, p.bt + sb, p.N, p.R, p.N, (int64_t)p.L * p.R * p.N, k / rt * 32,
+                               k % rt * 32);
         else
-            transpose_tile(static_cast<const T *>(p.a) + sa, static_cast<T *>(p.at) + sa, p.R, p.K,
-                           (k - rt * nt) % rt * 32, (k - rt * nt) / rt * 32);
+            transpose_tile<WB>(p.a, sa, p.at + sa * kTerms, p.R, p.K, (int64_t)kTerms * p.R, p.R,
+                               (k - rt * nt) % rt * 32, (k - rt * nt) / rt * 32);
         return;
     }
     if (blockIdx.y > 0)
@@ -498,49 +697,73 @@ __global__ __launch_bounds__(256) void adapter_outer_kernel(OuterArgs a)
 #pragma unroll
         for (int r = 0; r < RB; r++)
             acc[b][r] = f32x4{0, 0, 0, 0};
-    // Thread t brings 32 columns of token t / 8, and two ranks in 16 of p.
-    const int row = t / 8, xc = (t % 8) * 32, pc = (t % 8) * 2;
+    // Thread t brings 32 columns of token t / 8, sixteen bytes at a time (eight
+    // threads read 128 bytes in a row), and two ranks in 16 of p, into one of
+    // kSets register sets.
+    constexpr int kSets = X == X_F32 ? 1 : 2;
+    constexpr int kSize = X == X_I8 ? 1 : X == X_BF16 ? 2 : 4;
+    constexpr int kPieces = 2 * kSize, kPer = 16 / kSize;       // 16-byte pieces, values in one
+    const int row = t / 8, pc = (t % 8) * 2;
+    auto piece_col = [&](int q) { return (t % 8) * kPer + q * 8 * kPer; };
     auto token = [&](int i0) {
         const int i = i0 + row;
         const int64_t m = i < s.rows ? a.order[s.first + i] : -1;
         return m >= 0 && m < a.M ? m : (int64_t)-1;
     };
-    Raw16<X> xr[2];
-    f32x2 pr[RB];
-    float f = 0.0f;
-    auto load = [&](int64_t m) {
+    i32x4 xr[kSets][kPieces];
+    f32x2 pr[kSets][RB];
+    float f[kSets];
+    auto load = [&](int64_t m, auto S) {
+        constexpr int k = decltype(S)::value;
         const bool live = m >= 0;
         const int64_t mm = live ? m : 0;
 #pragma unroll
-        for (int h = 0; h < 2; h++)
-            xr[h] = load16<X>(a.x, mm * a.C + c0 + xc + 16 * h, live && c0 + xc + 16 * h < a.C);
-#pragma unroll
-        for (int r = 0; r < RB; r++) {
-            pr[r] = f32x2{0, 0};
-            if (live && 16 * r + pc < a.R)
-                pr[r] = *reinterpret_cast<const f32x2 *>(a.p + mm * a.R + 16 * r + pc);
+        for (int q = 0; q < kPieces; q++) {
+            xr[k][q] = i32x4{0, 0, 0, 0};
+            if (live && c0 + piece_col(q) < a.C)
+                xr[k][q] = *reinterpret_cast<const i32x4 *>(static_cast<const char *>(a.x) +
+                                                            (mm * a.C + c0 + piece_col(q)) * kSize);
         }
-        f = live && a.ps ? a.ps[mm] : 1.0f;
-    };
-    int64_t next = token(0);
-    load(next);
-    next = token(32);
-    for (int i0 = 0; i0 < s.rows; i0 += 32) {
-        __syncthreads();
-        auto put = [&](auto H) {
-            constexpr int h = decltype(H)::value;
-            const auto fr = frag_of<X, h % 2>(xr[h / 2]);
-#pragma unroll
-            for (int q = 0; q < XT; q++)
-                *reinterpret_cast<bf16x8 *>(&xs[q][XTile::at(row, xc + 8 * h)]) = fr.t[q];
-        };
-        put(std::integral_constant<int, 0>{});
-        put(std::integral_constant<int, 1>{});
-        put(std::integral_constant<int, 2>{});
-        put(std::integral_constant<int, 3>{});
 #pragma unroll
         for (int r = 0; r < RB; r++) {
-            float v0 = pr[r][0] * f, v1 = pr[r][1] * f;
+            pr[k][r] = f32x2{0, 0};
+            if (live && 16 * r + pc < a.R)
+                pr[k][r] = *reinterpret_cast<const f32x2 *>(a.p + mm * a.R + 16 * r + pc);
+        }
+        f[k] = live && a.ps ? a.ps[mm] : 1.0f;
+    };
+    int64_t next = -1;
+    // 32 tokens from i0, which set S holds; it is then loaded with those
+    // 32 kSets tokens on.
+    auto step = [&](int i0, auto S) {
+        constexpr int k = decltype(S)::value;
+        lds_barrier();
+#pragma unroll
+        for (int q = 0; q < kPieces; q++) {
+            const i32x4 raw = xr[k][q];
+            const int at = XTile::at(row, piece_col(q));
+            if constexpr (X == X_BF16) {
+                *reinterpret_cast<i32x4 *>(&xs[0][at]) = raw;
+            } else if constexpr (X == X_I8) {
+#pragma unroll
+                for (int h = 0; h < 2; h++) {
+                    float v[8];
+                    codes_to_float(i32x2{raw[2 * h], raw[2 * h + 1]}, v);
+                    *reinterpret_cast<bf16x8 *>(&xs[0][at + 8 * h]) = round8(v);
+                }
+            } else {
+                f32x4 v = __builtin_bit_cast(f32x4, raw);
+#pragma unroll
+                for (int h = 0; h < 3; h++) {
+                    const i32x2 b = {(int)pack_bf16x2(v[0], v[1]), (int)pack_bf16x2(v[2], v[3])};
+                    *reinterpret_cast<i32x2 *>(&xs[h][at]) = b;
+                    v = v - f32x4{bf16_lo(b[0]), bf16_hi(b[0]), bf16_lo(b[1]), bf16_hi(b[1])};
+                }
+            }
+        }
+#pragma unroll
+        for (int r = 0; r < RB; r++) {
+            float v0 = pr[k][r][0] * f[k], v1 = pr[k][r][1] * f[k];
 #pragma unroll
             for (int q = 0; q < 3; q++) {
                 const uint32_t b = pack_bf16x2(v0, v1);
@@ -549,9 +772,11 @@ __global__ __launch_bounds__(256) void adapter_outer_kernel(OuterArgs a)
                 v1 = v1 - bf16_hi(b);
             }
         }
-        __syncthreads();
-        load(next);             // (zeros after the last tokens)
-        next = token(i0 + 64);
+        // (No fence: the loads of the other set stay in flight.)
+        lds_barrier();
+        load(next, S);          // (zeros after the last tokens)
+        next = token(i0 + 32 * (kSets + 1));
+        __builtin_amdgcn_sched_barrier(0);
         Frag<XT> xf[4];
 #pragma unroll
         for (int b = 0; b < 4; b++)
@@ -567,6 +792,19 @@ __global__ __launch_bounds__(256) void adapter_outer_kernel(OuterArgs a)
 #pragma unroll
             for (int b = 0; b < 4; b++)
                 acc[b][r] = TRANS ? mfma(pf, xf[b], acc[b][r]) : mfma(xf[b], pf, acc[b][r]);
+        }
+    };
+    constexpr std::integral_constant<int, 0> kSet0{};
+    constexpr std::integral_constant<int, kSets - 1> kSet1{};
+    load(token(0), kSet0);
+    if constexpr (kSets == 2)
+        load(token(32), kSet1);
+    next = token(32 * kSets);
+    for (int i0 = 0; i0 < s.rows; i0 += 32 * kSets) {
+        step(i0, kSet0);
+        if constexpr (kSets == 2) {
+            if (i0 + 32 < s.rows)
+                step(i0 + 32, kSet1);
         }
     }
     float *part = a.part + (int64_t)blockIdx.y * a.R * a.C;
@@ -630,11 +868,29 @@ __global__ __launch_bounds__(256) void adapter_sum_kernel(const float *__restric
 
 } // namespace
 
-void launch_adapter_u(const AdapterArgs &g, const int8_t *qx, const float *sx, float *u,
-                      hipStream_t st)
+size_t adapter_terms_bytes(int64_t M, int64_t R, int qt)
 {
-    const ShrinkArgs s{qx, sx, g.a, g.scale, g.ids, g.M, g.K, g.L, g.R, u};
-    g.bf16 ? run_shrink<X_I8, true>(s, st) : run_shrink<X_I8, false>(s, st);
+    return (size_t)((M + 15) / 16) * terms_steps(qt, (int)R) * 1024;
+}
+
+void launch_adapter_u(const AdapterArgs &g, const int8_t *qx, const float *sx, float *u,
+                      uint16_t *terms, hipStream_t st)
+{
+    const ShrinkArgs s{qx, sx, g.a, g.scale, g.ids, g.M, g.K, g.L, g.R, u, terms, g.bf16 ? 1 : 0};
+    g.bf16 ? run_shrink<X_I8, X_BF16>(s, st) : run_shrink<X_I8, X_F32>(s, st);
+}
+
+void launch_adapter_expand(const AdapterEpilogue &ad, bool terms, int64_t M, int64_t C, float *out,
+                           hipStream_t st)
+{
+    const ExpandArgs e{ad, M, C, out};
+    const dim3 grid((unsigned)((C + 255) / 256), (unsigned)((M + 15) / 16));
+    if (ad.bf16)
+        hipLaunchKernelGGL(adapter_expand_kernel<1>, grid, dim3(256), 0, st, e);
+    else if (terms)
+        hipLaunchKernelGGL(adapter_expand_kernel<3>, grid, dim3(256), 0, st, e);
+    else
+        hipLaunchKernelGGL(adapter_expand_kernel<0>, grid, dim3(256), 0, st, e);
 }
 
 void launch_adapter_group(const int32_t *ids, int64_t M, int L, int32_t *order, int32_t *start,
@@ -650,7 +906,7 @@ static size_t round256(size_t n) { return (n + 255) & ~(size_t)255; }
 
 // Offsets of a backward call's workspace.
 struct BwdLayout {
-    size_t bt, at, v, table, first, pa, pb, end;
+    size_t bt, at, v, terms, table, first, pa, pb, end;
 };
 
 static BwdLayout bwd_layout(int64_t M, int64_t N, int64_t K, int64_t L, int64_t R)
@@ -658,9 +914,10 @@ static BwdLayout bwd_layout(int64_t M, int64_t N, int64_t K, int64_t L, int64_t 
     const size_t slabs = (size_t)slabs_of(M, L);
     BwdLayout o;
     o.bt = 0;
-    o.at = round256(o.bt + (size_t)L * R * N * 4);
-    o.v = round256(o.at + (size_t)L * R * K * 4);
-    o.table = round256(o.v + (size_t)M * R * 4);
+    o.at = round256(o.bt + (size_t)L * R * N * 6);
+    o.v = round256(o.at + (size_t)L * R * K * 6);
+    o.terms = round256(o.v + (size_t)M * R * 4);
+    o.table = round256(o.terms + adapter_terms_bytes(M, R, 3));
     o.first = round256(o.table + slabs * sizeof(Slab));
     o.pa = round256(o.first + ((size_t)L + 1) * 4);
     o.pb = round256(o.pa + slabs * (size_t)R * K * 4);
@@ -678,23 +935,25 @@ AdapterEpilogue launch_adapter_bwd_v(const AdapterArgs &g, const void *dy, bool 
 {
     char *w = static_cast<char *>(ws);
     const BwdLayout o = bwd_layout(g.M, g.N, g.K, g.L, g.R);
-    const PrepArgs p{g.a, g.b, w + o.at, w + o.bt, g.N, g.K, g.M, g.L, g.R, (int)slabs_of(g.M, g.L), start,
+    const PrepArgs p{g.a, g.b, reinterpret_cast<uint16_t *>(w + o.at), reinterpret_cast<uint16_t *>(w + o.bt),
+                     g.N, g.K, g.M, g.L, g.R, (int)slabs_of(g.M, g.L), start,
                      reinterpret_cast<Slab *>(w + o.table), reinterpret_cast<int32_t *>(w + o.first)};
     const int64_t tiles = (int64_t)((g.R + 31) / 32) * ((g.N + 31) / 32 + (g.K + 31) / 32);
     const dim3 grid((unsigned)(g.M > 0 ? 1 + tiles : 1), (unsigned)g.L);
     if (g.bf16)
-        hipLaunchKernelGGL(adapter_prep_kernel<uint16_t>, grid, dim3(256), 0, st, p);
+        hipLaunchKernelGGL(adapter_prep_kernel<true>, grid, dim3(256), 0, st, p);
     else
-        hipLaunchKernelGGL(adapter_prep_kernel<uint32_t>, grid, dim3(256), 0, st, p);
+        hipLaunchKernelGGL(adapter_prep_kernel<false>, grid, dim3(256), 0, st, p);
     const ShrinkArgs s{dy,  nullptr, w + o.bt, g.scale, g.ids, g.M, g.N,
-                       g.L, g.R,     reinterpret_cast<float *>(w + o.v)};
+                       g.L, g.R,     reinterpret_cast<float *>(w + o.v),
+                       reinterpret_cast<uint16_t *>(w + o.terms), g.bf16 ? 1 : 3};
     if (g.M > 0) {
         if (dy_bf16)
-            g.bf16 ? run_shrink<X_BF16, true>(s, st) : run_shrink<X_BF16, false>(s, st);
+            g.bf16 ? run_shrink<X_BF16, X_BF16>(s, st) : run_shrink<X_BF16, W_TERMS>(s, st);
         else
-            g.bf16 ? run_shrink<X_F32, true>(s, st) : run_shrink<X_F32, false>(s, st);
+            g.bf16 ? run_shrink<X_F32, X_BF16>(s, st) : run_shrink<X_F32, W_TERMS>(s, st);
     }
-    return AdapterEpilogue{s.out, w + o.at, g.ids, g.L, g.R, g.bf16};
+    return AdapterEpilogue{s.out, s.terms, w + o.at, g.ids, g.L, g.R, g.bf16};
 }
 
 void launch_adapter_bwd_w(const AdapterArgs &g, const void *dy, bool dy_bf16, const int8_t *qx,

@@ -108,6 +108,70 @@ __device__ __forceinline__ int id_of(const int32_t *ids, int64_t m, int64_t M, i
     return id >= 0 && id < L ? id : -1;
 }
 
+// The bf16 terms of a token matrix p [rows, R], laid out as the products with
+// it read them: for each block of 16 rows, step by step of 32 slots, the 64
+// lanes' eight values (lane l: row l % 16, slots 8 (l / 16) ..), so that a wave
+// reads 1024 bytes in a row.  (Read row by row, every lane was a cache access of
+// its own, and those took longer than the products.)  The form QT of the other
+// operand decides the slots: 1, one bf16 term: p's three terms one after
+// another, 3 R slots; 3, three terms: the six pairs of terms above 2^-24, the
+// smallest first, 6 R slots; 0, fp32, split where it is used: the ranks in
+// steps of 32, and each step once per term.
+constexpr int terms_steps(int qt, int R)
+{
+    return qt == 0 ? 3 * ((R + 31) / 32) : ((qt == 1 ? 3 : 6) * R + 31) / 32;
+}
+
+// Term of p in pair i of six (of the other operand: pair_other).
+__device__ __forceinline__ int pair_term(int i) { return (0x001012 >> (4 * i)) & 3; }
+__device__ __forceinline__ int pair_other(int i) { return (0x010210 >> (4 * i)) & 3; }
+
+// Where slot k of a row lies among the rows' terms.
+__device__ __forceinline__ int64_t term_at(int steps, int64_t row, int k)
+{
+    return (((row / 16) * steps + k / 32) * 64 + row % 16 + 16 * (k % 32 / 8)) * 8 + k % 8;
+}
+
+// Writes N consecutive values of a row, from rank r (a multiple of N; N
+// divides 8), into the terms.
+template <int N>
+__device__ __forceinline__ void put_terms(uint16_t *terms, int qt, int R, int64_t row, int r, const float (&v0)[N])
+{
+    const int steps = terms_steps(qt, R);
+    float v[N];
+#pragma unroll
+    for (int e = 0; e < N; e++)
+        v[e] = v0[e];
+#pragma unroll
+    for (int t = 0; t < 3; t++) {
+        uint16_t b[N];
+#pragma unroll
+        for (int e = 0; e < N; e++) {
+            const uint32_t w = pack_bf16x2(v[e], 0.0f);
+            b[e] = (uint16_t)w;
+            v[e] = v[e] - bf16_lo(w);
+        }
+        auto put = [&](int k) {
+            uint16_t *at = terms + term_at(steps, row, k);
+            if constexpr (N == 4)
+                *reinterpret_cast<i32x2 *>(at) =
+                    i32x2{(int)(b[0] | (uint32_t)b[1] << 16), (int)(b[2] | (uint32_t)b[3] << 16)};
+            else
+                *at = b[0];
+        };
+        if (qt == 0) {
+            put((r / 32 * 3 + t) * 32 + r % 32);
+        } else if (qt == 1) {
+            put(t * R + r);
+        } else {
+#pragma unroll
+            for (int i = 0; i < 6; i++)
+                if (pair_term(i) == t)
+                    put(i * R + r);
+        }
+    }
+}
+
 } // namespace
 
 } // namespace qlin

@@ -139,7 +139,8 @@ size_t qlin_adapter_fwd_ws_bytes(int64_t M, int64_t N, int64_t K, int64_t L, int
 {
     if (!adapter_shape_ok(M, N, K, L, R) || K > QLIN_MAX_CONTRACTION)
         return 0;
-    return qlin_product_ws_bytes(QLIN_OP_FWD, M, N, K);
+    return round256(qlin_product_ws_bytes(QLIN_OP_FWD, M, N, K)) +
+           qlin::adapter_terms_bytes(M, R, 0);
 }
 
 int qlin_adapter_fwd(const int8_t *qx, const float *sx, const int8_t *qw, const float *sw,
@@ -171,11 +172,13 @@ int qlin_adapter_fwd(const int8_t *qx, const float *sx, const int8_t *qw, const 
         return QLIN_EINVAL;
     const hipStream_t s = as_stream(stream);
     qlin::ProductArgs p{QLIN_OP_FWD, qx, qw, M, N, K, sx, sw, bias, y, false};
-    if (need)
+    const size_t pw = qlin_product_ws_bytes(QLIN_OP_FWD, M, N, K);
+    if (pw)
         p.split_ws = workspace;
+    uint16_t *terms = reinterpret_cast<uint16_t *>(static_cast<char *>(workspace) + round256(pw));
     const qlin::AdapterArgs g{a, b, w_dtype == QLIN_BF16, scale, ids, M, N, K, (int)L, (int)R};
-    qlin::launch_adapter_u(g, qx, sx, u, s);
-    qlin::launch_product_adapter(p, {u, b, ids, (int)L, (int)R, g.bf16}, s);
+    qlin::launch_adapter_u(g, qx, sx, u, terms, s);
+    qlin::launch_product_adapter(p, {u, terms, b, ids, (int)L, (int)R, g.bf16}, s);
     return finish();
 }
 

@@ -2,6 +2,8 @@
 // token's adapter is added to the outputs before they are first written, so
 // the adapters cost no pass over y or dx (reading and writing y once more took
 // 72 us of 546 at 12000 x 5376 -> 7168).
+#include <stdlib.h>
+
 #include "gemm_kernel.hpp"
 
 namespace qlin {
@@ -41,13 +43,24 @@ void launch_product_adapter(const ProductArgs &a, const AdapterEpilogue &ad, hip
     }
     GemmParams p = gemm_params(a);
     p.ad = ad;
+    // (Diagnostic switch, to be replaced by a rule.)
+    static const int cut = getenv("QCUT") ? atoi(getenv("QCUT")) : 128;
+    if (((p.R + 255) / 256) * ((p.S + 255) / 256) < cut) {
+        ProductArgs b = a;
+        b.had = 0;
+        launch_product(b, st);
+        launch_adapter_expand(ad, a.op == 1, p.R, p.S, static_cast<float *>(a.out), st);
+        if (a.op == 1 && a.had >= 2 && a.had <= 128)
+            launch_hadamard(a.out, false, a.M, a.K, a.had, a.had_scale, static_cast<float *>(a.out), st);
+        return;
+    }
     if (a.op == 0) {
         ad.bf16 ? run<false, EPI_FWD_ADAPTER_BF16>(p, st) : run<false, EPI_FWD_ADAPTER_F32>(p, st);
     } else {
         // (A block of 1: no rotation, or one that follows in a launch of its own.)
         p.had = a.had >= 2 && a.had <= 128 ? a.had : 1;
         p.had_scale = p.had > 1 ? a.had_scale : 1.0f;
-        ad.bf16 ? run<true, EPI_HAD_ADAPTER_BF16>(p, st) : run<true, EPI_HAD_ADAPTER_F32>(p, st);
+        ad.bf16 ? run<true, EPI_HAD_ADAPTER_BF16>(p, st) : run<true, EPI_HAD_ADAPTER_TERMS>(p, st);
     }
 }
 

@@ -298,10 +298,11 @@ __device__ __forceinline__ void barrier_no_fence()
 // Hadamard rotation of each output row (blocks of up to 128 columns).  The
 // ADAPTER ones add each token's low-rank term to the dequantized values, the
 // second before the rotation (a rotation block of 1 leaves them as they are).
-// F32 and BF16: the type of the adapters' matrices.
+// BF16, F32 and TERMS: the form of the adapters' column matrices (one bf16 term,
+// fp32, three bf16 terms).
 enum {
     EPI_RAW = 0, EPI_ROWSCALE = 1, EPI_FWD = 2, EPI_ROWSCALE_HAD = 3, EPI_FWD_ADAPTER_BF16 = 4,
-    EPI_FWD_ADAPTER_F32 = 5, EPI_HAD_ADAPTER_BF16 = 6, EPI_HAD_ADAPTER_F32 = 7
+    EPI_FWD_ADAPTER_F32 = 5, EPI_HAD_ADAPTER_BF16 = 6, EPI_HAD_ADAPTER_TERMS = 7
 };
 
 // Tile order: workgroups are dispatched round-robin over the 8 XCDs, so
@@ -638,75 +639,123 @@ __device__ __forceinline__ float tofloat(const GemmParams &p, int32_t c, int64_t
 // The adapters of the wave's rows go one by one, mostly a single one (requests
 // are runs of tokens): its columns' operands are loaded once for all row blocks
 // that have it, and a lane takes the sums if its row has it.
-template <int W, int FM, int FN>
-__device__ __forceinline__ void add_adapters(const GemmParams &p, int i, int j, f32x4 (&val)[FM][FN])
-{
+//
+// p comes as bf16 terms in the layout of adapter_frag.hpp, whose slots the form
+// QT of q decides: q as one bf16 term (1), as three terms like p's (3), or fp32
+// (0), which is split here.
+template <int QT, int FM, int FN> struct AdapterTerm {
     // Row blocks between the load of p's values and their use (the scheduler
-    // would otherwise load all of them at once and spill).
-    constexpr int kAhead = W == X_F32 ? 1 : 3;
-    const AdapterEpilogue &ad = p.ad;
-    const int lane = __lane_id();
-    int id[FM];
+    // would otherwise load all of them at once; with a split q they would not
+    // fit the registers).
+    static constexpr int kAhead = QT == 0 ? 1 : FM - 1;
+    static constexpr int kTerms = QT == 0 ? 3 : 1;  // of p and q per step
+    using F = Frag<kTerms>;
+    const GemmParams &p;
+    const int i, j, lane, length;
+    int id[FM], cur, k0;
+    F f[kAhead + 1], q[FN];
+
+    // Loads the rows' adapters.
+    __device__ __forceinline__ AdapterTerm(const GemmParams &p, int i, int j)
+        : p(p), i(i), j(j), lane(__lane_id()), length((QT == 0 ? 1 : QT == 1 ? 3 : 6) * p.ad.R)
+    {
 #pragma unroll
-    for (int a = 0; a < FM; a++)
-        id[a] = id_of(ad.ids, i + 16 * a + lane % 16, p.R, ad.L);
-    auto next = [&]() {
-        int cur = -1;
+        for (int a = 0; a < FM; a++)
+            id[a] = id_of(p.ad.ids, i + 16 * a + lane % 16, p.R, p.ad.L);
+    }
+
+    __device__ __forceinline__ void next()
+    {
+        cur = -1;
+        k0 = 0;
 #pragma unroll
         for (int a = 0; a < FM; a++) {
             const uint64_t left = __ballot(id[a] >= 0);
             if (left)
                 cur = __builtin_amdgcn_readlane(id[a], (int)__builtin_ctzll(left));
         }
-        return cur;
-    };
-    auto p_raw = [&](int a, int r) {
-        const int row = i + 16 * a + lane % 16;
-        return load_raw8<false>(ad.p, (int64_t)(row < p.R ? row : p.R - 1) * ad.R + (r < ad.R ? r : 0));
-    };
-    // (One loop over adapters and ranks: nested ones made the register
-    // allocator spill val.)
-    int cur = next(), r0 = 0;
-    while (cur >= 0) {
-        const int r = r0 + 8 * (lane / 16);
-        Raw8<false> raw[kAhead + 1];
+    }
+
+    // Where the lane's eight slots of the step lie in a row of q.
+    __device__ __forceinline__ int q_slot() const
+    {
+        const int R = p.ad.R, k = k0 + 8 * (lane / 16);
+        if constexpr (QT == 0)
+            return k;
+        const int pair = (k >= R) + (k >= 2 * R) + (QT == 3 ? (k >= 3 * R) + (k >= 4 * R) + (k >= 5 * R) : 0);
+        return k - pair * R + (QT == 3 ? pair_other(pair) * R : 0);
+    }
+
+    // (Slots past the end meet zeros in q; p's are then the step's first ones.)
+    __device__ __forceinline__ F p_frag(int a) const
+    {
+        const int steps = terms_steps(QT, p.ad.R), block = i + 16 * a < p.R ? i / 16 + a : 0;
+        const int at = k0 + 8 * (lane / 16) < length ? lane : lane % 16;
+        const int step = __builtin_amdgcn_readfirstlane(block * steps + k0 / 32 * kTerms);
+        const uint16_t *from = p.ad.terms + (int64_t)step * 512;
+        F v;
 #pragma unroll
-        for (int a = 0; a < kAhead; a++)
-            raw[a] = p_raw(a, r);
-        Frag<terms_of(W)> q[FN];
+        for (int t = 0; t < kTerms; t++)
+            v.t[t] = *reinterpret_cast<const bf16x8 *>(from + t * 512 + (uint32_t)at * 8);
+        return v;
+    }
+
+    // Loads the step's column operands and the first rows'.
+    __device__ __forceinline__ void load()
+    {
+        constexpr int W = QT == 0 ? X_F32 : X_BF16;
+        const int64_t per = (QT == 3 ? 3 : 1) * p.ad.R;
+        const bool ok = k0 + 8 * (lane / 16) < length;
+        const int r = q_slot();
 #pragma unroll
         for (int b = 0; b < FN; b++) {
             const int col = j + 16 * b + lane % 16;
-            q[b] = load_frag<W>(ad.q, ((int64_t)cur * p.S + col) * ad.R + r, r < ad.R && col < p.S);
+            q[b] = load_frag<W>(p.ad.q, ((int64_t)cur * p.S + col) * per + r, ok && col < p.S);
         }
 #pragma unroll
-        for (int a = 0; a < FM; a++) {
-            if (a + kAhead < FM)
-                raw[(a + kAhead) % (kAhead + 1)] = p_raw(a + kAhead, r);
-            const bool mine = id[a] == cur;
-            if (__any(mine)) {
-                // (Ranks past R meet zeros in q; p's are the row's first ones.)
-                float v[8];
-                unpack8<false>(raw[a % (kAhead + 1)], v);
-                const auto f = split8(v);
+        for (int a = 0; a < kAhead; a++)
+            f[a] = p_frag(a);
+    }
+
+    // Picks the first adapter and loads its first step.
+    __device__ __forceinline__ void begin()
+    {
+        next();
+        if (cur >= 0)
+            load();
+    }
+
+    __device__ __forceinline__ void add(f32x4 (&val)[FM][FN])
+    {
+        // (One loop over adapters and ranks: nested ones made the register
+        // allocator spill val.)
+        while (cur >= 0) {
 #pragma unroll
-                for (int b = 0; b < FN; b++) {
-                    const f32x4 t = mfma(q[b], f, val[a][b]);
-                    val[a][b] = mine ? t : val[a][b];
+            for (int a = 0; a < FM; a++) {
+                if (a + kAhead < FM)
+                    f[(a + kAhead) % (kAhead + 1)] = p_frag(a + kAhead);
+                const bool mine = id[a] == cur;
+                if (__any(mine)) {
+#pragma unroll
+                    for (int b = 0; b < FN; b++) {
+                        const f32x4 t = mfma(q[b], f[a % (kAhead + 1)], val[a][b]);
+                        val[a][b] = mine ? t : val[a][b];
+                    }
                 }
+                __builtin_amdgcn_sched_barrier(0);
             }
-            __builtin_amdgcn_sched_barrier(0);
-        }
-        r0 += 32;
-        if (r0 >= ad.R) {
+            k0 += 32;
+            if (k0 >= length) {
 #pragma unroll
-            for (int a = 0; a < FM; a++)
-                id[a] = id[a] == cur ? -1 : id[a];
-            cur = next();
-            r0 = 0;
+                for (int a = 0; a < FM; a++)
+                    id[a] = id[a] == cur ? -1 : id[a];
+                next();
+            }
+            if (cur >= 0)
+                load();
         }
     }
-}
+};
 
 // The product kernel: 256 x 256 tiles, 8 waves of RW x CW = 128 x 64 outputs
 // in FM x FN = 8 x 4 blocks of 16 x 16, 128 contraction bytes per stage in
@@ -731,8 +780,7 @@ __global__ __launch_bounds__(WM *WN * 64, 1) void gemm_kernel(GemmParams p)
         EPI == EPI_FWD || EPI == EPI_FWD_ADAPTER_BF16 || EPI == EPI_FWD_ADAPTER_F32;
     constexpr bool kAdapter = EPI >= EPI_FWD_ADAPTER_BF16;
     constexpr bool kHad = EPI == EPI_ROWSCALE_HAD || (kAdapter && !kFwd);
-    constexpr int kAdapterType =
-        EPI == EPI_FWD_ADAPTER_BF16 || EPI == EPI_HAD_ADAPTER_BF16 ? X_BF16 : X_F32;
+    constexpr int kQ = EPI == EPI_FWD_ADAPTER_F32 ? 0 : EPI == EPI_HAD_ADAPTER_TERMS ? 3 : 1;
     constexpr int BM = 256, BN = 256, kBK = 128;
     constexpr int NT = WM * WN * kWave;
     constexpr int RW = BM / WM, CW = BN / WN;
@@ -1039,6 +1087,10 @@ __global__ __launch_bounds__(WM *WN * 64, 1) void gemm_kernel(GemmParams p)
     // sums, and the term is added to all of them.
     f32x4 val[kAdapter ? FM : 1][FN];
     if constexpr (kAdapter) {
+        // The term's first loads are in flight during the dequantization.
+        AdapterTerm<kQ, FM, FN> term(p, i0 + wi * RW, j0 + wj * CW);
+        term.begin();
+        __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
         for (int a = 0; a < FM; a++)
 #pragma unroll
@@ -1055,7 +1107,7 @@ __global__ __launch_bounds__(WM *WN * 64, 1) void gemm_kernel(GemmParams p)
                 }
                 val[a][b] = v;
             }
-        add_adapters<kAdapterType, FM, FN>(p, i0 + wi * RW, j0 + wj * CW, val);
+        term.add(val);
     }
     auto block_values = [&](int a, uint32_t (&o)[FN][4]) {
         const int i = i0 + wi * RW + 16 * a + lane % 16;

@@ -53,9 +53,13 @@ struct ProductArgs {
 void launch_product(const ProductArgs &p, hipStream_t st);
 
 // The low-rank term of a product's output row i: sum_r p[i, r] q[ids[i], j, r]
-// with p [rows, R] fp32 and q [L, cols, R] fp32 or bf16.
+// with p [rows, R] fp32 and q [L, cols, R] bf16 or, in the forward product, fp32;
+// the dX product takes an fp32 q as three bf16 terms, [L, cols, 3, R].  terms
+// holds p as such terms, in the layout of adapter_frag.hpp (the forward product
+// of 16 rows or fewer reads p instead).
 struct AdapterEpilogue {
     const float *p;
+    const uint16_t *terms;
     const void *q;
     const int32_t *ids;
     int L, R;
@@ -64,6 +68,10 @@ struct AdapterEpilogue {
 // A forward or dX product (no workspace mode, contraction within the int32
 // bound) with that term added.
 void launch_product_adapter(const ProductArgs &p, const AdapterEpilogue &ad, hipStream_t st);
+// The term added to outputs [M, C] in memory; terms: an fp32 q comes as three
+// bf16 terms.
+void launch_adapter_expand(const AdapterEpilogue &ad, bool terms, int64_t M, int64_t C, float *out,
+                           hipStream_t st);
 
 // Whether the product kernels can address every operand byte of this shape
 // with their 32-bit buffer offsets (for contractions past the int32 bound,
@@ -148,9 +156,11 @@ struct AdapterArgs {
     int64_t M, N, K;
     int L, R;
 };
-// u = scale x^ A^T.
+// u = scale x^ A^T; terms: u as bf16 terms, adapter_terms_bytes of them, for a
+// q of form qt (1: bf16, 0: fp32, 3: three bf16 terms).
+size_t adapter_terms_bytes(int64_t M, int64_t R, int qt);
 void launch_adapter_u(const AdapterArgs &g, const int8_t *qx, const float *sx, float *u,
-                      hipStream_t st);
+                      uint16_t *terms, hipStream_t st);
 void launch_adapter_group(const int32_t *ids, int64_t M, int L, int32_t *order, int32_t *start,
                           hipStream_t st);
 // Backward, with a workspace of adapter_bwd_bytes: v = scale dY B (kept in
