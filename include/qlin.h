@@ -503,9 +503,10 @@ size_t qlin_rmsnorm_bwd_ws_bytes(int64_t rows, int64_t cols);
  * zeros); 1 <= L; M <= QLIN_MAX_ADAPTER_ROWS.  The projection's own part is
  * exactly qlin_product_ws's; the adapter's part is summed in fp32 from
  * operands kept to their 24 bits.  Any M, a single token too.
- * workspace: qlin_adapter_fwd_ws_bytes bytes, zero-filled before its first use
- * (every call leaves it ready for the next; calls that share one must not
- * overlap in time).
+ * workspace: qlin_adapter_fwd_ws_bytes bytes, zero-filled before its first use.
+ * Every call leaves it ready for the next, of any shape and of the backward
+ * call too where it is large enough for it; calls that share one must not
+ * overlap in time.
  */
 #define QLIN_MAX_RANK 128
 #define QLIN_MAX_ADAPTERS 1023          /* of the grouped and backward calls */
@@ -542,7 +543,7 @@ int qlin_adapter_group(const int32_t *ids, int64_t M, int64_t L, int32_t *order,
  *   dx     may be NULL (then qg1, sg1 and qw may be too): adapter gradients only.
  * The sums over tokens are fp32, in a fixed order.  Limits as in the forward
  * call, L <= QLIN_MAX_ADAPTERS; had_block as in qlin_bwd_dx.
- * workspace: qlin_adapter_bwd_ws_bytes bytes, zero-filled before its first use.
+ * workspace: qlin_adapter_bwd_ws_bytes bytes, under the same rules.
  */
 int qlin_adapter_bwd(const void *dy, int dy_dtype, const int8_t *qg1, const float *sg1,
                      const int8_t *qw, const int8_t *qx, const float *sx, const float *u,

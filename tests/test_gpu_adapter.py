@@ -321,3 +321,24 @@ def test_other_stream_and_graph():
         torch.cuda.synchronize()
         for a, b in zip(want, out):
             assert torch.equal(a, b)
+
+
+def test_one_workspace_for_all_calls():
+    """Forward and backward calls of different shapes, one after another on one
+    workspace, give what fresh ones give, whole and split contractions alike."""
+    torch = torch_cuda()
+    import w8a8_integer_linear_amd as qlin
+    shapes = [(40, 512, 2048, 3, 16, "bf16"), (700, 2304, 1024, 2, 64, "f32"), (5, 64, 512, 2, 8, "f32"),
+              (40, 4096, 512, 4, 128, "f32"), (1500, 2304, 2304, 3, 24, "bf16"), (33, 512, 2048, 3, 16, "bf16")]
+    size = max(max(qlin.qlin_adapter_fwd_ws_bytes(*s[:5]), qlin.qlin_adapter_bwd_ws_bytes(*s[:5]))
+               for s in shapes)
+    ws = torch.zeros(size, dtype=torch.uint8, device="cuda")
+    for k, (M, N, K, L, R, w) in enumerate(shapes * 2):
+        announce("shared workspace", M, N, K, L, R, w)
+        d = _cuda(_case(torch, M, N, K, L, R, w, "bf16", seed=k, runs=3))
+        got = [*_run_fwd(qlin, d, workspace=ws)]
+        d["u"] = got[1]
+        got += _run_bwd(qlin, d, L, 128, workspace=ws)
+        want = [*_run_fwd(qlin, d)] + [*_run_bwd(qlin, d, L, 128)]
+        for a, b in zip(want, got):
+            assert torch.equal(a, b)

@@ -41,6 +41,11 @@ struct ShrinkArgs {
     float *out;             // [M, R]
     uint16_t *terms;        // out as bf16 terms for a q of form qt
     int qt;
+    // The contraction in `splits` workgroups per 32 tokens and 16 ranks: their
+    // sums (part: 512 values each) and arrival counters (zero before and after).
+    int splits;
+    float *part;
+    unsigned *count;
 };
 
 // Four values of a row of out, from rank r.
@@ -128,7 +133,10 @@ __global__ __launch_bounds__(512) void adapter_shrink_kernel(ShrinkArgs a)
     for (int t = 0; t < 2; t++)
         left[t] = id[t] = id_of(a.ids, m0 + 16 * t + lane % 16, a.M, a.L);
     const int mine_id = tb ? id[1] : id[0];
-    const int steps = (int)((a.C + kStep - 1) / kStep);
+    // This workgroup's stages of the contraction.
+    const int all = (int)((a.C + kStep - 1) / kStep);
+    const int first = all * (int)blockIdx.z / a.splits;
+    const int steps = all * ((int)blockIdx.z + 1) / a.splits - first;
     f32x4 acc[RB];
 #pragma unroll
     for (int b = 0; b < RB; b++)
@@ -148,7 +156,7 @@ __global__ __launch_bounds__(512) void adapter_shrink_kernel(ShrinkArgs a)
             lds_byte *dst = (lds_byte *)smem + (s % STAGES) * kStageBytes;
             // (Stages past the end read zeros, so that every iteration waits
             // for the same number of loads.)
-            const int64_t k0 = (int64_t)s * kStep;
+            const int64_t k0 = (int64_t)(s < steps ? first + s : all) * kStep;
 #pragma unroll
             for (int n = 0; n < kXLoads; n++) {
                 int r, byte;
@@ -245,13 +253,45 @@ __global__ __launch_bounds__(512) void adapter_shrink_kernel(ShrinkArgs a)
         red[(b * 8 + w) * kWave + lane] = acc[b];
     __syncthreads();
     const int64_t m = m0 + 16 * tb + lane % 16;
-    const float f = mine_id >= 0 ? a.scale[mine_id] * (a.xs ? a.xs[m] : 1.0f) : 0.0f;
     const int r = rb0 + 16 * quarter + 4 * (lane / 16);
-    if (quarter < RB && m < a.M && r < a.R) {
-        f32x4 s = red[(quarter * 8 + tb) * kWave + lane];
+    f32x4 s = {0, 0, 0, 0};
+    if (quarter < RB) {
+        s = red[(quarter * 8 + tb) * kWave + lane];
 #pragma unroll
         for (int q = 1; q < 4; q++)
             s += red[(quarter * 8 + tb + 2 * q) * kWave + lane];
+    }
+    if (a.splits > 1) {
+        // The sums cross XCDs, whose L2s are not coherent: stored and read with
+        // the device-scope bit, the stores complete before the arrival counts.
+        constexpr int kCoherentBit = 16;
+        const int unit = blockIdx.x * gridDim.y + blockIdx.y;
+        const __amdgpu_buffer_rsrc_t pr =
+            buffer_of(a.part + (int64_t)unit * a.splits * (RB * 2 * kWave * 4));
+        const uint32_t at = ((quarter * 2 + tb) * kWave + lane) * 16;
+        constexpr uint32_t kPart = RB * 2 * kWave * 16;
+        if (quarter < RB)
+            __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(i32x4, s), pr,
+                                                   blockIdx.z * kPart + at, 0, kCoherentBit);
+        asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+        __syncthreads();
+        int *flag = reinterpret_cast<int *>(smem);
+        if (threadIdx.x == 0) {
+            const unsigned arrived = atomicAdd(a.count + unit, 1u);
+            *flag = arrived == (unsigned)(a.splits - 1);
+            if (*flag)
+                atomicExch(a.count + unit, 0u);
+        }
+        __syncthreads();
+        if (!*flag || quarter >= RB)
+            return;
+        s = f32x4{0, 0, 0, 0};
+        for (int z = 0; z < a.splits; z++)
+            s += __builtin_bit_cast(
+                f32x4, __builtin_amdgcn_raw_buffer_load_b128(pr, z * kPart + at, 0, kCoherentBit));
+    }
+    if (quarter < RB && m < a.M && r < a.R) {
+        const float f = mine_id >= 0 ? a.scale[mine_id] * (a.xs ? a.xs[m] : 1.0f) : 0.0f;
         put_out(a, m, r, mine_id >= 0 ? s * f : f32x4{0, 0, 0, 0});
     }
 }
@@ -314,12 +354,31 @@ template <int W> __global__ __launch_bounds__(256) void adapter_shrink_few_kerne
 // Most tokens of the kernel above: it reads an adapter once per token.
 constexpr int64_t kFewTokens = 32;
 
-template <int X, int W, int RB> void go_shrink(const ShrinkArgs &a, hipStream_t st)
+// Workgroups that a product is split up to, fewest stages of a split's, and most
+// units (32 tokens by 16 ranks) that are split at all: each has an arrival
+// counter.
+constexpr int kSplitGroups = 512, kSplitStages = 2, kMaxUnits = 512;
+static_assert(kMaxUnits * 4 <= kAdapterCountBytes, "arrival counters");
+constexpr size_t kPartBytes = (size_t)2 * kSplitGroups * 512 * 4;
+
+// Splits of a product of `units` workgroups and `stages` stages each.
+int splits_of(int64_t units, int64_t stages)
+{
+    if (units > kMaxUnits)
+        return 1;
+    int64_t n = kSplitGroups / units;
+    n = n < stages / kSplitStages ? n : stages / kSplitStages;
+    return (int)(n < 1 ? 1 : n);
+}
+
+template <int X, int W, int RB> void go_shrink(ShrinkArgs a, hipStream_t st)
 {
     constexpr int kSize = X == X_I8 ? 1 : X == X_BF16 ? 2 : 4;
     constexpr int kStage = 32 * 512 + 16 * RB * (W == W_TERMS ? 3 : 1) * (W == X_F32 ? 4 : 2) * 512 / kSize;
     constexpr int kStages = kStage <= 26 * 1024 ? 3 : 2;
-    const dim3 grid((unsigned)((a.M + 31) / 32), (unsigned)((a.R + 16 * RB - 1) / (16 * RB)));
+    const int64_t blocks = (a.M + 31) / 32, groups = (a.R + 16 * RB - 1) / (16 * RB);
+    a.splits = splits_of(blocks * groups, (a.C * kSize + 511) / 512);
+    const dim3 grid((unsigned)blocks, (unsigned)groups, (unsigned)a.splits);
     hipLaunchKernelGGL((adapter_shrink_kernel<X, W, RB, kStages>), grid, dim3(512), 0, st, a);
 }
 
@@ -375,8 +434,8 @@ template <int QT> __global__ __launch_bounds__(256) void adapter_expand_kernel(E
             const bool ok = k < length;
             int pair = 0;
             if constexpr (QT != 0)
-                pair = (k >= R) + (k >= 2 * R) + (QT == 3 ? (k >= 3 * R) + (k >= 4 * R) + (k >= 5 * R) : 0);
-            const int r = k - pair * R + (QT == 3 ? pair_other(pair) * R : 0);
+                pair = (k >= R) + (k >= 2 * R);
+            const int r = k - pair * R;
             Frag<kTerms> pf, qf[4];
 #pragma unroll
             for (int t = 0; t < kTerms; t++)
@@ -385,8 +444,13 @@ template <int QT> __global__ __launch_bounds__(256) void adapter_expand_kernel(E
 #pragma unroll
             for (int b = 0; b < 4; b++) {
                 const int64_t c = c0 + 16 * b + lane % 16;
-                qf[b] = load_frag<QT == 0 ? X_F32 : X_BF16>(
-                    a.ad.q, ((int64_t)cur * a.C + c) * (QT == 3 ? 3 : 1) * R + r, ok && c < a.C);
+                if constexpr (QT == 3)
+                    qf[b].t[0] = load_frag<X_BF16>(
+                        a.ad.q, (((int64_t)cur * (a.C / 16) + c / 16) * steps + k0 / 32) * 512 + lane * 8,
+                        ok && c < a.C).t[0];
+                else
+                    qf[b] = load_frag<QT == 0 ? X_F32 : X_BF16>(a.ad.q, ((int64_t)cur * a.C + c) * R + r,
+                                                               ok && c < a.C);
             }
             __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
@@ -530,7 +594,7 @@ struct Slab {
 
 struct PrepArgs {
     const void *a, *b;      // [L, R, K], [L, N, R]
-    uint16_t *at, *bt;      // [L, K, terms, R], [terms, L, R, N]
+    uint16_t *at, *bt;
     int64_t N, K, M;
     int L, R, slabs;
     const int32_t *start;
@@ -538,13 +602,11 @@ struct PrepArgs {
     int32_t *first;         // [L + 1]: the first slab of each adapter
 };
 
-// One 32 x 32 tile of src [rows, cols] turned into dst: element (r, c) goes to
-// dst[c * pitch + r], as bf16; fp32 values as three terms, `plane` elements
-// apart.
-template <bool WB>
-__device__ __forceinline__ void transpose_tile(const void *src, int64_t s0, uint16_t *dst, int64_t rows,
-                                               int64_t cols, int64_t pitch, int64_t plane, int64_t r0,
-                                               int64_t c0)
+// One 32 x 32 tile of src [rows, cols], turned: put(c, r, bits or value) for
+// element (r, c), with neighbouring lanes at neighbouring r.
+template <bool WB, typename F>
+__device__ __forceinline__ void transpose_tile(const void *src, int64_t s0, int64_t rows, int64_t cols,
+                                               int64_t r0, int64_t c0, F put)
 {
     __shared__ uint32_t tile[32][33];
     const int x = threadIdx.x % 32, y = threadIdx.x / 32;
@@ -560,41 +622,59 @@ __device__ __forceinline__ void transpose_tile(const void *src, int64_t s0, uint
     __syncthreads();
 #pragma unroll
     for (int i = y; i < 32; i += 8)
-        if (c0 + i < cols && r0 + x < rows) {
-            uint16_t *to = dst + (c0 + i) * pitch + r0 + x;
-            if constexpr (WB) {
-                *to = (uint16_t)tile[x][i];
-            } else {
-                float v = __uint_as_float(tile[x][i]);
-#pragma unroll
-                for (int q = 0; q < 3; q++) {
-                    const uint32_t t = pack_bf16x2(v, 0.0f);
-                    to[q * plane] = (uint16_t)t;
-                    v = v - bf16_lo(t);
-                }
-            }
-        }
+        if (c0 + i < cols && r0 + x < rows)
+            put(c0 + i, r0 + x, tile[x][i]);
 }
 
 // What the backward kernels need first, in one launch: B transposed for the
 // product with dY, A for dX's epilogue (both then have the contraction index
-// contiguous), fp32 ones split into bf16 terms (B [3, L, R, N], A [L, K, 3, R]),
+// contiguous), fp32 ones split into bf16 terms (B [3, L, R, N]; A, per adapter,
+// as the six pairs' slots of its K columns in the layout of adapter_frag.hpp),
 // and the table of slabs.  Workgroup 0 of adapter 0 makes the table, 256
 // adapters at a time.
 template <bool WB> __global__ __launch_bounds__(256) void adapter_prep_kernel(PrepArgs p)
 {
-    constexpr int kTerms = WB ? 1 : 3;
     const int t = threadIdx.x;
     if (blockIdx.x > 0) {
         const int64_t rt = (p.R + 31) / 32, nt = (p.N + 31) / 32, l = blockIdx.y;
         const int64_t k = blockIdx.x - 1;
         const int64_t sb = l * p.N * p.R, sa = l * p.K * p.R;
-        if (k < rt * nt)
-            transpose_tile<WB>(p.b, sb, p.bt + sb, p.N, p.R, p.N, (int64_t)p.L * p.R * p.N, k / rt * 32,
-                               k % rt * 32);
-        else
-            transpose_tile<WB>(p.a, sa, p.at + sa * kTerms, p.R, p.K, (int64_t)kTerms * p.R, p.R,
-                               (k - rt * nt) % rt * 32, (k - rt * nt) / rt * 32);
+        if (k < rt * nt) {
+            const int64_t plane = (int64_t)p.L * p.R * p.N;
+            transpose_tile<WB>(p.b, sb, p.N, p.R, k / rt * 32, k % rt * 32,
+                               [&](int64_t r, int64_t n, uint32_t bits) {
+                                   uint16_t *to = p.bt + sb + r * p.N + n;
+                                   if constexpr (WB) {
+                                       *to = (uint16_t)bits;
+                                   } else {
+                                       float v = __uint_as_float(bits);
+#pragma unroll
+                                       for (int q = 0; q < 3; q++) {
+                                           const uint32_t w = pack_bf16x2(v, 0.0f);
+                                           to[q * plane] = (uint16_t)w;
+                                           v = v - bf16_lo(w);
+                                       }
+                                   }
+                               });
+        } else {
+            const int64_t r0 = (k - rt * nt) % rt * 32, c0 = (k - rt * nt) / rt * 32;
+            if constexpr (WB) {
+                transpose_tile<WB>(p.a, sa, p.R, p.K, r0, c0, [&](int64_t c, int64_t r, uint32_t bits) {
+                    p.at[sa + c * p.R + r] = (uint16_t)bits;
+                });
+            } else if (t < 128) {
+                // Eight ranks of a column per thread (the reads are coalesced
+                // over the columns).
+                const int64_t c = c0 + t % 32, r = r0 + t / 32 * 8;
+                if (c < p.K && r < p.R) {
+                    float v[8];
+#pragma unroll
+                    for (int e = 0; e < 8; e++)
+                        v[e] = static_cast<const float *>(p.a)[sa + (r + e) * p.K + c];
+                    put_pairs(p.at + l * (p.K / 16) * terms_steps(3, p.R) * 512, p.R, c, (int)r, v);
+                }
+            }
+        }
         return;
     }
     if (blockIdx.y > 0)
@@ -868,16 +948,24 @@ __global__ __launch_bounds__(256) void adapter_sum_kernel(const float *__restric
 
 } // namespace
 
-size_t adapter_terms_bytes(int64_t M, int64_t R, int qt)
+static size_t round256(size_t n) { return (n + 255) & ~(size_t)255; }
+
+// A forward call's workspace: partial sums, terms.
+size_t adapter_fwd_bytes(int64_t M, int64_t R)
 {
-    return (size_t)((M + 15) / 16) * terms_steps(qt, (int)R) * 1024;
+    const size_t terms = (size_t)((M + 15) / 16) * terms_steps(0, (int)R) * 1024;
+    return kPartBytes + terms;
 }
 
-void launch_adapter_u(const AdapterArgs &g, const int8_t *qx, const float *sx, float *u,
-                      uint16_t *terms, hipStream_t st)
+const uint16_t *launch_adapter_u(const AdapterArgs &g, const int8_t *qx, const float *sx, float *u,
+                                 unsigned *count, void *ws, hipStream_t st)
 {
-    const ShrinkArgs s{qx, sx, g.a, g.scale, g.ids, g.M, g.K, g.L, g.R, u, terms, g.bf16 ? 1 : 0};
+    char *w = static_cast<char *>(ws);
+    uint16_t *terms = reinterpret_cast<uint16_t *>(w + kPartBytes);
+    const ShrinkArgs s{qx, sx, g.a, g.scale, g.ids, g.M, g.K, g.L, g.R, u, terms, g.bf16 ? 1 : 0, 1,
+                       reinterpret_cast<float *>(w), count};
     g.bf16 ? run_shrink<X_I8, X_BF16>(s, st) : run_shrink<X_I8, X_F32>(s, st);
+    return terms;
 }
 
 void launch_adapter_expand(const AdapterEpilogue &ad, bool terms, int64_t M, int64_t C, float *out,
@@ -902,22 +990,21 @@ void launch_adapter_group(const int32_t *ids, int64_t M, int L, int32_t *order, 
 
 static int64_t slabs_of(int64_t M, int64_t L) { return M / kSlab + (M < L ? M : L); }
 
-static size_t round256(size_t n) { return (n + 255) & ~(size_t)255; }
-
 // Offsets of a backward call's workspace.
 struct BwdLayout {
-    size_t bt, at, v, terms, table, first, pa, pb, end;
+    size_t part, bt, at, v, terms, table, first, pa, pb, end;
 };
 
 static BwdLayout bwd_layout(int64_t M, int64_t N, int64_t K, int64_t L, int64_t R)
 {
     const size_t slabs = (size_t)slabs_of(M, L);
     BwdLayout o;
-    o.bt = 0;
+    o.part = 0;
+    o.bt = round256(o.part + kPartBytes);
     o.at = round256(o.bt + (size_t)L * R * N * 6);
-    o.v = round256(o.at + (size_t)L * R * K * 6);
+    o.v = round256(o.at + (size_t)L * (K / 16) * terms_steps(3, (int)R) * 1024);
     o.terms = round256(o.v + (size_t)M * R * 4);
-    o.table = round256(o.terms + adapter_terms_bytes(M, R, 3));
+    o.table = round256(o.terms + (size_t)((M + 15) / 16) * terms_steps(3, (int)R) * 1024);
     o.first = round256(o.table + slabs * sizeof(Slab));
     o.pa = round256(o.first + ((size_t)L + 1) * 4);
     o.pb = round256(o.pa + slabs * (size_t)R * K * 4);
@@ -931,7 +1018,7 @@ size_t adapter_bwd_bytes(int64_t M, int64_t N, int64_t K, int64_t L, int64_t R)
 }
 
 AdapterEpilogue launch_adapter_bwd_v(const AdapterArgs &g, const void *dy, bool dy_bf16,
-                                     const int32_t *start, void *ws, hipStream_t st)
+                                     const int32_t *start, unsigned *count, void *ws, hipStream_t st)
 {
     char *w = static_cast<char *>(ws);
     const BwdLayout o = bwd_layout(g.M, g.N, g.K, g.L, g.R);
@@ -946,7 +1033,8 @@ AdapterEpilogue launch_adapter_bwd_v(const AdapterArgs &g, const void *dy, bool 
         hipLaunchKernelGGL(adapter_prep_kernel<false>, grid, dim3(256), 0, st, p);
     const ShrinkArgs s{dy,  nullptr, w + o.bt, g.scale, g.ids, g.M, g.N,
                        g.L, g.R,     reinterpret_cast<float *>(w + o.v),
-                       reinterpret_cast<uint16_t *>(w + o.terms), g.bf16 ? 1 : 3};
+                       reinterpret_cast<uint16_t *>(w + o.terms), g.bf16 ? 1 : 3, 1,
+                       reinterpret_cast<float *>(w + o.part), count};
     if (g.M > 0) {
         if (dy_bf16)
             g.bf16 ? run_shrink<X_BF16, X_BF16>(s, st) : run_shrink<X_BF16, W_TERMS>(s, st);

@@ -123,8 +123,8 @@ constexpr int terms_steps(int qt, int R)
 }
 
 // Term of p in pair i of six (of the other operand: pair_other).
-__device__ __forceinline__ int pair_term(int i) { return (0x001012 >> (4 * i)) & 3; }
-__device__ __forceinline__ int pair_other(int i) { return (0x010210 >> (4 * i)) & 3; }
+__host__ __device__ constexpr int pair_term(int i) { return (0x001012 >> (4 * i)) & 3; }
+__host__ __device__ constexpr int pair_other(int i) { return (0x010210 >> (4 * i)) & 3; }
 
 // Where slot k of a row lies among the rows' terms.
 __device__ __forceinline__ int64_t term_at(int steps, int64_t row, int k)
@@ -170,6 +170,17 @@ __device__ __forceinline__ void put_terms(uint16_t *terms, int qt, int R, int64_
                     put(i * R + r);
         }
     }
+}
+
+// Writes eight values of the other operand's three terms into the slots of the
+// six pairs (QT = 3): column c, ranks r .. r + 7.
+__device__ __forceinline__ void put_pairs(uint16_t *terms, int R, int64_t c, int r, const float (&v)[8])
+{
+    const int steps = terms_steps(3, R);
+    const Frag<3> f = split8(v);
+#pragma unroll
+    for (int i = 0; i < 6; i++)
+        *reinterpret_cast<bf16x8 *>(terms + term_at(steps, c, i * R + r)) = f.t[pair_other(i)];
 }
 
 } // namespace

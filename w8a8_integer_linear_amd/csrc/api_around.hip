@@ -135,12 +135,29 @@ int qlin_rmsnorm_bwd(const void *dn, int dn_dtype, const void *h, const void *dr
     return finish();
 }
 
+// Where the parts of an adapter call's workspace lie: both kinds of arrival
+// counters first, at the same places for every call and shape (so that one
+// workspace serves them all), then the product's sums, then the adapters' part.
+struct AdapterWs {
+    unsigned *count;
+    char *product, *rest;
+};
+static size_t product_part(int op, int64_t M, int64_t N, int64_t K)
+{
+    const size_t n = qlin_product_ws_bytes(op, M, N, K);
+    return qlin::kAdapterCountBytes + round256(n > qlin::kSplitCountBytes ? n : qlin::kSplitCountBytes);
+}
+static AdapterWs parts_of(void *workspace, int op, int64_t M, int64_t N, int64_t K)
+{
+    char *w = static_cast<char *>(workspace);
+    return {static_cast<unsigned *>(workspace), w + qlin::kAdapterCountBytes, w + product_part(op, M, N, K)};
+}
+
 size_t qlin_adapter_fwd_ws_bytes(int64_t M, int64_t N, int64_t K, int64_t L, int64_t R)
 {
     if (!adapter_shape_ok(M, N, K, L, R) || K > QLIN_MAX_CONTRACTION)
         return 0;
-    return round256(qlin_product_ws_bytes(QLIN_OP_FWD, M, N, K)) +
-           qlin::adapter_terms_bytes(M, R, 0);
+    return product_part(QLIN_OP_FWD, M, N, K) + qlin::adapter_fwd_bytes(M, R);
 }
 
 int qlin_adapter_fwd(const int8_t *qx, const float *sx, const int8_t *qw, const float *sw,
@@ -172,12 +189,11 @@ int qlin_adapter_fwd(const int8_t *qx, const float *sx, const int8_t *qw, const 
         return QLIN_EINVAL;
     const hipStream_t s = as_stream(stream);
     qlin::ProductArgs p{QLIN_OP_FWD, qx, qw, M, N, K, sx, sw, bias, y, false};
-    const size_t pw = qlin_product_ws_bytes(QLIN_OP_FWD, M, N, K);
-    if (pw)
-        p.split_ws = workspace;
-    uint16_t *terms = reinterpret_cast<uint16_t *>(static_cast<char *>(workspace) + round256(pw));
+    const AdapterWs w = parts_of(workspace, QLIN_OP_FWD, M, N, K);
+    if (qlin_product_ws_bytes(QLIN_OP_FWD, M, N, K))
+        p.split_ws = w.product;
     const qlin::AdapterArgs g{a, b, w_dtype == QLIN_BF16, scale, ids, M, N, K, (int)L, (int)R};
-    qlin::launch_adapter_u(g, qx, sx, u, terms, s);
+    const uint16_t *terms = qlin::launch_adapter_u(g, qx, sx, u, w.count, w.rest, s);
     qlin::launch_product_adapter(p, {u, terms, b, ids, (int)L, (int)R, g.bf16}, s);
     return finish();
 }
@@ -201,8 +217,7 @@ size_t qlin_adapter_bwd_ws_bytes(int64_t M, int64_t N, int64_t K, int64_t L, int
 {
     if (!adapter_shape_ok(M, N, K, L, R) || N > QLIN_MAX_CONTRACTION || L > QLIN_MAX_ADAPTERS)
         return 0;
-    return round256(qlin_product_ws_bytes(QLIN_OP_DX, M, N, K)) +
-           qlin::adapter_bwd_bytes(M, N, K, L, R);
+    return product_part(QLIN_OP_DX, M, N, K) + qlin::adapter_bwd_bytes(M, N, K, L, R);
 }
 
 int qlin_adapter_bwd(const void *dy, int dy_dtype, const int8_t *qg1, const float *sg1,
@@ -241,22 +256,21 @@ int qlin_adapter_bwd(const void *dy, int dy_dtype, const int8_t *qg1, const floa
     if (clash(out, in))
         return QLIN_EINVAL;
     const hipStream_t s = as_stream(stream);
-    const size_t pw = qlin_product_ws_bytes(QLIN_OP_DX, M, N, K);
-    void *aw = static_cast<char *>(workspace) + round256(pw);
+    const AdapterWs w = parts_of(workspace, QLIN_OP_DX, M, N, K);
     const qlin::AdapterArgs g{a, b, w_dtype == QLIN_BF16, scale, ids, M, N, K, (int)L, (int)R};
     const qlin::AdapterEpilogue va =
-        qlin::launch_adapter_bwd_v(g, dy, dy_dtype == QLIN_BF16, start, aw, s);
+        qlin::launch_adapter_bwd_v(g, dy, dy_dtype == QLIN_BF16, start, w.count, w.rest, s);
     if (any && dx) {
         qlin::ProductArgs p{QLIN_OP_DX, qg1, qw, M, N, K, sg1, nullptr, nullptr, dx, false};
-        if (pw)
-            p.split_ws = workspace;
+        if (qlin_product_ws_bytes(QLIN_OP_DX, M, N, K))
+            p.split_ws = w.product;
         p.had = had_block;
         p.had_scale = had_block ? hadamard_scale(had_block) : 1.0f;
         qlin::launch_product_adapter(p, va, s);
         if (had_block > 128)
             qlin::launch_hadamard(dx, false, M, K, had_block, hadamard_scale(had_block), dx, s);
     }
-    qlin::launch_adapter_bwd_w(g, dy, dy_dtype == QLIN_BF16, qx, sx, u, order, da, db, aw, s);
+    qlin::launch_adapter_bwd_w(g, dy, dy_dtype == QLIN_BF16, qx, sx, u, order, da, db, w.rest, s);
     return finish();
 }
 

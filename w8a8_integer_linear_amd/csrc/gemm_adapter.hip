@@ -2,8 +2,6 @@
 // token's adapter is added to the outputs before they are first written, so
 // the adapters cost no pass over y or dx (reading and writing y once more took
 // 72 us of 546 at 12000 x 5376 -> 7168).
-#include <stdlib.h>
-
 #include "gemm_kernel.hpp"
 
 namespace qlin {
@@ -43,9 +41,11 @@ void launch_product_adapter(const ProductArgs &a, const AdapterEpilogue &ad, hip
     }
     GemmParams p = gemm_params(a);
     p.ad = ad;
-    // (Diagnostic switch, to be replaced by a rule.)
-    static const int cut = getenv("QCUT") ? atoi(getenv("QCUT")) : 128;
-    if (((p.R + 255) / 256) * ((p.S + 255) / 256) < cut) {
+    // Few tiles: added in the epilogues, the term would be the work of as few
+    // compute units (333 tokens, 4096 x 4096, rank 64 in fp32: 147 us for the
+    // backward call against 125 us with the term in a launch of its own; 611
+    // tokens, 4096 -> 14336, rank 32, 168 tiles: 72 us against 90 us).
+    if (((p.R + 255) / 256) * ((p.S + 255) / 256) < 128) {
         ProductArgs b = a;
         b.had = 0;
         launch_product(b, st);

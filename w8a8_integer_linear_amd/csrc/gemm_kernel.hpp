@@ -647,7 +647,7 @@ template <int QT, int FM, int FN> struct AdapterTerm {
     // Row blocks between the load of p's values and their use (the scheduler
     // would otherwise load all of them at once; with a split q they would not
     // fit the registers).
-    static constexpr int kAhead = QT == 0 ? 1 : FM - 1;
+    static constexpr int kAhead = QT == 0 ? 0 : FM - 1;
     static constexpr int kTerms = QT == 0 ? 3 : 1;  // of p and q per step
     using F = Frag<kTerms>;
     const GemmParams &p;
@@ -676,16 +676,6 @@ template <int QT, int FM, int FN> struct AdapterTerm {
         }
     }
 
-    // Where the lane's eight slots of the step lie in a row of q.
-    __device__ __forceinline__ int q_slot() const
-    {
-        const int R = p.ad.R, k = k0 + 8 * (lane / 16);
-        if constexpr (QT == 0)
-            return k;
-        const int pair = (k >= R) + (k >= 2 * R) + (QT == 3 ? (k >= 3 * R) + (k >= 4 * R) + (k >= 5 * R) : 0);
-        return k - pair * R + (QT == 3 ? pair_other(pair) * R : 0);
-    }
-
     // (Slots past the end meet zeros in q; p's are then the step's first ones.)
     __device__ __forceinline__ F p_frag(int a) const
     {
@@ -703,14 +693,25 @@ template <int QT, int FM, int FN> struct AdapterTerm {
     // Loads the step's column operands and the first rows'.
     __device__ __forceinline__ void load()
     {
-        constexpr int W = QT == 0 ? X_F32 : X_BF16;
-        const int64_t per = (QT == 3 ? 3 : 1) * p.ad.R;
-        const bool ok = k0 + 8 * (lane / 16) < length;
-        const int r = q_slot();
+        const int R = p.ad.R, k = k0 + 8 * (lane / 16);
+        const bool ok = k < length;
+        if constexpr (QT == 3) {
+            // (q's terms in the same layout as p's, a block of 16 columns each.)
+            const int steps = terms_steps(3, R);
 #pragma unroll
-        for (int b = 0; b < FN; b++) {
-            const int col = j + 16 * b + lane % 16;
-            q[b] = load_frag<W>(p.ad.q, ((int64_t)cur * p.S + col) * per + r, ok && col < p.S);
+            for (int b = 0; b < FN; b++) {
+                const int block = j + 16 * b < p.S ? j / 16 + b : 0;
+                const int64_t step = ((int64_t)cur * (p.S / 16) + block) * steps + k0 / 32;
+                q[b].t[0] = load_frag<X_BF16>(p.ad.q, step * 512 + lane * 8, ok).t[0];
+            }
+        } else {
+            const int r = QT == 0 ? k : k - ((k >= R) + (k >= 2 * R)) * R;
+#pragma unroll
+            for (int b = 0; b < FN; b++) {
+                const int col = j + 16 * b + lane % 16;
+                q[b] = load_frag<QT == 0 ? X_F32 : X_BF16>(p.ad.q, ((int64_t)cur * p.S + col) * R + r,
+                                                          ok && col < p.S);
+            }
         }
 #pragma unroll
         for (int a = 0; a < kAhead; a++)

@@ -54,7 +54,7 @@ void launch_product(const ProductArgs &p, hipStream_t st);
 
 // The low-rank term of a product's output row i: sum_r p[i, r] q[ids[i], j, r]
 // with p [rows, R] fp32 and q [L, cols, R] bf16 or, in the forward product, fp32;
-// the dX product takes an fp32 q as three bf16 terms, [L, cols, 3, R].  terms
+// the dX product takes an fp32 q as bf16 terms, as adapter_prep_kernel makes them.  terms
 // holds p as such terms, in the layout of adapter_frag.hpp (the forward product
 // of 16 rows or fewer reads p instead).
 struct AdapterEpilogue {
@@ -156,11 +156,13 @@ struct AdapterArgs {
     int64_t M, N, K;
     int L, R;
 };
-// u = scale x^ A^T; terms: u as bf16 terms, adapter_terms_bytes of them, for a
-// q of form qt (1: bf16, 0: fp32, 3: three bf16 terms).
-size_t adapter_terms_bytes(int64_t M, int64_t R, int qt);
-void launch_adapter_u(const AdapterArgs &g, const int8_t *qx, const float *sx, float *u,
-                      uint16_t *terms, hipStream_t st);
+// u = scale x^ A^T, with a workspace of adapter_fwd_bytes and kAdapterCountBytes of
+// arrival counters (zero before and after); the result is u as bf16 terms, in the
+// workspace.
+constexpr size_t kAdapterCountBytes = 4096;
+size_t adapter_fwd_bytes(int64_t M, int64_t R);
+const uint16_t *launch_adapter_u(const AdapterArgs &g, const int8_t *qx, const float *sx, float *u,
+                                 unsigned *count, void *ws, hipStream_t st);
 void launch_adapter_group(const int32_t *ids, int64_t M, int L, int32_t *order, int32_t *start,
                           hipStream_t st);
 // Backward, with a workspace of adapter_bwd_bytes: v = scale dY B (kept in
@@ -168,7 +170,7 @@ void launch_adapter_group(const int32_t *ids, int64_t M, int L, int32_t *order, 
 // product), then both adapter gradients.
 size_t adapter_bwd_bytes(int64_t M, int64_t N, int64_t K, int64_t L, int64_t R);
 AdapterEpilogue launch_adapter_bwd_v(const AdapterArgs &g, const void *dy, bool dy_bf16,
-                                     const int32_t *start, void *ws, hipStream_t st);
+                                     const int32_t *start, unsigned *count, void *ws, hipStream_t st);
 void launch_adapter_bwd_w(const AdapterArgs &g, const void *dy, bool dy_bf16, const int8_t *qx,
                           const float *sx, const float *u, const int32_t *order, float *da,
                           float *db, void *ws, hipStream_t st);
