@@ -45,6 +45,13 @@ __device__ __forceinline__ float row_reduce(float v, float *red, Op op)
     return v;
 }
 
+// Stores of what nothing reads soon (h, y): cached, they would push the codes,
+// which the products read next, out of the infinity cache.
+template <typename V> __device__ __forceinline__ void store_once(void *p, V v)
+{
+    __builtin_nontemporal_store(v, static_cast<V *>(p));
+}
+
 struct NormArgs {
     const void *x, *res;
     int64_t rows, cols;
@@ -91,6 +98,20 @@ __global__ __launch_bounds__(WPR > 4 ? WPR *kWave : 4 * kWave) void rmsnorm_quan
             rr[j] = load_raw8<BF16>(a.res, base + cc * 8);
         }
     }
+    // gamma is loaded before h is stored: a load's wait includes the stores
+    // issued before it.  (Rows of 1024 threads have no registers for it.)
+    constexpr bool kEarly = WPR <= 4;
+    Raw8<false> gr[kEarly ? J : 1];
+    auto gamma_at = [&](int j) {
+        const int64_t c = chunk(j);
+        return load_raw8<false>(a.gamma, (c < nch ? c : nch - 1) * 8);
+    };
+    if constexpr (kEarly) {
+#pragma unroll
+        for (int j = 0; j < J; j++)
+            gr[j] = gamma_at(j);
+        __builtin_amdgcn_sched_barrier(0);
+    }
     float v[J][8];
     float ss = 0.0f;
 #pragma unroll
@@ -109,7 +130,7 @@ __global__ __launch_bounds__(WPR > 4 ? WPR *kWave : 4 * kWave) void rmsnorm_quan
                 // backward pass, which reads h, sees the same values.
                 const i32x4 w = pack_bf16x8(v[j]);
                 if (ok)
-                    *reinterpret_cast<i32x4 *>(static_cast<uint16_t *>(a.h) + base + c * 8) = w;
+                    store_once(static_cast<uint16_t *>(a.h) + base + c * 8, w);
                 unpack8<true>(Raw8<true>{w}, v[j]);
             } else if (ok) {
                 store8(static_cast<float *>(a.h), base + c * 8, v[j]);
@@ -126,9 +147,8 @@ __global__ __launch_bounds__(WPR > 4 ? WPR *kWave : 4 * kWave) void rmsnorm_quan
     float amax = 0.0f;
 #pragma unroll
     for (int j = 0; j < J; j++) {
-        const int64_t c = chunk(j), cc = c < nch ? c : nch - 1;
         float gm[8];
-        load8<false>(a.gamma, cc * 8, gm);
+        unpack8<false>(kEarly ? gr[kEarly ? j : 0] : gamma_at(j), gm);
 #pragma unroll
         for (int e = 0; e < 8; e++)
             v[j][e] = (v[j][e] * rstd) * gm[e];
@@ -181,7 +201,7 @@ __global__ __launch_bounds__(WPR > 4 ? WPR *kWave : 4 * kWave) void rmsnorm_quan
 #pragma unroll
                 for (int e = 0; e < 8; e++)
                     f[e] = f[e] * sc;
-                *reinterpret_cast<i32x4 *>(a.y + base + c * 8) = pack_bf16x8(f);
+                store_once(a.y + base + c * 8, pack_bf16x8(f));
             }
         }
     }
@@ -242,7 +262,7 @@ struct NormBwdArgs {
 
 // One row at a time over 256 threads, J chunks per lane.
 template <bool DNBF, bool BF16, int J>
-__global__ __launch_bounds__(256) void rmsnorm_bwd_kernel(NormBwdArgs a)
+__global__ __launch_bounds__(256, J <= 3 ? 3 : 2) void rmsnorm_bwd_kernel(NormBwdArgs a)
 {
     __shared__ float red[2][4];
     const int t = threadIdx.x;
@@ -415,8 +435,9 @@ __global__ __launch_bounds__(1024) void rmsnorm_dgamma_sum_kernel(const float *_
 
 // Longest row of the one-pass kernel.
 constexpr int64_t kOnePassCols = 256 * 8 * 4;
-// Workgroups that walk the rows, each with its own partial column sums.
-constexpr int kBwdGrid = 768;
+// Workgroups that walk the rows, each with its own partial column sums: as many
+// as are resident at once.
+constexpr int bwd_grid(int64_t cols) { return cols <= 3 * 2048 ? 768 : 512; }
 
 template <bool DNBF, bool BF16>
 void run_bwd(const NormBwdArgs &a, int n, hipStream_t st)
@@ -453,7 +474,7 @@ void launch_rmsnorm_quant(const void *x, const void *res, bool bf16, int64_t row
 // Rows of partial column sums that a backward call writes.
 int rmsnorm_bwd_parts(int64_t rows, int64_t cols)
 {
-    const int64_t most = cols <= kOnePassCols ? kBwdGrid : 64;
+    const int64_t most = cols <= kOnePassCols ? bwd_grid(cols) : 64;
     return (int)(rows < most ? rows : most);
 }
 
