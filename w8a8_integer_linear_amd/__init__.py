@@ -13,4 +13,5 @@ from ._native import (  # noqa: F401
     qlin_quantize_cols, qlin_quantize_grad, qlin_quantize_rows, qlin_rmsnorm_bwd,
     qlin_rmsnorm_bwd_ws_bytes, qlin_rmsnorm_quant, qlin_sgd_requant, qlin_stream_copy, qlin_wn_init,
     qlin_wn_sgd_requant)
+from .adapters import AdaptedLinearW8A8, pack_adapters  # noqa: F401
 from .layer import LinearW8A8Training  # noqa: F401
