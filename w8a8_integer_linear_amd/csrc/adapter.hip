@@ -428,37 +428,49 @@ template <int QT> __global__ __launch_bounds__(256) void adapter_expand_kernel(E
     }
     constexpr int kTerms = QT == 0 ? 3 : 1;
     const int length = (QT == 0 ? 1 : QT == 1 ? 3 : 6) * R, steps = terms_steps(QT, R);
+    struct Step {
+        Frag<kTerms> p, q[4];
+    };
     for_adapters(id, [&](int cur, bool mine) {
-        for (int k0 = 0; k0 < length; k0 += 32) {
+        auto load = [&](int k0) {
             const int k = k0 + 8 * (lane / 16);
             const bool ok = k < length;
-            int pair = 0;
-            if constexpr (QT != 0)
-                pair = (k >= R) + (k >= 2 * R);
-            const int r = k - pair * R;
-            Frag<kTerms> pf, qf[4];
+            const int r = QT == 1 ? k - ((k >= R) + (k >= 2 * R)) * R : k;
+            Step f;
 #pragma unroll
             for (int t = 0; t < kTerms; t++)
-                pf.t[t] = load_frag<X_BF16>(
+                f.p.t[t] = load_frag<X_BF16>(
                     a.ad.terms, (((int64_t)blockIdx.y * steps + k0 / 32 * kTerms + t) * 64 + lane) * 8, ok).t[0];
 #pragma unroll
             for (int b = 0; b < 4; b++) {
                 const int64_t c = c0 + 16 * b + lane % 16;
                 if constexpr (QT == 3)
-                    qf[b].t[0] = load_frag<X_BF16>(
+                    f.q[b].t[0] = load_frag<X_BF16>(
                         a.ad.q, (((int64_t)cur * (a.C / 16) + c / 16) * steps + k0 / 32) * 512 + lane * 8,
                         ok && c < a.C).t[0];
                 else
-                    qf[b] = load_frag<QT == 0 ? X_F32 : X_BF16>(a.ad.q, ((int64_t)cur * a.C + c) * R + r,
-                                                               ok && c < a.C);
+                    f.q[b] = load_frag<QT == 0 ? X_F32 : X_BF16>(
+                        a.ad.q, ((int64_t)cur * a.C + c) * R + r, ok && c < a.C);
             }
-            __builtin_amdgcn_sched_barrier(0);
+            return f;
+        };
+        auto use = [&](const Step &f) {
 #pragma unroll
             for (int b = 0; b < 4; b++) {
-                const f32x4 t = mfma(qf[b], pf, acc[b]);
+                const f32x4 t = mfma(f.q[b], f.p, acc[b]);
                 acc[b] = mine ? t : acc[b];
             }
+        };
+        // Two steps at a time, so that their loads are in flight together.
+        int k0 = 0;
+        for (; k0 + 32 < length; k0 += 64) {
+            const Step f0 = load(k0), f1 = load(k0 + 32);
+            __builtin_amdgcn_sched_barrier(0);
+            use(f0);
+            use(f1);
         }
+        if (k0 < length)
+            use(load(k0));
     });
     if (id < 0)
         return;
@@ -759,18 +771,19 @@ template <int COLS> struct TokenTile {
 // the way; the next ones' loads are in flight meanwhile.  The read of x bounds
 // it.
 template <int X, bool TRANS, int RB>
-__global__ __launch_bounds__(256) void adapter_outer_kernel(OuterArgs a)
+__device__ __forceinline__ void outer_product(const OuterArgs &a, int column_block, uint16_t *smem)
 {
     constexpr int XT = terms_of(X);
     using XTile = TokenTile<256>;
     using PTile = TokenTile<RB * 16>;
-    __shared__ __attribute__((aligned(16))) uint16_t xs[XT][XTile::kSize];
-    __shared__ __attribute__((aligned(16))) uint16_t ps[3][PTile::kSize];
+    uint16_t(&xs)[XT][XTile::kSize] = *reinterpret_cast<uint16_t(*)[XT][XTile::kSize]>(smem);
+    uint16_t(&ps)[3][PTile::kSize] =
+        *reinterpret_cast<uint16_t(*)[3][PTile::kSize]>(smem + XT * XTile::kSize);
     const Slab s = a.table[blockIdx.y];
     if (s.rows <= 0)
         return;
     const int t = threadIdx.x, w = t / kWave, lane = __lane_id();
-    const int64_t c0 = (int64_t)blockIdx.x * 256;
+    const int64_t c0 = (int64_t)column_block * 256;
     f32x4 acc[4][RB];
 #pragma unroll
     for (int b = 0; b < 4; b++)
@@ -907,17 +920,31 @@ __global__ __launch_bounds__(256) void adapter_outer_kernel(OuterArgs a)
         }
 }
 
-template <int X, bool TRANS> void run_outer(const OuterArgs &a, int slabs, hipStream_t st)
+// Both gradients in one launch: the first `blocks` column blocks are A's (from
+// the INT8 codes), the others B's (from dY, of type X).
+template <int X, int RB>
+__global__ __launch_bounds__(256) void adapter_outer_kernel(OuterArgs a, OuterArgs b, int blocks)
 {
-    const dim3 grid((unsigned)((a.C + 255) / 256), (unsigned)slabs), block(256);
-    if (a.R <= 16)
-        hipLaunchKernelGGL((adapter_outer_kernel<X, TRANS, 1>), grid, block, 0, st, a);
-    else if (a.R <= 32)
-        hipLaunchKernelGGL((adapter_outer_kernel<X, TRANS, 2>), grid, block, 0, st, a);
-    else if (a.R <= 64)
-        hipLaunchKernelGGL((adapter_outer_kernel<X, TRANS, 4>), grid, block, 0, st, a);
+    __shared__ __attribute__((aligned(16)))
+    uint16_t smem[terms_of(X) * TokenTile<256>::kSize + 3 * TokenTile<RB * 16>::kSize];
+    if ((int)blockIdx.x < blocks)
+        outer_product<X_I8, false, RB>(a, blockIdx.x, smem);
     else
-        hipLaunchKernelGGL((adapter_outer_kernel<X, TRANS, 8>), grid, block, 0, st, a);
+        outer_product<X, true, RB>(b, blockIdx.x - blocks, smem);
+}
+
+template <int X> void run_outer(const OuterArgs &a, const OuterArgs &b, int slabs, hipStream_t st)
+{
+    const int blocks = (int)((a.C + 255) / 256);
+    const dim3 grid((unsigned)(blocks + (b.C + 255) / 256), (unsigned)slabs), block(256);
+    if (a.R <= 16)
+        hipLaunchKernelGGL((adapter_outer_kernel<X, 1>), grid, block, 0, st, a, b, blocks);
+    else if (a.R <= 32)
+        hipLaunchKernelGGL((adapter_outer_kernel<X, 2>), grid, block, 0, st, a, b, blocks);
+    else if (a.R <= 64)
+        hipLaunchKernelGGL((adapter_outer_kernel<X, 4>), grid, block, 0, st, a, b, blocks);
+    else
+        hipLaunchKernelGGL((adapter_outer_kernel<X, 8>), grid, block, 0, st, a, b, blocks);
 }
 
 // out[l] = the sum of l's slabs, in order; zeros for an adapter without tokens.
@@ -1055,9 +1082,9 @@ void launch_adapter_bwd_w(const AdapterArgs &g, const void *dy, bool dy_bf16, co
     float *pa = reinterpret_cast<float *>(w + o.pa), *pb = reinterpret_cast<float *>(w + o.pb);
     const float *v = reinterpret_cast<const float *>(w + o.v);
     if (g.M > 0) {
-        run_outer<X_I8, false>(OuterArgs{v, sx, qx, order, table, g.M, g.K, g.R, pa}, slabs, st);
+        const OuterArgs a{v, sx, qx, order, table, g.M, g.K, g.R, pa};
         const OuterArgs b{u, nullptr, dy, order, table, g.M, g.N, g.R, pb};
-        dy_bf16 ? run_outer<X_BF16, true>(b, slabs, st) : run_outer<X_F32, true>(b, slabs, st);
+        dy_bf16 ? run_outer<X_BF16>(a, b, slabs, st) : run_outer<X_F32>(a, b, slabs, st);
     }
     const int64_t sa = (int64_t)g.R * g.K, sb = (int64_t)g.R * g.N;
     hipLaunchKernelGGL(adapter_sum_kernel, dim3((unsigned)((sa + 1023) / 1024 + (sb + 1023) / 1024), (unsigned)g.L),
