@@ -484,13 +484,13 @@ template <int QT> __global__ __launch_bounds__(256) void adapter_expand_kernel(E
 
 // ------------------------------------------------------- grouping of tokens
 
-// A stable counting sort of the tokens by adapter, in one workgroup: each of 8
+// A stable counting sort of the tokens by adapter, in one workgroup: each of 16
 // waves counts its own run of tokens, the counts become first places (adapter
 // by adapter, and for one adapter wave by wave), and each wave places its
 // tokens 64 at a time, one adapter among them after another.  Tokens without
 // an adapter come last.  The reads' latency is what takes the time: a wave
 // loads 512 tokens' adapters at once.
-constexpr int kGroupWaves = 8;
+constexpr int kGroupWaves = 16;
 
 __global__ __launch_bounds__(kGroupWaves *kWave) void adapter_group_kernel(const int32_t *__restrict__ ids,
                                                                            int64_t M, int L,
@@ -506,11 +506,10 @@ __global__ __launch_bounds__(kGroupWaves *kWave) void adapter_group_kernel(const
     const int64_t per = ((M + kGroupWaves * kWave - 1) / (kGroupWaves * kWave)) * kWave;
     const int64_t r0 = w * per < M ? w * per : M, r1 = r0 + per < M ? r0 + per : M;
     // f(m, bin, mask, n) for each adapter among 64 tokens of the wave's run; of
-    // 512 tokens with one adapter f is called at once, with a full mask and n =
-    // 8 groups of 64.  (The eight groups go through LDS so that the loop over
-    // them stays rolled: fetching unrolled code once costs more than running
-    // it.)
-    constexpr int kAtOnce = 8;
+    // 768 tokens with one adapter f is called at once, with a full mask and n =
+    // 12 groups of 64.  (The groups go through LDS so that the loop over them
+    // stays rolled: fetching unrolled code once costs more than running it.)
+    constexpr int kAtOnce = 12;
     __shared__ int16_t seen[kGroupWaves][kAtOnce * kWave];
     auto for_runs = [&](auto f) {
         for (int64_t m0 = r0; m0 < r1; m0 += kAtOnce * kWave) {

@@ -260,6 +260,9 @@ int qlin_adapter_bwd(const void *dy, int dy_dtype, const int8_t *qg1, const floa
     const qlin::AdapterArgs g{a, b, w_dtype == QLIN_BF16, scale, ids, M, N, K, (int)L, (int)R};
     const qlin::AdapterEpilogue va =
         qlin::launch_adapter_bwd_v(g, dy, dy_dtype == QLIN_BF16, start, w.count, w.rest, s);
+    // The adapters' gradients come before the product: they read dY again, while
+    // the product with B has just left what fits of it in the infinity cache.
+    qlin::launch_adapter_bwd_w(g, dy, dy_dtype == QLIN_BF16, qx, sx, u, order, da, db, w.rest, s);
     if (any && dx) {
         qlin::ProductArgs p{QLIN_OP_DX, qg1, qw, M, N, K, sg1, nullptr, nullptr, dx, false};
         if (qlin_product_ws_bytes(QLIN_OP_DX, M, N, K))
@@ -270,7 +273,6 @@ int qlin_adapter_bwd(const void *dy, int dy_dtype, const int8_t *qg1, const floa
         if (had_block > 128)
             qlin::launch_hadamard(dx, false, M, K, had_block, hadamard_scale(had_block), dx, s);
     }
-    qlin::launch_adapter_bwd_w(g, dy, dy_dtype == QLIN_BF16, qx, sx, u, order, da, db, w.rest, s);
     return finish();
 }
 
