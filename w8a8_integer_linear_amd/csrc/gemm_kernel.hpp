@@ -655,13 +655,33 @@ template <int QT, int FM, int FN> struct AdapterTerm {
     int id[FM], cur, k0;
     F f[kAhead + 1], q[FN];
 
-    // Loads the rows' adapters.
-    __device__ __forceinline__ AdapterTerm(const GemmParams &p, int i, int j)
+    // The adapter that all the rows have (-1: none), or kMixed.  Found before the
+    // main loop, it saves the epilogue one trip to memory before it knows which
+    // columns' operands to load.
+    static constexpr int kMixed = -2;
+    __device__ static __forceinline__ int common(const GemmParams &p, int i)
+    {
+        const int lane = __lane_id();
+        int first = -1;
+        bool same = true;
+#pragma unroll
+        for (int a = 0; a < FM; a++) {
+            const int row = i + 16 * a + lane % 16, id = id_of(p.ad.ids, row, p.R, p.ad.L);
+            if (a == 0)
+                first = __builtin_amdgcn_readfirstlane(id);
+            same = same && (id == first || row >= p.R);
+        }
+        return __all(same) ? first : kMixed;
+    }
+
+    // (Rows past the end may be counted to the common adapter: they are never
+    // stored.)
+    __device__ __forceinline__ AdapterTerm(const GemmParams &p, int i, int j, int common)
         : p(p), i(i), j(j), lane(__lane_id()), length((QT == 0 ? 1 : QT == 1 ? 3 : 6) * p.ad.R)
     {
 #pragma unroll
         for (int a = 0; a < FM; a++)
-            id[a] = id_of(p.ad.ids, i + 16 * a + lane % 16, p.R, p.ad.L);
+            id[a] = common != kMixed ? common : id_of(p.ad.ids, i + 16 * a + lane % 16, p.R, p.ad.L);
     }
 
     __device__ __forceinline__ void next()
@@ -824,6 +844,9 @@ __global__ __launch_bounds__(WM *WN * 64, 1) void gemm_kernel(GemmParams p)
     const int lane = __lane_id();
     const int w = threadIdx.x / kWave;
     const int wi = w / WN, wj = w % WN;
+    int common = -1;
+    if constexpr (kAdapter)
+        common = AdapterTerm<kQ, FM, FN>::common(p, i0 + wi * RW);
     const int8_t *abase = AKM ? p.a + i0 : p.a + (int64_t)i0 * p.lda;
     const int8_t *bbase = BKM ? p.b + j0 : p.b + (int64_t)j0 * p.ldb;
     const int alim = p.R - i0, blim = p.S - j0;
@@ -1089,7 +1112,7 @@ __global__ __launch_bounds__(WM *WN * 64, 1) void gemm_kernel(GemmParams p)
     f32x4 val[kAdapter ? FM : 1][FN];
     if constexpr (kAdapter) {
         // The term's first loads are in flight during the dequantization.
-        AdapterTerm<kQ, FM, FN> term(p, i0 + wi * RW, j0 + wj * CW);
+        AdapterTerm<kQ, FM, FN> term(p, i0 + wi * RW, j0 + wj * CW, common);
         term.begin();
         __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
