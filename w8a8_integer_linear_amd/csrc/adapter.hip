@@ -406,13 +406,18 @@ struct ExpandArgs {
     AdapterEpilogue ad;
     int64_t M, C;
     float *out;             // [M, C], added to
+    int had;                // rotation block of the sums (up to 128), or 0
+    float cb;
 };
 
 // out[m, c] += sum_r p[m, r] q[id, c, r], for products of so few tiles that
 // adding the term in their epilogues would leave it to a few compute units: 16
 // tokens and 64 columns per wave.  QT as in the epilogues: q as one bf16 term, as
-// three, or fp32.
-template <int QT> __global__ __launch_bounds__(256) void adapter_expand_kernel(ExpandArgs a)
+// three, or fp32.  ROTATE: the sums go through LDS and are rotated in blocks along
+// their rows before they are written (the rotation of dX, which the product's
+// own epilogue cannot do before the term is added; a launch of its own cost 5 us
+// of 107 at 333 tokens, 4096 x 4096, rank 64 in fp32).
+template <int QT, bool ROTATE> __global__ __launch_bounds__(256) void adapter_expand_kernel(ExpandArgs a)
 {
     const int lane = __lane_id(), w = threadIdx.x / kWave, R = a.ad.R;
     const int64_t m = (int64_t)blockIdx.y * 16 + lane % 16;
@@ -423,7 +428,7 @@ template <int QT> __global__ __launch_bounds__(256) void adapter_expand_kernel(E
     for (int b = 0; b < 4; b++) {
         const int64_t c = c0 + 16 * b + 4 * (lane / 16);
         acc[b] = f32x4{0, 0, 0, 0};
-        if (id >= 0 && c < a.C)
+        if ((ROTATE ? m < a.M : id >= 0) && c < a.C)
             acc[b] = *reinterpret_cast<const f32x4 *>(a.out + m * a.C + c);
     }
     constexpr int kTerms = QT == 0 ? 3 : 1;
@@ -472,13 +477,36 @@ template <int QT> __global__ __launch_bounds__(256) void adapter_expand_kernel(E
         if (k0 < length)
             use(load(k0));
     });
-    if (id < 0)
-        return;
+    if constexpr (ROTATE) {
+        // 16 rows of 256 columns; a row's pitch keeps the four column groups of
+        // a write on banks of their own.
+        constexpr int kPitch = 256 + 4;
+        __shared__ float tile[16 * kPitch];
 #pragma unroll
-    for (int b = 0; b < 4; b++) {
-        const int64_t c = c0 + 16 * b + 4 * (lane / 16);
-        if (c < a.C)
-            *reinterpret_cast<f32x4 *>(a.out + m * a.C + c) = acc[b];
+        for (int b = 0; b < 4; b++)
+            *reinterpret_cast<f32x4 *>(tile + (lane % 16) * kPitch + w * 64 + 16 * b + 4 * (lane / 16)) = acc[b];
+        __syncthreads();
+        // Eight consecutive values per lane, 32 lanes per row.  (All lanes take
+        // part in the exchange; blocks lie inside a row's C columns or outside.)
+#pragma unroll
+        for (int i = 0; i < 2; i++) {
+            const int chunk = i * 256 + threadIdx.x, row = chunk / 32, col = chunk % 32 * 8;
+            float v[8];
+            load8<false>(tile, row * kPitch + col, v);
+            fwht8_lanes(v, a.had, a.cb);
+            const int64_t om = (int64_t)blockIdx.y * 16 + row, oc = (int64_t)blockIdx.x * 256 + col;
+            if (om < a.M && oc < a.C)
+                store8(a.out, om * a.C + oc, v);
+        }
+    } else {
+        if (id < 0)
+            return;
+#pragma unroll
+        for (int b = 0; b < 4; b++) {
+            const int64_t c = c0 + 16 * b + 4 * (lane / 16);
+            if (c < a.C)
+                *reinterpret_cast<f32x4 *>(a.out + m * a.C + c) = acc[b];
+        }
     }
 }
 
@@ -611,6 +639,7 @@ struct PrepArgs {
     const int32_t *start;
     Slab *table;            // [slabs]
     int32_t *first;         // [L + 1]: the first slab of each adapter
+    float *da, *db;         // to be cleared for adapters without tokens, or null
 };
 
 // One 32 x 32 tile of src [rows, cols], turned: put(c, r, bits or value) for
@@ -641,8 +670,9 @@ __device__ __forceinline__ void transpose_tile(const void *src, int64_t s0, int6
 // product with dY, A for dX's epilogue (both then have the contraction index
 // contiguous), fp32 ones split into bf16 terms (B [3, L, R, N]; A, per adapter,
 // as the six pairs' slots of its K columns in the layout of adapter_frag.hpp),
-// and the table of slabs.  Workgroup 0 of adapter 0 makes the table, 256
-// adapters at a time.
+// the table of slabs, and zeros in the gradients of adapters without tokens where
+// the gradients are written without a sum over slabs.  Workgroup 0 of adapter 0
+// makes the table, 256 adapters at a time.
 template <bool WB> __global__ __launch_bounds__(256) void adapter_prep_kernel(PrepArgs p)
 {
     const int t = threadIdx.x;
@@ -650,6 +680,17 @@ template <bool WB> __global__ __launch_bounds__(256) void adapter_prep_kernel(Pr
         const int64_t rt = (p.R + 31) / 32, nt = (p.N + 31) / 32, l = blockIdx.y;
         const int64_t k = blockIdx.x - 1;
         const int64_t sb = l * p.N * p.R, sa = l * p.K * p.R;
+        if (p.da && p.start[l + 1] <= p.start[l]) {
+            // (32 x 32 elements per workgroup, and the matrices have as many.)
+            const bool is_b = k < rt * nt;
+            const int64_t size = (is_b ? p.N : p.K) * p.R;
+            for (int64_t i = (is_b ? k : k - rt * nt) * 1024 + t; i < size; i += 256) {
+                if (i >= ((is_b ? k : k - rt * nt) + 1) * 1024)
+                    break;
+                (is_b ? p.db + sb : p.da + sa)[i] = 0.0f;
+            }
+            return;
+        }
         if (k < rt * nt) {
             const int64_t plane = (int64_t)p.L * p.R * p.N;
             transpose_tile<WB>(p.b, sb, p.N, p.R, k / rt * 32, k % rt * 32,
@@ -737,6 +778,7 @@ struct OuterArgs {
     int64_t M, C;
     int R;
     float *part;            // per slab: [R, C], or [C, R] (TRANS)
+    float *out;             // per adapter, if each has one slab at most; else null
 };
 
 // An LDS tile of 32 tokens by COLS bf16 values, rows as in memory.  The
@@ -899,7 +941,7 @@ __device__ __forceinline__ void outer_product(const OuterArgs &a, int column_blo
                 step(i0 + 32, kSet1);
         }
     }
-    float *part = a.part + (int64_t)blockIdx.y * a.R * a.C;
+    float *part = a.out ? a.out + (int64_t)s.adapter * a.R * a.C : a.part + (int64_t)blockIdx.y * a.R * a.C;
 #pragma unroll
     for (int b = 0; b < 4; b++)
 #pragma unroll
@@ -994,17 +1036,26 @@ const uint16_t *launch_adapter_u(const AdapterArgs &g, const int8_t *qx, const f
     return terms;
 }
 
-void launch_adapter_expand(const AdapterEpilogue &ad, bool terms, int64_t M, int64_t C, float *out,
-                           hipStream_t st)
+template <bool ROTATE> static void run_expand(const ExpandArgs &e, int qt, hipStream_t st)
 {
-    const ExpandArgs e{ad, M, C, out};
-    const dim3 grid((unsigned)((C + 255) / 256), (unsigned)((M + 15) / 16));
-    if (ad.bf16)
-        hipLaunchKernelGGL(adapter_expand_kernel<1>, grid, dim3(256), 0, st, e);
-    else if (terms)
-        hipLaunchKernelGGL(adapter_expand_kernel<3>, grid, dim3(256), 0, st, e);
+    const dim3 grid((unsigned)((e.C + 255) / 256), (unsigned)((e.M + 15) / 16));
+    if (qt == 1)
+        hipLaunchKernelGGL((adapter_expand_kernel<1, ROTATE>), grid, dim3(256), 0, st, e);
+    else if (qt == 3)
+        hipLaunchKernelGGL((adapter_expand_kernel<3, ROTATE>), grid, dim3(256), 0, st, e);
+    else if constexpr (!ROTATE)
+        hipLaunchKernelGGL((adapter_expand_kernel<0, false>), grid, dim3(256), 0, st, e);
+}
+
+void launch_adapter_expand(const AdapterEpilogue &ad, bool dx, int64_t M, int64_t C, int had, float cb,
+                           float *out, hipStream_t st)
+{
+    const int qt = ad.bf16 ? 1 : dx ? 3 : 0;
+    const ExpandArgs e{ad, M, C, out, had, cb};
+    if (dx && had)
+        run_expand<true>(e, qt, st);
     else
-        hipLaunchKernelGGL(adapter_expand_kernel<0>, grid, dim3(256), 0, st, e);
+        run_expand<false>(e, qt, st);
 }
 
 void launch_adapter_group(const int32_t *ids, int64_t M, int L, int32_t *order, int32_t *start,
@@ -1015,6 +1066,11 @@ void launch_adapter_group(const int32_t *ids, int64_t M, int L, int32_t *order, 
 }
 
 static int64_t slabs_of(int64_t M, int64_t L) { return M / kSlab + (M < L ? M : L); }
+
+// So few tokens that no adapter has two slabs: the gradients need no sum (23
+// tokens, 4096 x 4096, rank 64, five adapters in fp32: 97 us for the call against
+// 101 us with the sum's launch).  No tokens at all: the sum writes the zeros.
+static bool one_slab(int64_t M) { return M > 0 && M <= kSlab; }
 
 // Offsets of a backward call's workspace.
 struct BwdLayout {
@@ -1044,13 +1100,15 @@ size_t adapter_bwd_bytes(int64_t M, int64_t N, int64_t K, int64_t L, int64_t R)
 }
 
 AdapterEpilogue launch_adapter_bwd_v(const AdapterArgs &g, const void *dy, bool dy_bf16,
-                                     const int32_t *start, unsigned *count, void *ws, hipStream_t st)
+                                     const int32_t *start, float *da, float *db, unsigned *count,
+                                     void *ws, hipStream_t st)
 {
     char *w = static_cast<char *>(ws);
     const BwdLayout o = bwd_layout(g.M, g.N, g.K, g.L, g.R);
     const PrepArgs p{g.a, g.b, reinterpret_cast<uint16_t *>(w + o.at), reinterpret_cast<uint16_t *>(w + o.bt),
                      g.N, g.K, g.M, g.L, g.R, (int)slabs_of(g.M, g.L), start,
-                     reinterpret_cast<Slab *>(w + o.table), reinterpret_cast<int32_t *>(w + o.first)};
+                     reinterpret_cast<Slab *>(w + o.table), reinterpret_cast<int32_t *>(w + o.first),
+                     one_slab(g.M) ? da : nullptr, one_slab(g.M) ? db : nullptr};
     const int64_t tiles = (int64_t)((g.R + 31) / 32) * ((g.N + 31) / 32 + (g.K + 31) / 32);
     const dim3 grid((unsigned)(g.M > 0 ? 1 + tiles : 1), (unsigned)g.L);
     if (g.bf16)
@@ -1081,10 +1139,13 @@ void launch_adapter_bwd_w(const AdapterArgs &g, const void *dy, bool dy_bf16, co
     float *pa = reinterpret_cast<float *>(w + o.pa), *pb = reinterpret_cast<float *>(w + o.pb);
     const float *v = reinterpret_cast<const float *>(w + o.v);
     if (g.M > 0) {
-        const OuterArgs a{v, sx, qx, order, table, g.M, g.K, g.R, pa};
-        const OuterArgs b{u, nullptr, dy, order, table, g.M, g.N, g.R, pb};
+        const bool one = one_slab(g.M);
+        const OuterArgs a{v, sx, qx, order, table, g.M, g.K, g.R, pa, one ? da : nullptr};
+        const OuterArgs b{u, nullptr, dy, order, table, g.M, g.N, g.R, pb, one ? db : nullptr};
         dy_bf16 ? run_outer<X_BF16>(a, b, slabs, st) : run_outer<X_F32>(a, b, slabs, st);
     }
+    if (one_slab(g.M))
+        return;
     const int64_t sa = (int64_t)g.R * g.K, sb = (int64_t)g.R * g.N;
     hipLaunchKernelGGL(adapter_sum_kernel, dim3((unsigned)((sa + 1023) / 1024 + (sb + 1023) / 1024), (unsigned)g.L),
                        dim3(256), 0, st, pa, sa, da, pb, sb, db,

@@ -259,7 +259,7 @@ int qlin_adapter_bwd(const void *dy, int dy_dtype, const int8_t *qg1, const floa
     const AdapterWs w = parts_of(workspace, QLIN_OP_DX, M, N, K);
     const qlin::AdapterArgs g{a, b, w_dtype == QLIN_BF16, scale, ids, M, N, K, (int)L, (int)R};
     const qlin::AdapterEpilogue va =
-        qlin::launch_adapter_bwd_v(g, dy, dy_dtype == QLIN_BF16, start, w.count, w.rest, s);
+        qlin::launch_adapter_bwd_v(g, dy, dy_dtype == QLIN_BF16, start, da, db, w.count, w.rest, s);
     // The adapters' gradients come before the product: they read dY again, while
     // the product with B has just left what fits of it in the infinity cache.
     qlin::launch_adapter_bwd_w(g, dy, dy_dtype == QLIN_BF16, qx, sx, u, order, da, db, w.rest, s);

@@ -49,9 +49,8 @@ void launch_product_adapter(const ProductArgs &a, const AdapterEpilogue &ad, hip
         ProductArgs b = a;
         b.had = 0;
         launch_product(b, st);
-        launch_adapter_expand(ad, a.op == 1, p.R, p.S, static_cast<float *>(a.out), st);
-        if (a.op == 1 && a.had >= 2 && a.had <= 128)
-            launch_hadamard(a.out, false, a.M, a.K, a.had, a.had_scale, static_cast<float *>(a.out), st);
+        launch_adapter_expand(ad, a.op == 1, p.R, p.S, a.had >= 2 && a.had <= 128 ? a.had : 0,
+                              a.had_scale, static_cast<float *>(a.out), st);
         return;
     }
     if (a.op == 0) {

@@ -68,10 +68,10 @@ struct AdapterEpilogue {
 // A forward or dX product (no workspace mode, contraction within the int32
 // bound) with that term added.
 void launch_product_adapter(const ProductArgs &p, const AdapterEpilogue &ad, hipStream_t st);
-// The term added to outputs [M, C] in memory; terms: an fp32 q comes as three
-// bf16 terms.
-void launch_adapter_expand(const AdapterEpilogue &ad, bool terms, int64_t M, int64_t C, float *out,
-                           hipStream_t st);
+// The term added to outputs [M, C] in memory, of a forward or (dx) of a dX
+// product, whose sums are then rotated in blocks of `had` (up to 128; 0: not).
+void launch_adapter_expand(const AdapterEpilogue &ad, bool dx, int64_t M, int64_t C, int had, float cb,
+                           float *out, hipStream_t st);
 
 // Whether the product kernels can address every operand byte of this shape
 // with their 32-bit buffer offsets (for contractions past the int32 bound,
@@ -170,7 +170,8 @@ void launch_adapter_group(const int32_t *ids, int64_t M, int L, int32_t *order, 
 // product), then both adapter gradients.
 size_t adapter_bwd_bytes(int64_t M, int64_t N, int64_t K, int64_t L, int64_t R);
 AdapterEpilogue launch_adapter_bwd_v(const AdapterArgs &g, const void *dy, bool dy_bf16,
-                                     const int32_t *start, unsigned *count, void *ws, hipStream_t st);
+                                     const int32_t *start, float *da, float *db, unsigned *count,
+                                     void *ws, hipStream_t st);
 void launch_adapter_bwd_w(const AdapterArgs &g, const void *dy, bool dy_bf16, const int8_t *qx,
                           const float *sx, const float *u, const int32_t *order, float *da,
                           float *db, void *ws, hipStream_t st);
