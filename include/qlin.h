@@ -51,7 +51,10 @@
  *  - Arithmetic: IEEE binary32, round to nearest even, no fused multiply-add,
  *    IEEE division.  Results are deterministic and do not depend on the
  *    launch configuration, except col_sum of qlin_quantize_cols (fp32 sums
- *    combined in arbitrary order).
+ *    combined in arbitrary order).  The calls of the section "around the
+ *    projection" are deterministic too, but use fused multiply-adds and bf16
+ *    matrix instructions with fp32 sums (fp32 operands as three bf16 terms);
+ *    each states its own precision.
  */
 #ifndef QLIN_H
 #define QLIN_H

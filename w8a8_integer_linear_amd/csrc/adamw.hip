@@ -18,7 +18,9 @@
 //
 // A chunk of 4096 elements is one workgroup's work; a lane holds two runs of
 // eight elements, and 16 lanes a block of 256, whose absmax is found with four
-// DPP steps.  One read and one write of each array: the HBM traffic bounds it.
+// DPP steps.  One read and one write of each array: the HBM traffic bounds it
+// (fp32 moments, 1.98 GB: 359 us; 8 bits, 1.61 GB: 295 us; both 5.5 TB/s, where a
+// streaming copy of 1 GiB reaches 6.2).
 #include <type_traits>
 
 #include "common.hpp"

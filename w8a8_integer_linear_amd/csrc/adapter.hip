@@ -14,9 +14,10 @@
 // are exact in bf16; an fp32 operand is split into three bf16 terms, which hold
 // its 24 bits, and a product of two such operands keeps the six partial
 // products above 2^-24.  (Two terms and three products were 2.5 to 5 times as
-// far from the 64-bit result as fp32 products are.)  Every lane of an accumulator belongs to one token, so the rows of a
-// 16-token block that have another adapter are dropped by a select and never
-// meet its matrices' values (a NaN in one adapter stays with its tokens).
+// far from the 64-bit result as fp32 products are.)  Every lane of an
+// accumulator belongs to one token, so the rows of a 16-token block that have
+// another adapter are dropped by a select and never meet its matrices' values (a
+// NaN in one adapter stays with its tokens).
 #include <type_traits>
 
 #include "adapter_frag.hpp"
@@ -106,7 +107,9 @@ __device__ __forceinline__ __amdgpu_buffer_rsrc_t buffer_of(const void *p)
 // takes a quarter, and their sums are added at the end.  What bounds it is the
 // read of x.  (Fragments straight from global memory took two to three times as
 // long: neighbouring lanes hold different rows, and each was a cache access of
-// its own.)
+// its own.)  12000 tokens of 7168 bf16 values, rank 16: 34-38 us, 4.5-5.1 TB/s.
+// Few tokens: the contraction is split over workgroups until there are two per
+// compute unit (611 tokens, 4096 codes, rank 32 in fp32: 13.5 us, latency).
 template <int X, int W, int RB, int STAGES>
 __global__ __launch_bounds__(512) void adapter_shrink_kernel(ShrinkArgs a)
 {
@@ -300,7 +303,8 @@ __global__ __launch_bounds__(512) void adapter_shrink_kernel(ShrinkArgs a)
 constexpr int64_t kSkinnyTokens = 16;
 
 // The same for a few tokens: one wave per token and rank, whose read of w (the
-// ranks of one token's adapter in as many waves) is what takes the time.
+// ranks of one token's adapter in as many waves) is what takes the time (7 tokens,
+// 4096 codes, rank 16: 3.5 us).
 template <int W> __global__ __launch_bounds__(256) void adapter_shrink_few_kernel(ShrinkArgs a)
 {
     const int lane = __lane_id();
@@ -642,6 +646,16 @@ struct PrepArgs {
     float *da, *db;         // to be cleared for adapters without tokens, or null
 };
 
+// Adapter l's tokens in the grouped order, as one slab, within the M tokens that
+// there are whatever start holds.
+__device__ __forceinline__ Slab tokens_of(const PrepArgs &p, int l)
+{
+    int64_t s0 = p.start[l], s1 = p.start[l + 1];
+    s0 = s0 < 0 ? 0 : s0 > p.M ? p.M : s0;
+    s1 = s1 < s0 ? s0 : s1 > p.M ? p.M : s1;
+    return Slab{l, (int32_t)s0, (int32_t)(s1 - s0), 0};
+}
+
 // One 32 x 32 tile of src [rows, cols], turned: put(c, r, bits or value) for
 // element (r, c), with neighbouring lanes at neighbouring r.
 template <bool WB, typename F>
@@ -680,15 +694,12 @@ template <bool WB> __global__ __launch_bounds__(256) void adapter_prep_kernel(Pr
         const int64_t rt = (p.R + 31) / 32, nt = (p.N + 31) / 32, l = blockIdx.y;
         const int64_t k = blockIdx.x - 1;
         const int64_t sb = l * p.N * p.R, sa = l * p.K * p.R;
-        if (p.da && p.start[l + 1] <= p.start[l]) {
-            // (32 x 32 elements per workgroup, and the matrices have as many.)
+        if (p.da && tokens_of(p, (int)l).rows == 0) {
+            // (As many elements per workgroup as a tile of 32 x 32 has.)
             const bool is_b = k < rt * nt;
-            const int64_t size = (is_b ? p.N : p.K) * p.R;
-            for (int64_t i = (is_b ? k : k - rt * nt) * 1024 + t; i < size; i += 256) {
-                if (i >= ((is_b ? k : k - rt * nt) + 1) * 1024)
-                    break;
+            const int64_t size = (is_b ? p.N : p.K) * p.R, i0 = (is_b ? k : k - rt * nt) * 1024;
+            for (int64_t i = i0 + t; i < i0 + 1024 && i < size; i += 256)
                 (is_b ? p.db + sb : p.da + sa)[i] = 0.0f;
-            }
             return;
         }
         if (k < rt * nt) {
@@ -739,14 +750,8 @@ template <bool WB> __global__ __launch_bounds__(256) void adapter_prep_kernel(Pr
     for (int l0 = 0; l0 <= p.L; l0 += 256) {
         __syncthreads();        // the zeros above, and the last round's sums
         const int l = l0 + t;
-        int64_t s0 = 0, s1 = 0;
-        if (l < p.L) {
-            s0 = p.start[l];
-            s1 = p.start[l + 1];
-            s0 = s0 < 0 ? 0 : s0 > p.M ? p.M : s0;
-            s1 = s1 < s0 ? s0 : s1 > p.M ? p.M : s1;
-        }
-        const int n = (int)((s1 - s0 + kSlab - 1) / kSlab);
+        const Slab mine = l < p.L ? tokens_of(p, l) : Slab{0, 0, 0, 0};
+        const int n = (mine.rows + kSlab - 1) / kSlab;
         int s = n;
         for (int o = 1; o < kWave; o <<= 1) {
             const int x = __shfl_up(s, o);
@@ -763,8 +768,8 @@ template <bool WB> __global__ __launch_bounds__(256) void adapter_prep_kernel(Pr
         if (l <= p.L)
             p.first[l] = before < p.slabs ? before : p.slabs;
         for (int i = 0; i < n && before + i < p.slabs; i++) {
-            const int64_t f = s0 + (int64_t)i * kSlab;
-            p.table[before + i] = Slab{l, (int32_t)f, (int32_t)(s1 - f < kSlab ? s1 - f : kSlab), 0};
+            const int past = i * kSlab, rows = mine.rows - past;
+            p.table[before + i] = Slab{l, mine.first + past, rows < kSlab ? rows : kSlab, 0};
         }
     }
 }
@@ -810,7 +815,9 @@ template <int COLS> struct TokenTile {
 // part[slab] = sum over the slab's tokens of p^T x, for 256 columns: 64 per
 // wave.  32 tokens at a time are brought into LDS, split into bf16 terms on
 // the way; the next ones' loads are in flight meanwhile.  The read of x bounds
-// it.
+// it: 12000 tokens of 7168 bf16 values and 5376 codes, rank 16, take 36-38 us for
+// both gradients, 6.2-6.5 TB/s, part of it out of the infinity cache, since the
+// product with B has just read the same dY.
 template <int X, bool TRANS, int RB>
 __device__ __forceinline__ void outer_product(const OuterArgs &a, int column_block, uint16_t *smem)
 {

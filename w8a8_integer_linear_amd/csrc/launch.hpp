@@ -54,9 +54,9 @@ void launch_product(const ProductArgs &p, hipStream_t st);
 
 // The low-rank term of a product's output row i: sum_r p[i, r] q[ids[i], j, r]
 // with p [rows, R] fp32 and q [L, cols, R] bf16 or, in the forward product, fp32;
-// the dX product takes an fp32 q as bf16 terms, as adapter_prep_kernel makes them.  terms
-// holds p as such terms, in the layout of adapter_frag.hpp (the forward product
-// of 16 rows or fewer reads p instead).
+// the dX product takes an fp32 q as bf16 terms, as adapter_prep_kernel makes
+// them.  terms holds p as such terms, in the layout of adapter_frag.hpp (the
+// forward product of 16 rows or fewer reads p instead).
 struct AdapterEpilogue {
     const float *p;
     const uint16_t *terms;
