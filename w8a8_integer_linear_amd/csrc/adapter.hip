@@ -42,8 +42,9 @@ struct ShrinkArgs {
     float *out;             // [M, R]
     uint16_t *terms;        // out as bf16 terms for a q of form qt
     int qt;
-    // The contraction in `splits` workgroups per 32 tokens and 16 ranks: their
-    // sums (part: 512 values each) and arrival counters (zero before and after).
+    // The contraction in `splits` workgroups per 32 tokens and group of ranks:
+    // their sums (part: 512 RB values each) and arrival counters (zero before and
+    // after).
     int splits;
     float *part;
     unsigned *count;
@@ -102,14 +103,15 @@ __device__ __forceinline__ __amdgpu_buffer_rsrc_t buffer_of(const void *p)
 
 // out[m, r] = scale xs[m] sum_c x[m, c] w[id, r, c] for 32 tokens and RB blocks of
 // 16 ranks per workgroup.  512 bytes of every token's row and w's values for
-// them are brought into LDS at a time, STAGES - 1 such stages ahead; of a
-// stage's steps of 32 contraction indexes each of four waves per token block
-// takes a quarter, and their sums are added at the end.  What bounds it is the
-// read of x.  (Fragments straight from global memory took two to three times as
-// long: neighbouring lanes hold different rows, and each was a cache access of
+// them are brought into LDS at a time, STAGES - 1 such stages ahead.  The waves
+// share a stage's steps of 32 contraction indexes, an eighth each for both token
+// blocks, so that w is split into terms once (fp32 x: four steps, a quarter each
+// for one token block), and their sums are added at the end.  What bounds it is
+// the read of x.  (Fragments straight from global memory took two to three times
+// as long: neighbouring lanes hold different rows, and each was a cache access of
 // its own.)  12000 tokens of 7168 bf16 values, rank 16: 34-38 us, 4.5-5.1 TB/s.
 // Few tokens: the contraction is split over workgroups until there are two per
-// compute unit (611 tokens, 4096 codes, rank 32 in fp32: 13.5 us, latency).
+// compute unit (611 tokens, 4096 codes, rank 32 in fp32: 11 us, latency).
 template <int X, int W, int RB, int STAGES>
 __global__ __launch_bounds__(512) void adapter_shrink_kernel(ShrinkArgs a)
 {
@@ -122,160 +124,204 @@ __global__ __launch_bounds__(512) void adapter_shrink_kernel(ShrinkArgs a)
     constexpr int kStageBytes = kXBytes + kWBytes;
     constexpr int kXLoads = kXBytes / 1024 / 8, kWLoads = (kWBytes / 1024 + 7) / 8;
     constexpr int kLoads = kXLoads + kWLoads;           // per wave and stage
-    static_assert(RB * 8 * kWave * 16 <= STAGES * kStageBytes, "the sums reuse the stages");
+    constexpr int kBlocks = X == X_F32 ? 1 : 2;         // token blocks of a wave
+    constexpr int kParts = 4 * kBlocks;                 // waves per token block
+    static_assert(RB * 2 * kParts * kWave * 16 <= STAGES * kStageBytes, "the sums reuse the stages");
     __shared__ __attribute__((aligned(1024))) int8_t smem[STAGES * kStageBytes];
     const int lane = __lane_id(), w = __builtin_amdgcn_readfirstlane((int)(threadIdx.x / kWave));
-    const int tb = w % 2, quarter = w / 2, rb0 = blockIdx.y * RB * 16;
+    const int tb0 = kBlocks == 2 ? 0 : w % 2, part = kBlocks == 2 ? w : w / 2;
+    const int rb0 = blockIdx.y * RB * 16;
     const int64_t m0 = (int64_t)blockIdx.x * 32;
     const int64_t plane = (int64_t)a.L * a.R * a.C * 2;
     const int row_bytes = (int)(a.C * kSize);
     const __amdgpu_buffer_rsrc_t xr = buffer_of(static_cast<const int8_t *>(a.x) + m0 * row_bytes);
-    // The adapters of both token blocks (every wave goes through them all).
-    int id[2], left[2];
-#pragma unroll
-    for (int t = 0; t < 2; t++)
-        left[t] = id[t] = id_of(a.ids, m0 + 16 * t + lane % 16, a.M, a.L);
-    const int mine_id = tb ? id[1] : id[0];
     // This workgroup's stages of the contraction.
     const int all = (int)((a.C + kStep - 1) / kStep);
     const int first = all * (int)blockIdx.z / a.splits;
     const int steps = all * ((int)blockIdx.z + 1) / a.splits - first;
-    f32x4 acc[RB];
+    // The work is one sequence: the stages of each adapter among the tokens, one
+    // adapter after another.  A cursor walks it: one where loads are issued, one
+    // where they are used.  (cur < 0: past the end.)
+    int id[2];
 #pragma unroll
-    for (int b = 0; b < RB; b++)
-        acc[b] = f32x4{0, 0, 0, 0};
-    while (true) {
-        int cur = -1;
+    for (int t = 0; t < 2; t++)
+        id[t] = id_of(a.ids, m0 + 16 * t + lane % 16, a.M, a.L);
+    struct Cursor {
+        int left[2], cur, st;
+        __device__ __forceinline__ void next_adapter()
+        {
+            cur = -1;
+            st = 0;
 #pragma unroll
-        for (int t = 0; t < 2; t++) {
-            const uint64_t any = __ballot(left[t] >= 0);
-            if (any)
-                cur = __builtin_amdgcn_readlane(left[t], (int)__builtin_ctzll(any));
+            for (int t = 0; t < 2; t++) {
+                const uint64_t any = __ballot(left[t] >= 0);
+                if (any)
+                    cur = __builtin_amdgcn_readlane(left[t], (int)__builtin_ctzll(any));
+            }
+#pragma unroll
+            for (int t = 0; t < 2; t++)
+                left[t] = left[t] == cur ? -1 : left[t];
         }
-        if (cur < 0)
-            break;
-        const int8_t *wbase = static_cast<const int8_t *>(a.w) + ((int64_t)cur * a.R + rb0) * a.C * kWSize;
-        auto issue = [&](int s) {
-            lds_byte *dst = (lds_byte *)smem + (s % STAGES) * kStageBytes;
-            // (Stages past the end read zeros, so that every iteration waits
-            // for the same number of loads.)
-            const int64_t k0 = (int64_t)(s < steps ? first + s : all) * kStep;
+        __device__ __forceinline__ void advance(int steps)
+        {
+            if (++st == steps)
+                next_adapter();
+        }
+    };
+    Cursor to = {{id[0], id[1]}, -1, 0};
+    to.next_adapter();
+    Cursor at = to;
+    f32x4 acc[kBlocks][RB];
 #pragma unroll
-            for (int n = 0; n < kXLoads; n++) {
-                int r, byte;
-                XTile::slot(w * kXLoads + n, r, byte);
-                const bool ok = m0 + r < a.M && k0 * kSize + byte < row_bytes;
-                const uint32_t off = ok ? (uint32_t)(r * row_bytes + byte + k0 * kSize) : kPastEnd;
-                __builtin_amdgcn_raw_ptr_buffer_load_lds(
-                    xr, (__attribute__((address_space(3))) void *)(dst + (w * kXLoads + n) * 1024), 16, off,
-                    0, 0, 0);
-            }
-#pragma unroll
-            for (int n = 0; n < kWLoads; n++) {
-                const int at = w * kWLoads + n;         // KiB of the stage's w
-                constexpr int kKiB = kWBytes / 1024, kPlaneKiB = kKiB / kPlanes;
-                // (A wave without a piece of its own repeats the last one.)
-                const int piece = at < kKiB ? at : kKiB - 1, p = piece / kPlaneKiB;
-                const __amdgpu_buffer_rsrc_t wr = buffer_of(wbase + p * plane);
-                int r, byte;
-                WTile::slot(piece % kPlaneKiB, r, byte);
-                const int64_t in = k0 * kWSize + byte;
-                const bool ok = rb0 + r < a.R && in < a.C * kWSize;
-                const uint32_t off = ok ? (uint32_t)(r * a.C * kWSize + in) : kPastEnd;
-                __builtin_amdgcn_raw_ptr_buffer_load_lds(
-                    wr, (__attribute__((address_space(3))) void *)(dst + kXBytes + piece * 1024), 16, off, 0,
-                    0, 0);
-            }
-        };
-        f32x4 s[RB];
+    for (int t = 0; t < kBlocks; t++)
 #pragma unroll
         for (int b = 0; b < RB; b++)
-            s[b] = f32x4{0, 0, 0, 0};
+            acc[t][b] = f32x4{0, 0, 0, 0};
+    const bool none = at.cur < 0;
+    // (Stages past the end read zeros, so that every iteration waits for the same
+    // number of loads.)
+    auto issue = [&](int slot) {
+        lds_byte *dst = (lds_byte *)smem + slot * kStageBytes;
+        const int64_t k0 = (int64_t)(to.cur >= 0 ? first + to.st : all) * kStep;
+        const int64_t w0 = ((int64_t)(to.cur >= 0 ? to.cur : 0) * a.R + rb0) * a.C * kWSize;
 #pragma unroll
-        for (int st = 0; st < STAGES - 1; st++)
-            issue(st);
-        for (int st = 0; st < steps; st++) {
-            issue(st + STAGES - 1);
-            asm volatile("s_waitcnt vmcnt(%0)" ::"n"(kLoads *(STAGES - 1)) : "memory");
-            asm volatile("s_barrier" ::: "memory");
-            const lds_byte *xt = (const lds_byte *)smem + (st % STAGES) * kStageBytes;
-            const lds_byte *wt = xt + kXBytes;
-            constexpr int kMine = kStep / 32 / 4;       // steps of this wave
+        for (int n = 0; n < kXLoads; n++) {
+            int r, byte;
+            XTile::slot(w * kXLoads + n, r, byte);
+            const bool ok = m0 + r < a.M && k0 * kSize + byte < row_bytes;
+            const uint32_t off = ok ? (uint32_t)(r * row_bytes + byte + k0 * kSize) : kPastEnd;
+            __builtin_amdgcn_raw_ptr_buffer_load_lds(
+                xr, (__attribute__((address_space(3))) void *)(dst + (w * kXLoads + n) * 1024), 16, off,
+                0, 0, 0);
+        }
 #pragma unroll
-            for (int q = 0; q < kMine; q++) {
-                const int k = (quarter * kMine + q) * 32 + 8 * (lane / 16), row = tb * 16 + lane % 16;
-                Frag<terms_of(X)> xf;
+        for (int n = 0; n < kWLoads; n++) {
+            const int at = w * kWLoads + n;         // KiB of the stage's w
+            constexpr int kKiB = kWBytes / 1024, kPlaneKiB = kKiB / kPlanes;
+            // (A wave without a piece of its own repeats the last one.)
+            const int piece = at < kKiB ? at : kKiB - 1, p = piece / kPlaneKiB;
+            const __amdgpu_buffer_rsrc_t wr = buffer_of(static_cast<const int8_t *>(a.w) + w0 + p * plane);
+            int r, byte;
+            WTile::slot(piece % kPlaneKiB, r, byte);
+            const int64_t in = k0 * kWSize + byte;
+            const bool ok = rb0 + r < a.R && in < a.C * kWSize;
+            const uint32_t off = ok ? (uint32_t)(r * a.C * kWSize + in) : kPastEnd;
+            __builtin_amdgcn_raw_ptr_buffer_load_lds(
+                wr, (__attribute__((address_space(3))) void *)(dst + kXBytes + piece * 1024), 16, off, 0,
+                0, 0);
+        }
+        to.advance(steps);
+    };
+    f32x4 s[kBlocks][RB];
+#pragma unroll
+    for (int t = 0; t < kBlocks; t++)
+#pragma unroll
+        for (int b = 0; b < RB; b++)
+            s[t][b] = f32x4{0, 0, 0, 0};
+#pragma unroll
+    for (int st = 0; st < STAGES - 1; st++)
+        issue(st);
+    int slot = 0;
+    while (at.cur >= 0) {
+        issue(slot + STAGES - 1 < STAGES ? slot + STAGES - 1 : slot - 1);
+        asm volatile("s_waitcnt vmcnt(%0)" ::"n"(kLoads *(STAGES - 1)) : "memory");
+        asm volatile("s_barrier" ::: "memory");
+        const lds_byte *xt = (const lds_byte *)smem + slot * kStageBytes;
+        const lds_byte *wt = xt + kXBytes;
+        constexpr int kMine = kStep / 32 / kParts;      // steps of this wave
+#pragma unroll
+        for (int q = 0; q < kMine; q++) {
+            const int k = (part * kMine + q) * 32 + 8 * (lane / 16);
+            Frag<terms_of(X)> xf[kBlocks];
+#pragma unroll
+            for (int t = 0; t < kBlocks; t++) {
+                const int row = (tb0 + t) * 16 + lane % 16;
                 if constexpr (X == X_BF16) {
-                    xf.t[0] = __builtin_bit_cast(bf16x8, XTile::read(xt, row, 2 * k));
+                    xf[t].t[0] = __builtin_bit_cast(bf16x8, XTile::read(xt, row, 2 * k));
                 } else if constexpr (X == X_I8) {
                     float v[8];
                     codes_to_float(XTile::read8(xt, row, k), v);
-                    xf.t[0] = round8(v);
+                    xf[t].t[0] = round8(v);
                 } else {
                     float v[8];
                     unpack8<false>({__builtin_bit_cast(f32x4, XTile::read(xt, row, 4 * k)),
                                     __builtin_bit_cast(f32x4, XTile::read(xt, row, 4 * k + 16))},
                                    v);
-                    xf = split8(v);
-                }
-#pragma unroll
-                for (int b = 0; b < RB; b++) {
-                    Frag<terms_of_w(W)> wf;
-                    const int r = 16 * b + lane % 16;
-                    if constexpr (W == X_F32) {
-                        float v[8];
-                        unpack8<false>({__builtin_bit_cast(f32x4, WTile::read(wt, r, 4 * k)),
-                                        __builtin_bit_cast(f32x4, WTile::read(wt, r, 4 * k + 16))},
-                                       v);
-                        wf = split8(v);
-                    } else {
-#pragma unroll
-                        for (int p = 0; p < kPlanes; p++)
-                            wf.t[p] = __builtin_bit_cast(
-                                bf16x8, WTile::read(wt + p * (kWBytes / kPlanes), r, 2 * k));
-                    }
-                    s[b] = mfma(wf, xf, s[b]);
+                    xf[t] = split8(v);
                 }
             }
-            // Every wave has read the stage before the next issue refills it.
-            lds_barrier();
-        }
-        // (The stages past the end are still landing.)
-        asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
-        asm volatile("s_barrier" ::: "memory");
 #pragma unroll
-        for (int t = 0; t < 2; t++)
-            left[t] = id[t] == cur ? -1 : left[t];
+            for (int b = 0; b < RB; b++) {
+                Frag<terms_of_w(W)> wf;
+                const int r = 16 * b + lane % 16;
+                if constexpr (W == X_F32) {
+                    float v[8];
+                    unpack8<false>({__builtin_bit_cast(f32x4, WTile::read(wt, r, 4 * k)),
+                                    __builtin_bit_cast(f32x4, WTile::read(wt, r, 4 * k + 16))},
+                                   v);
+                    wf = split8(v);
+                } else {
+#pragma unroll
+                    for (int p = 0; p < kPlanes; p++)
+                        wf.t[p] = __builtin_bit_cast(
+                            bf16x8, WTile::read(wt + p * (kWBytes / kPlanes), r, 2 * k));
+                }
+#pragma unroll
+                for (int t = 0; t < kBlocks; t++)
+                    s[t][b] = mfma(wf, xf[t], s[t][b]);
+            }
+        }
+        if (at.st == steps - 1) {
+#pragma unroll
+            for (int t = 0; t < kBlocks; t++)
+#pragma unroll
+                for (int b = 0; b < RB; b++) {
+                    acc[t][b] = (kBlocks == 2 ? id[t] : tb0 ? id[1] : id[0]) == at.cur ? s[t][b] : acc[t][b];
+                    s[t][b] = f32x4{0, 0, 0, 0};
+                }
+        }
+        // Every wave has read the stage before the next issue refills it.
+        lds_barrier();
+        at.advance(steps);
+        slot = slot + 1 < STAGES ? slot + 1 : 0;
+    }
+    // (The stages past the end are still landing.)
+    asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+    asm volatile("s_barrier" ::: "memory");
+    // (Without any adapter the first split writes the zeros.)
+    if (none && blockIdx.z > 0)
+        return;
+    f32x4 *red = reinterpret_cast<f32x4 *>(smem);       // [RB][2][kParts][64]
+#pragma unroll
+    for (int t = 0; t < kBlocks; t++)
 #pragma unroll
         for (int b = 0; b < RB; b++)
-            acc[b] = mine_id == cur ? s[b] : acc[b];
-    }
-    f32x4 *red = reinterpret_cast<f32x4 *>(smem);       // [RB][8 waves][64]
-#pragma unroll
-    for (int b = 0; b < RB; b++)
-        red[(b * 8 + w) * kWave + lane] = acc[b];
+            red[((b * 2 + tb0 + t) * kParts + part) * kWave + lane] = acc[t][b];
     __syncthreads();
+    // Waves 0 .. 2 RB - 1: token block tb, ranks rb.
+    const int tb = w % 2, rb = w / 2;
+    const int mine_id = tb ? id[1] : id[0];
     const int64_t m = m0 + 16 * tb + lane % 16;
-    const int r = rb0 + 16 * quarter + 4 * (lane / 16);
-    f32x4 s = {0, 0, 0, 0};
-    if (quarter < RB) {
-        s = red[(quarter * 8 + tb) * kWave + lane];
+    const int r = rb0 + 16 * rb + 4 * (lane / 16);
+    f32x4 sum = {0, 0, 0, 0};
+    if (rb < RB) {
+        sum = red[(w * kParts) * kWave + lane];
 #pragma unroll
-        for (int q = 1; q < 4; q++)
-            s += red[(quarter * 8 + tb + 2 * q) * kWave + lane];
+        for (int q = 1; q < kParts; q++)
+            sum += red[(w * kParts + q) * kWave + lane];
     }
-    if (a.splits > 1) {
+    if (!none && a.splits > 1) {
         // The sums cross XCDs, whose L2s are not coherent: stored and read with
         // the device-scope bit, the stores complete before the arrival counts.
         constexpr int kCoherentBit = 16;
         const int unit = blockIdx.x * gridDim.y + blockIdx.y;
         const __amdgpu_buffer_rsrc_t pr =
             buffer_of(a.part + (int64_t)unit * a.splits * (RB * 2 * kWave * 4));
-        const uint32_t at = ((quarter * 2 + tb) * kWave + lane) * 16;
+        const uint32_t mine = (w * kWave + lane) * 16;
         constexpr uint32_t kPart = RB * 2 * kWave * 16;
-        if (quarter < RB)
-            __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(i32x4, s), pr,
-                                                   blockIdx.z * kPart + at, 0, kCoherentBit);
+        if (rb < RB)
+            __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(i32x4, sum), pr,
+                                                   blockIdx.z * kPart + mine, 0, kCoherentBit);
         asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
         __syncthreads();
         int *flag = reinterpret_cast<int *>(smem);
@@ -286,16 +332,25 @@ __global__ __launch_bounds__(512) void adapter_shrink_kernel(ShrinkArgs a)
                 atomicExch(a.count + unit, 0u);
         }
         __syncthreads();
-        if (!*flag || quarter >= RB)
+        if (!*flag || rb >= RB)
             return;
-        s = f32x4{0, 0, 0, 0};
-        for (int z = 0; z < a.splits; z++)
-            s += __builtin_bit_cast(
-                f32x4, __builtin_amdgcn_raw_buffer_load_b128(pr, z * kPart + at, 0, kCoherentBit));
+        // In the order of the splits, four loads in flight.
+        sum = f32x4{0, 0, 0, 0};
+        for (int z0 = 0; z0 < a.splits; z0 += 4) {
+            f32x4 v[4];
+#pragma unroll
+            for (int z = 0; z < 4; z++)
+                v[z] = __builtin_bit_cast(
+                    f32x4, __builtin_amdgcn_raw_buffer_load_b128(
+                               pr, z0 + z < a.splits ? (z0 + z) * kPart + mine : kPastEnd, 0, kCoherentBit));
+#pragma unroll
+            for (int z = 0; z < 4; z++)
+                sum += v[z];
+        }
     }
-    if (quarter < RB && m < a.M && r < a.R) {
+    if (rb < RB && m < a.M && r < a.R) {
         const float f = mine_id >= 0 ? a.scale[mine_id] * (a.xs ? a.xs[m] : 1.0f) : 0.0f;
-        put_out(a, m, r, mine_id >= 0 ? s * f : f32x4{0, 0, 0, 0});
+        put_out(a, m, r, mine_id >= 0 ? sum * f : f32x4{0, 0, 0, 0});
     }
 }
 
