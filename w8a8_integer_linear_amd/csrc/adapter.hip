@@ -525,16 +525,19 @@ template <int QT, bool ROTATE> __global__ __launch_bounds__(256) void adapter_ex
                 acc[b] = mine ? t : acc[b];
             }
         };
-        // Two steps at a time, so that their loads are in flight together.
-        int k0 = 0;
-        for (; k0 + 32 < length; k0 += 64) {
-            const Step f0 = load(k0), f1 = load(k0 + 32);
+        // Several steps at a time, so that their loads are in flight together (those
+        // past the end are zeros).
+        constexpr int kAtOnce = QT == 0 ? 2 : 4;
+        for (int k0 = 0; k0 < length; k0 += 32 * kAtOnce) {
+            Step f[kAtOnce];
+#pragma unroll
+            for (int i = 0; i < kAtOnce; i++)
+                f[i] = load(k0 + 32 * i);
             __builtin_amdgcn_sched_barrier(0);
-            use(f0);
-            use(f1);
+#pragma unroll
+            for (int i = 0; i < kAtOnce; i++)
+                use(f[i]);
         }
-        if (k0 < length)
-            use(load(k0));
     });
     if constexpr (ROTATE) {
         // 16 rows of 256 columns; a row's pitch keeps the four column groups of
@@ -867,8 +870,11 @@ template <int COLS> struct TokenTile {
     }
 };
 
-// part[slab] = sum over the slab's tokens of p^T x, for 256 columns: 64 per
-// wave.  32 tokens at a time are brought into LDS, split into bf16 terms on
+// Columns of x per workgroup: fp32 ones take six products of terms each.
+constexpr int outer_cols(int x) { return x == X_F32 ? 128 : 256; }
+
+// part[slab] = sum over the slab's tokens of p^T x, for outer_cols(X) columns, a
+// quarter of them per wave.  32 tokens at a time are brought into LDS, split into bf16 terms on
 // the way; the next ones' loads are in flight meanwhile.  The read of x bounds
 // it: 12000 tokens of 7168 bf16 values and 5376 codes, rank 16, take 36-38 us for
 // both gradients, 6.2-6.5 TB/s, part of it out of the infinity cache, since the
@@ -876,8 +882,8 @@ template <int COLS> struct TokenTile {
 template <int X, bool TRANS, int RB>
 __device__ __forceinline__ void outer_product(const OuterArgs &a, int column_block, uint16_t *smem)
 {
-    constexpr int XT = terms_of(X);
-    using XTile = TokenTile<256>;
+    constexpr int XT = terms_of(X), kCols = outer_cols(X), CB = kCols / 64;
+    using XTile = TokenTile<kCols>;
     using PTile = TokenTile<RB * 16>;
     uint16_t(&xs)[XT][XTile::kSize] = *reinterpret_cast<uint16_t(*)[XT][XTile::kSize]>(smem);
     uint16_t(&ps)[3][PTile::kSize] =
@@ -886,19 +892,19 @@ __device__ __forceinline__ void outer_product(const OuterArgs &a, int column_blo
     if (s.rows <= 0)
         return;
     const int t = threadIdx.x, w = t / kWave, lane = __lane_id();
-    const int64_t c0 = (int64_t)column_block * 256;
-    f32x4 acc[4][RB];
+    const int64_t c0 = (int64_t)column_block * kCols;
+    f32x4 acc[CB][RB];
 #pragma unroll
-    for (int b = 0; b < 4; b++)
+    for (int b = 0; b < CB; b++)
 #pragma unroll
         for (int r = 0; r < RB; r++)
             acc[b][r] = f32x4{0, 0, 0, 0};
-    // Thread t brings 32 columns of token t / 8, sixteen bytes at a time (eight
-    // threads read 128 bytes in a row), and two ranks in 16 of p, into one of
-    // kSets register sets.
-    constexpr int kSets = X == X_F32 ? 1 : 2;
+    // Thread t brings an eighth of the columns of token t / 8, sixteen bytes at a
+    // time (eight threads read 128 bytes in a row), and two ranks in 16 of p, into
+    // one of two register sets.
+    constexpr int kSets = 2;
     constexpr int kSize = X == X_I8 ? 1 : X == X_BF16 ? 2 : 4;
-    constexpr int kPieces = 2 * kSize, kPer = 16 / kSize;       // 16-byte pieces, values in one
+    constexpr int kPieces = kCols * kSize / 128, kPer = 16 / kSize;       // 16-byte pieces, values in one
     const int row = t / 8, pc = (t % 8) * 2;
     auto piece_col = [&](int q) { return (t % 8) * kPer + q * 8 * kPer; };
     auto token = [&](int i0) {
@@ -973,12 +979,12 @@ __device__ __forceinline__ void outer_product(const OuterArgs &a, int column_blo
         load(next, S);          // (zeros after the last tokens)
         next = token(i0 + 32 * (kSets + 1));
         __builtin_amdgcn_sched_barrier(0);
-        Frag<XT> xf[4];
+        Frag<XT> xf[CB];
 #pragma unroll
-        for (int b = 0; b < 4; b++)
+        for (int b = 0; b < CB; b++)
 #pragma unroll
             for (int q = 0; q < XT; q++)
-                xf[b].t[q] = XTile::operand(xs[q], w * 64 + 16 * b);
+                xf[b].t[q] = XTile::operand(xs[q], w * (kCols / 4) + 16 * b);
 #pragma unroll
         for (int r = 0; r < RB; r++) {
             Frag<3> pf;
@@ -986,29 +992,26 @@ __device__ __forceinline__ void outer_product(const OuterArgs &a, int column_blo
             for (int q = 0; q < 3; q++)
                 pf.t[q] = PTile::operand(ps[q], 16 * r);
 #pragma unroll
-            for (int b = 0; b < 4; b++)
+            for (int b = 0; b < CB; b++)
                 acc[b][r] = TRANS ? mfma(pf, xf[b], acc[b][r]) : mfma(xf[b], pf, acc[b][r]);
         }
     };
     constexpr std::integral_constant<int, 0> kSet0{};
-    constexpr std::integral_constant<int, kSets - 1> kSet1{};
+    constexpr std::integral_constant<int, 1> kSet1{};
     load(token(0), kSet0);
-    if constexpr (kSets == 2)
-        load(token(32), kSet1);
+    load(token(32), kSet1);
     next = token(32 * kSets);
-    for (int i0 = 0; i0 < s.rows; i0 += 32 * kSets) {
+    for (int i0 = 0; i0 < s.rows; i0 += 64) {
         step(i0, kSet0);
-        if constexpr (kSets == 2) {
-            if (i0 + 32 < s.rows)
-                step(i0 + 32, kSet1);
-        }
+        if (i0 + 32 < s.rows)
+            step(i0 + 32, kSet1);
     }
     float *part = a.out ? a.out + (int64_t)s.adapter * a.R * a.C : a.part + (int64_t)blockIdx.y * a.R * a.C;
 #pragma unroll
-    for (int b = 0; b < 4; b++)
+    for (int b = 0; b < CB; b++)
 #pragma unroll
         for (int rb = 0; rb < RB; rb++) {
-            const int64_t cb = c0 + w * 64 + 16 * b;
+            const int64_t cb = c0 + w * (kCols / 4) + 16 * b;
             if (TRANS) {
                 const int64_t c = cb + lane % 16;
                 const int r = 16 * rb + 4 * (lane / 16);
@@ -1028,8 +1031,10 @@ __device__ __forceinline__ void outer_product(const OuterArgs &a, int column_blo
 template <int X, int RB>
 __global__ __launch_bounds__(256) void adapter_outer_kernel(OuterArgs a, OuterArgs b, int blocks)
 {
+    constexpr int kX = terms_of(X) * TokenTile<outer_cols(X)>::kSize;
+    constexpr int kCodes = TokenTile<outer_cols(X_I8)>::kSize;
     __shared__ __attribute__((aligned(16)))
-    uint16_t smem[terms_of(X) * TokenTile<256>::kSize + 3 * TokenTile<RB * 16>::kSize];
+    uint16_t smem[(kX > kCodes ? kX : kCodes) + 3 * TokenTile<RB * 16>::kSize];
     if ((int)blockIdx.x < blocks)
         outer_product<X_I8, false, RB>(a, blockIdx.x, smem);
     else
@@ -1038,8 +1043,9 @@ __global__ __launch_bounds__(256) void adapter_outer_kernel(OuterArgs a, OuterAr
 
 template <int X> void run_outer(const OuterArgs &a, const OuterArgs &b, int slabs, hipStream_t st)
 {
-    const int blocks = (int)((a.C + 255) / 256);
-    const dim3 grid((unsigned)(blocks + (b.C + 255) / 256), (unsigned)slabs), block(256);
+    auto column_blocks = [](int64_t c, int cols) { return (c + cols - 1) / cols; };
+    const int blocks = (int)column_blocks(a.C, outer_cols(X_I8));
+    const dim3 grid((unsigned)(blocks + column_blocks(b.C, outer_cols(X))), (unsigned)slabs), block(256);
     if (a.R <= 16)
         hipLaunchKernelGGL((adapter_outer_kernel<X, 1>), grid, block, 0, st, a, b, blocks);
     else if (a.R <= 32)
