@@ -471,8 +471,8 @@ struct ExpandArgs {
 
 // out[m, c] += sum_r p[m, r] q[id, c, r], for products of so few tiles that
 // adding the term in their epilogues would leave it to a few compute units: 16
-// tokens and 64 columns per wave.  QT as in the epilogues: q as one bf16 term, as
-// three, or fp32.  ROTATE: the sums go through LDS and are rotated in blocks along
+// tokens and 64 columns per wave.  QT: q as one bf16 term (1), as three (4), or
+// fp32 (0).  ROTATE: the sums go through LDS and are rotated in blocks along
 // their rows before they are written (the rotation of dX, which the product's
 // own epilogue cannot do before the term is added; a launch of its own cost 5 us
 // of 107 at 333 tokens, 4096 x 4096, rank 64 in fp32).
@@ -490,8 +490,8 @@ template <int QT, bool ROTATE> __global__ __launch_bounds__(256) void adapter_ex
         if ((ROTATE ? m < a.M : id >= 0) && c < a.C)
             acc[b] = *reinterpret_cast<const f32x4 *>(a.out + m * a.C + c);
     }
-    constexpr int kTerms = QT == 0 ? 3 : 1;
-    const int length = (QT == 0 ? 1 : QT == 1 ? 3 : 6) * R, steps = terms_steps(QT, R);
+    constexpr int kTerms = QT == 1 ? 1 : 3;
+    const int length = (QT == 1 ? 3 : 1) * R, steps = terms_steps(QT, R);
     struct Step {
         Frag<kTerms> p, q[4];
     };
@@ -508,11 +508,13 @@ template <int QT, bool ROTATE> __global__ __launch_bounds__(256) void adapter_ex
 #pragma unroll
             for (int b = 0; b < 4; b++) {
                 const int64_t c = c0 + 16 * b + lane % 16;
-                if constexpr (QT == 3)
-                    f.q[b].t[0] = load_frag<X_BF16>(
-                        a.ad.q, (((int64_t)cur * (a.C / 16) + c / 16) * steps + k0 / 32) * 512 + lane * 8,
-                        ok && c < a.C).t[0];
-                else
+                if constexpr (QT == 4) {
+                    const int64_t block = (int64_t)cur * (a.C / 16) + c / 16;
+#pragma unroll
+                    for (int t = 0; t < kTerms; t++)
+                        f.q[b].t[t] = load_frag<X_BF16>(
+                            a.ad.q, (block * steps + k0 / 32 * kTerms + t) * 512 + lane * 8, ok && c < a.C).t[0];
+                } else
                     f.q[b] = load_frag<QT == 0 ? X_F32 : X_BF16>(
                         a.ad.q, ((int64_t)cur * a.C + c) * R + r, ok && c < a.C);
             }
@@ -527,7 +529,7 @@ template <int QT, bool ROTATE> __global__ __launch_bounds__(256) void adapter_ex
         };
         // Several steps at a time, so that their loads are in flight together (those
         // past the end are zeros).
-        constexpr int kAtOnce = QT == 0 ? 2 : 4;
+        constexpr int kAtOnce = QT == 1 ? 4 : 2;
         for (int k0 = 0; k0 < length; k0 += 32 * kAtOnce) {
             Step f[kAtOnce];
 #pragma unroll
@@ -697,7 +699,7 @@ struct PrepArgs {
     const void *a, *b;      // [L, R, K], [L, N, R]
     uint16_t *at, *bt;
     int64_t N, K, M;
-    int L, R, slabs;
+    int L, R, qt, slabs;    // qt: the form of A's terms
     const int32_t *start;
     Slab *table;            // [slabs]
     int32_t *first;         // [L + 1]: the first slab of each adapter
@@ -740,8 +742,8 @@ __device__ __forceinline__ void transpose_tile(const void *src, int64_t s0, int6
 
 // What the backward kernels need first, in one launch: B transposed for the
 // product with dY, A for dX's epilogue (both then have the contraction index
-// contiguous), fp32 ones split into bf16 terms (B [3, L, R, N]; A, per adapter,
-// as the six pairs' slots of its K columns in the layout of adapter_frag.hpp),
+// contiguous), fp32 ones split into bf16 terms (B [3, L, R, N]; A, per adapter, in
+// the layout of adapter_frag.hpp, a row per column),
 // the table of slabs, and zeros in the gradients of adapters without tokens where
 // the gradients are written without a sum over slabs.  Workgroup 0 of adapter 0
 // makes the table, 256 adapters at a time.
@@ -792,7 +794,7 @@ template <bool WB> __global__ __launch_bounds__(256) void adapter_prep_kernel(Pr
 #pragma unroll
                     for (int e = 0; e < 8; e++)
                         v[e] = static_cast<const float *>(p.a)[sa + (r + e) * p.K + c];
-                    put_pairs(p.at + l * (p.K / 16) * terms_steps(3, p.R) * 512, p.R, c, (int)r, v);
+                    put_other(p.at + l * (p.K / 16) * terms_steps(p.qt, p.R) * 512, p.qt, p.R, c, (int)r, v);
                 }
             }
         }
@@ -1109,8 +1111,8 @@ template <bool ROTATE> static void run_expand(const ExpandArgs &e, int qt, hipSt
     const dim3 grid((unsigned)((e.C + 255) / 256), (unsigned)((e.M + 15) / 16));
     if (qt == 1)
         hipLaunchKernelGGL((adapter_expand_kernel<1, ROTATE>), grid, dim3(256), 0, st, e);
-    else if (qt == 3)
-        hipLaunchKernelGGL((adapter_expand_kernel<3, ROTATE>), grid, dim3(256), 0, st, e);
+    else if (qt == 4)
+        hipLaunchKernelGGL((adapter_expand_kernel<4, ROTATE>), grid, dim3(256), 0, st, e);
     else if constexpr (!ROTATE)
         hipLaunchKernelGGL((adapter_expand_kernel<0, false>), grid, dim3(256), 0, st, e);
 }
@@ -1118,7 +1120,7 @@ template <bool ROTATE> static void run_expand(const ExpandArgs &e, int qt, hipSt
 void launch_adapter_expand(const AdapterEpilogue &ad, bool dx, int64_t M, int64_t C, int had, float cb,
                            float *out, hipStream_t st)
 {
-    const int qt = ad.bf16 ? 1 : dx ? 3 : 0;
+    const int qt = ad.bf16 ? 1 : dx ? 4 : 0;
     const ExpandArgs e{ad, M, C, out, had, cb};
     if (dx && had)
         run_expand<true>(e, qt, st);
@@ -1148,13 +1150,14 @@ struct BwdLayout {
 static BwdLayout bwd_layout(int64_t M, int64_t N, int64_t K, int64_t L, int64_t R)
 {
     const size_t slabs = (size_t)slabs_of(M, L);
+    const int pairs = terms_steps(3, (int)R), steps = pairs > terms_steps(4, (int)R) ? pairs : terms_steps(4, (int)R);
     BwdLayout o;
     o.part = 0;
     o.bt = round256(o.part + kPartBytes);
     o.at = round256(o.bt + (size_t)L * R * N * 6);
-    o.v = round256(o.at + (size_t)L * (K / 16) * terms_steps(3, (int)R) * 1024);
+    o.v = round256(o.at + (size_t)L * (K / 16) * steps * 1024);
     o.terms = round256(o.v + (size_t)M * R * 4);
-    o.table = round256(o.terms + (size_t)((M + 15) / 16) * terms_steps(3, (int)R) * 1024);
+    o.table = round256(o.terms + (size_t)((M + 15) / 16) * steps * 1024);
     o.first = round256(o.table + slabs * sizeof(Slab));
     o.pa = round256(o.first + ((size_t)L + 1) * 4);
     o.pb = round256(o.pa + slabs * (size_t)R * K * 4);
@@ -1174,7 +1177,7 @@ AdapterEpilogue launch_adapter_bwd_v(const AdapterArgs &g, const void *dy, bool 
     char *w = static_cast<char *>(ws);
     const BwdLayout o = bwd_layout(g.M, g.N, g.K, g.L, g.R);
     const PrepArgs p{g.a, g.b, reinterpret_cast<uint16_t *>(w + o.at), reinterpret_cast<uint16_t *>(w + o.bt),
-                     g.N, g.K, g.M, g.L, g.R, (int)slabs_of(g.M, g.L), start,
+                     g.N, g.K, g.M, g.L, g.R, adapter_term_apart(g.M, g.K) ? 4 : 3, (int)slabs_of(g.M, g.L), start,
                      reinterpret_cast<Slab *>(w + o.table), reinterpret_cast<int32_t *>(w + o.first),
                      one_slab(g.M) ? da : nullptr, one_slab(g.M) ? db : nullptr};
     const int64_t tiles = (int64_t)((g.R + 31) / 32) * ((g.N + 31) / 32 + (g.K + 31) / 32);
@@ -1185,7 +1188,7 @@ AdapterEpilogue launch_adapter_bwd_v(const AdapterArgs &g, const void *dy, bool 
         hipLaunchKernelGGL(adapter_prep_kernel<false>, grid, dim3(256), 0, st, p);
     const ShrinkArgs s{dy,  nullptr, w + o.bt, g.scale, g.ids, g.M, g.N,
                        g.L, g.R,     reinterpret_cast<float *>(w + o.v),
-                       reinterpret_cast<uint16_t *>(w + o.terms), g.bf16 ? 1 : 3, 1,
+                       reinterpret_cast<uint16_t *>(w + o.terms), g.bf16 ? 1 : p.qt, 1,
                        reinterpret_cast<float *>(w + o.part), count};
     if (g.M > 0) {
         if (dy_bf16)

@@ -115,11 +115,13 @@ __device__ __forceinline__ int id_of(const int32_t *ids, int64_t m, int64_t M, i
 // its own, and those took longer than the products.)  The form QT of the other
 // operand decides the slots: 1, one bf16 term: p's three terms one after
 // another, 3 R slots; 3, three terms: the six pairs of terms above 2^-24, the
-// smallest first, 6 R slots; 0, fp32, split where it is used: the ranks in
-// steps of 32, and each step once per term.
+// smallest first, 6 R slots; 0, fp32, split where it is used, and 4, three
+// terms: the ranks in steps of 32, and each step once per term.  (3 is for the
+// products' epilogues, whose registers hold one term of 64 columns at a time; 4
+// is half its size.)
 constexpr int terms_steps(int qt, int R)
 {
-    return qt == 0 ? 3 * ((R + 31) / 32) : ((qt == 1 ? 3 : 6) * R + 31) / 32;
+    return qt == 0 || qt == 4 ? 3 * ((R + 31) / 32) : ((qt == 1 ? 3 : 6) * R + 31) / 32;
 }
 
 // Term of p in pair i of six (of the other operand: pair_other).
@@ -159,7 +161,7 @@ __device__ __forceinline__ void put_terms(uint16_t *terms, int qt, int R, int64_
             else
                 *at = b[0];
         };
-        if (qt == 0) {
+        if (qt == 0 || qt == 4) {
             put((r / 32 * 3 + t) * 32 + r % 32);
         } else if (qt == 1) {
             put(t * R + r);
@@ -172,12 +174,18 @@ __device__ __forceinline__ void put_terms(uint16_t *terms, int qt, int R, int64_
     }
 }
 
-// Writes eight values of the other operand's three terms into the slots of the
-// six pairs (QT = 3): column c, ranks r .. r + 7.
-__device__ __forceinline__ void put_pairs(uint16_t *terms, int R, int64_t c, int r, const float (&v)[8])
+// Writes eight values of the other operand's three terms into their slots (of
+// the six pairs, QT = 3, or QT = 4): column c, ranks r .. r + 7.
+__device__ __forceinline__ void put_other(uint16_t *terms, int qt, int R, int64_t c, int r, const float (&v)[8])
 {
-    const int steps = terms_steps(3, R);
+    const int steps = terms_steps(qt, R);
     const Frag<3> f = split8(v);
+    if (qt == 4) {
+#pragma unroll
+        for (int t = 0; t < 3; t++)
+            *reinterpret_cast<bf16x8 *>(terms + term_at(steps, c, (r / 32 * 3 + t) * 32 + r % 32)) = f.t[t];
+        return;
+    }
 #pragma unroll
     for (int i = 0; i < 6; i++)
         *reinterpret_cast<bf16x8 *>(terms + term_at(steps, c, i * R + r)) = f.t[pair_other(i)];

@@ -24,6 +24,15 @@ template <bool BKM, int EPI> void run(GemmParams &p, hipStream_t st)
 
 } // namespace
 
+// Few tiles: added in the epilogues, the term would be the work of as few compute
+// units (333 tokens, 4096 x 4096, rank 64 in fp32: 147 us for the backward call
+// against 125 us with the term in a launch of its own; 611 tokens, 4096 -> 14336,
+// rank 32, 168 tiles: 72 us against 90 us).
+bool adapter_term_apart(int64_t rows, int64_t cols)
+{
+    return ((rows + 255) / 256) * ((cols + 255) / 256) < 128;
+}
+
 void launch_product_adapter(const ProductArgs &a, const AdapterEpilogue &ad, hipStream_t st)
 {
     if (a.op == 0 && a.M <= 16) {
@@ -41,11 +50,7 @@ void launch_product_adapter(const ProductArgs &a, const AdapterEpilogue &ad, hip
     }
     GemmParams p = gemm_params(a);
     p.ad = ad;
-    // Few tiles: added in the epilogues, the term would be the work of as few
-    // compute units (333 tokens, 4096 x 4096, rank 64 in fp32: 147 us for the
-    // backward call against 125 us with the term in a launch of its own; 611
-    // tokens, 4096 -> 14336, rank 32, 168 tiles: 72 us against 90 us).
-    if (((p.R + 255) / 256) * ((p.S + 255) / 256) < 128) {
+    if (adapter_term_apart(p.R, p.S)) {
         ProductArgs b = a;
         b.had = 0;
         launch_product(b, st);

@@ -55,8 +55,8 @@ void launch_product(const ProductArgs &p, hipStream_t st);
 // The low-rank term of a product's output row i: sum_r p[i, r] q[ids[i], j, r]
 // with p [rows, R] fp32 and q [L, cols, R] bf16 or, in the forward product, fp32;
 // the dX product takes an fp32 q as bf16 terms, as adapter_prep_kernel makes
-// them.  terms holds p as such terms, in the layout of adapter_frag.hpp (the
-// forward product of 16 rows or fewer reads p instead).
+// them.  terms holds p as such terms, in the layout of adapter_frag.hpp that goes
+// with q's form (the forward product of 16 rows or fewer reads p instead).
 struct AdapterEpilogue {
     const float *p;
     const uint16_t *terms;
@@ -68,6 +68,8 @@ struct AdapterEpilogue {
 // A forward or dX product (no workspace mode, contraction within the int32
 // bound) with that term added.
 void launch_product_adapter(const ProductArgs &p, const AdapterEpilogue &ad, hipStream_t st);
+// Whether that term has a launch of its own, for outputs of this size.
+bool adapter_term_apart(int64_t rows, int64_t cols);
 // The term added to outputs [M, C] in memory, of a forward or (dx) of a dX
 // product, whose sums are then rotated in blocks of `had` (up to 128; 0: not).
 void launch_adapter_expand(const AdapterEpilogue &ad, bool dx, int64_t M, int64_t C, int had, float cb,
