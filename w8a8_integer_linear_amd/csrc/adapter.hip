@@ -109,7 +109,7 @@ __device__ __forceinline__ __amdgpu_buffer_rsrc_t buffer_of(const void *p)
 // for one token block), and their sums are added at the end.  What bounds it is
 // the read of x.  (Fragments straight from global memory took two to three times
 // as long: neighbouring lanes hold different rows, and each was a cache access of
-// its own.)  12000 tokens of 7168 bf16 values, rank 16: 34-38 us, 4.5-5.1 TB/s.
+// its own.)  12000 tokens of 7168 bf16 values, rank 16: 34-37 us, 4.6-5.1 TB/s.
 // Few tokens: the contraction is split over workgroups until there are two per
 // compute unit (611 tokens, 4096 codes, rank 32 in fp32: 11 us, latency).
 template <int X, int W, int RB, int STAGES>
@@ -413,19 +413,22 @@ template <int W> __global__ __launch_bounds__(256) void adapter_shrink_few_kerne
 // Most tokens of the kernel above: it reads an adapter once per token.
 constexpr int64_t kFewTokens = 32;
 
-// Workgroups that a product is split up to, fewest stages of a split's, and most
-// units (32 tokens by 16 ranks) that are split at all: each has an arrival
-// counter.
-constexpr int kSplitGroups = 512, kSplitStages = 2, kMaxUnits = 512;
+// Workgroups that a product of fewer units (32 tokens by a group of ranks) than
+// compute units is split up to, fewest stages of a split's, and most units that
+// are split at all: each has an arrival counter.
+constexpr int kCus = 256, kSplitGroups = 2 * kCus, kSplitStages = 2, kMaxUnits = 2 * kCus;
 static_assert(kMaxUnits * 4 <= kAdapterCountBytes, "arrival counters");
-constexpr size_t kPartBytes = (size_t)2 * kSplitGroups * 512 * 4;
+constexpr size_t kPartBytes = (size_t)2 * kMaxUnits * 2 * 512 * 4;
 
-// Splits of a product of `units` workgroups and `stages` stages each.
+// Splits of a product of `units` workgroups and `stages` stages each.  More units
+// than compute units are halved where that takes half a round less (375 units of
+// 7168 bf16 values: 43 us in one piece, 37 us in two).
 int splits_of(int64_t units, int64_t stages)
 {
     if (units > kMaxUnits)
         return 1;
-    int64_t n = kSplitGroups / units;
+    auto rounds = [](int64_t n) { return (n + kCus - 1) / kCus; };
+    int64_t n = units <= kCus ? kSplitGroups / units : rounds(2 * units) < 2 * rounds(units) ? 2 : 1;
     n = n < stages / kSplitStages ? n : stages / kSplitStages;
     return (int)(n < 1 ? 1 : n);
 }
@@ -625,7 +628,7 @@ __global__ __launch_bounds__(kGroupWaves *kWave) void adapter_group_kernel(const
                 continue;
             }
 #pragma unroll 1
-            for (int q = 0; q < kAtOnce; q++) {
+            for (int q = 0; q < kAtOnce && m0 + q * kWave < r1; q++) {
                 const int bin = seen[w][q * kWave + lane];
                 uint64_t left = __ballot(bin >= 0);
                 while (left) {
