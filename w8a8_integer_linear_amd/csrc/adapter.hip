@@ -706,7 +706,11 @@ struct PrepArgs {
     const int32_t *start;
     Slab *table;            // [slabs]
     int32_t *first;         // [L + 1]: the first slab of each adapter
-    float *da, *db;         // to be cleared for adapters without tokens, or null
+    // Where the gradients are finished by their own kernel: cleared for adapters
+    // without tokens, and its arrival counters; else null.
+    float *da, *db;
+    unsigned *count;
+    int64_t counts;
 };
 
 // Adapter l's tokens in the grouped order, as one slab, within the M tokens that
@@ -747,9 +751,9 @@ __device__ __forceinline__ void transpose_tile(const void *src, int64_t s0, int6
 // product with dY, A for dX's epilogue (both then have the contraction index
 // contiguous), fp32 ones split into bf16 terms (B [3, L, R, N]; A, per adapter, in
 // the layout of adapter_frag.hpp, a row per column),
-// the table of slabs, and zeros in the gradients of adapters without tokens where
-// the gradients are written without a sum over slabs.  Workgroup 0 of adapter 0
-// makes the table, 256 adapters at a time.
+// the table of slabs, and zeros in the arrival counters and in the gradients of
+// adapters without tokens.  Workgroup 0 of adapter 0 makes the table, 256 adapters
+// at a time.
 template <bool WB> __global__ __launch_bounds__(256) void adapter_prep_kernel(PrepArgs p)
 {
     const int t = threadIdx.x;
@@ -809,6 +813,8 @@ template <bool WB> __global__ __launch_bounds__(256) void adapter_prep_kernel(Pr
     const int w = t / kWave, lane = __lane_id();
     for (int i = t; i < p.slabs; i += 256)
         p.table[i] = Slab{0, 0, 0, 0};
+    for (int64_t i = t; i < p.counts; i += 256)
+        p.count[i] = 0;
     int base = 0;
     for (int l0 = 0; l0 <= p.L; l0 += 256) {
         __syncthreads();        // the zeros above, and the last round's sums
@@ -846,8 +852,34 @@ struct OuterArgs {
     int64_t M, C;
     int R;
     float *part;            // per slab: [R, C], or [C, R] (TRANS)
-    float *out;             // per adapter, if each has one slab at most; else null
+    // For few tokens, the adapters' sums over their slabs are made here too (else
+    // out is null): per adapter as part per slab; first: each adapter's first
+    // slab; count [L, gridDim.x]: arrivals, zero before.
+    float *out;
+    const int32_t *first;
+    unsigned *count;
 };
+
+// Values that other workgroups, on other XCDs whose L2s are not coherent with
+// this one's, read or have written.
+__device__ __forceinline__ void store_shared(float *p, f32x4 v)
+{
+    typedef unsigned long long u64x2 __attribute__((ext_vector_type(2)));
+    const u64x2 w = __builtin_bit_cast(u64x2, v);
+    unsigned long long *to = reinterpret_cast<unsigned long long *>(p);
+    __hip_atomic_store(to, w[0], __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+    __hip_atomic_store(to + 1, w[1], __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+}
+
+__device__ __forceinline__ f32x4 load_shared(float *p)
+{
+    typedef unsigned long long u64x2 __attribute__((ext_vector_type(2)));
+    unsigned long long *from = reinterpret_cast<unsigned long long *>(p);
+    u64x2 w;
+    w[0] = __hip_atomic_load(from, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+    w[1] = __hip_atomic_load(from + 1, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+    return __builtin_bit_cast(f32x4, w);
+}
 
 // An LDS tile of 32 tokens by COLS bf16 values, rows as in memory.  The
 // operands have the token index as the contraction, which the transposing read
@@ -1011,24 +1043,45 @@ __device__ __forceinline__ void outer_product(const OuterArgs &a, int column_blo
         if (i0 + 32 < s.rows)
             step(i0 + 32, kSet1);
     }
-    float *part = a.out ? a.out + (int64_t)s.adapter * a.R * a.C : a.part + (int64_t)blockIdx.y * a.R * a.C;
+    const int64_t size = (int64_t)a.R * a.C;
+    // f(index within one gradient, value) for this lane's results.
+    auto for_results = [&](auto f) {
 #pragma unroll
-    for (int b = 0; b < CB; b++)
+        for (int b = 0; b < CB; b++)
 #pragma unroll
-        for (int rb = 0; rb < RB; rb++) {
-            const int64_t cb = c0 + w * (kCols / 4) + 16 * b;
-            if (TRANS) {
-                const int64_t c = cb + lane % 16;
-                const int r = 16 * rb + 4 * (lane / 16);
+            for (int rb = 0; rb < RB; rb++) {
+                const int64_t cb = c0 + w * (kCols / 4) + 16 * b;
+                const int64_t c = cb + (TRANS ? lane % 16 : 4 * (lane / 16));
+                const int r = 16 * rb + (TRANS ? 4 * (lane / 16) : lane % 16);
                 if (c < a.C && r < a.R)
-                    *reinterpret_cast<f32x4 *>(part + c * a.R + r) = acc[b][rb];
-            } else {
-                const int64_t c = cb + 4 * (lane / 16);
-                const int r = 16 * rb + lane % 16;
-                if (c < a.C && r < a.R)
-                    *reinterpret_cast<f32x4 *>(part + r * a.C + c) = acc[b][rb];
+                    f(TRANS ? c * a.R + r : r * a.C + c, acc[b][rb]);
             }
-        }
+    };
+    float *part = a.part + (int64_t)blockIdx.y * size;
+    if (!a.out) {
+        for_results([&](int64_t at, f32x4 v) { *reinterpret_cast<f32x4 *>(part + at) = v; });
+        return;
+    }
+    float *out = a.out + (int64_t)s.adapter * size;
+    const int k0 = a.first[s.adapter], k1 = a.first[s.adapter + 1];
+    if (k1 - k0 > 1) {
+        // The last of the adapter's slabs to arrive adds them up, in their order.
+        for_results([&](int64_t at, f32x4 v) { store_shared(part + at, v); });
+        asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+        __syncthreads();
+        int *last = reinterpret_cast<int *>(smem);
+        if (t == 0)
+            *last = (int)atomicAdd(a.count + s.adapter * gridDim.x + blockIdx.x, 1u) == k1 - k0 - 1;
+        __syncthreads();
+        if (!*last)
+            return;
+        for_results([&](int64_t at, f32x4 &v) {
+            v = f32x4{0, 0, 0, 0};
+            for (int k = k0; k < k1; k++)
+                v += load_shared(a.part + k * size + at);
+        });
+    }
+    for_results([&](int64_t at, f32x4 v) { *reinterpret_cast<f32x4 *>(out + at) = v; });
 }
 
 // Both gradients in one launch: the first `blocks` column blocks are A's (from
@@ -1140,14 +1193,21 @@ void launch_adapter_group(const int32_t *ids, int64_t M, int L, int32_t *order, 
 
 static int64_t slabs_of(int64_t M, int64_t L) { return M / kSlab + (M < L ? M : L); }
 
-// So few tokens that no adapter has two slabs: the gradients need no sum (23
-// tokens, 4096 x 4096, rank 64, five adapters in fp32: 97 us for the call against
-// 101 us with the sum's launch).  No tokens at all: the sum writes the zeros.
-static bool one_slab(int64_t M) { return M > 0 && M <= kSlab; }
+// So few tokens, hence slabs of one adapter, that the last to arrive adds them up
+// (333 tokens, 4096 x 4096, rank 64, five adapters in fp32: 84 us for the call
+// against 91.5 us with the sums in a launch of their own; 12000 tokens of three
+// adapters: 497 us against 463 us).  No tokens at all: the launch writes the zeros.
+static bool sums_in_place(int64_t M) { return M > 0 && M <= 4 * kSlab; }
+
+// Column blocks of both gradients (a gradient's with the fewest columns each).
+static int64_t outer_blocks(int64_t N, int64_t K)
+{
+    return (K + outer_cols(X_I8) - 1) / outer_cols(X_I8) + (N + outer_cols(X_F32) - 1) / outer_cols(X_F32);
+}
 
 // Offsets of a backward call's workspace.
 struct BwdLayout {
-    size_t part, bt, at, v, terms, table, first, pa, pb, end;
+    size_t part, bt, at, v, terms, table, first, count, pa, pb, end;
 };
 
 static BwdLayout bwd_layout(int64_t M, int64_t N, int64_t K, int64_t L, int64_t R)
@@ -1162,7 +1222,8 @@ static BwdLayout bwd_layout(int64_t M, int64_t N, int64_t K, int64_t L, int64_t 
     o.terms = round256(o.v + (size_t)M * R * 4);
     o.table = round256(o.terms + (size_t)((M + 15) / 16) * steps * 1024);
     o.first = round256(o.table + slabs * sizeof(Slab));
-    o.pa = round256(o.first + ((size_t)L + 1) * 4);
+    o.count = round256(o.first + ((size_t)L + 1) * 4);
+    o.pa = round256(o.count + (sums_in_place(M) ? (size_t)L * outer_blocks(N, K) * 4 : 0));
     o.pb = round256(o.pa + slabs * (size_t)R * K * 4);
     o.end = round256(o.pb + slabs * (size_t)R * N * 4);
     return o;
@@ -1182,7 +1243,9 @@ AdapterEpilogue launch_adapter_bwd_v(const AdapterArgs &g, const void *dy, bool 
     const PrepArgs p{g.a, g.b, reinterpret_cast<uint16_t *>(w + o.at), reinterpret_cast<uint16_t *>(w + o.bt),
                      g.N, g.K, g.M, g.L, g.R, adapter_term_apart(g.M, g.K) ? 4 : 3, (int)slabs_of(g.M, g.L), start,
                      reinterpret_cast<Slab *>(w + o.table), reinterpret_cast<int32_t *>(w + o.first),
-                     one_slab(g.M) ? da : nullptr, one_slab(g.M) ? db : nullptr};
+                     sums_in_place(g.M) ? da : nullptr, sums_in_place(g.M) ? db : nullptr,
+                     reinterpret_cast<unsigned *>(w + o.count),
+                     sums_in_place(g.M) ? g.L * outer_blocks(g.N, g.K) : 0};
     const int64_t tiles = (int64_t)((g.R + 31) / 32) * ((g.N + 31) / 32 + (g.K + 31) / 32);
     const dim3 grid((unsigned)(g.M > 0 ? 1 + tiles : 1), (unsigned)g.L);
     if (g.bf16)
@@ -1213,12 +1276,14 @@ void launch_adapter_bwd_w(const AdapterArgs &g, const void *dy, bool dy_bf16, co
     float *pa = reinterpret_cast<float *>(w + o.pa), *pb = reinterpret_cast<float *>(w + o.pb);
     const float *v = reinterpret_cast<const float *>(w + o.v);
     if (g.M > 0) {
-        const bool one = one_slab(g.M);
-        const OuterArgs a{v, sx, qx, order, table, g.M, g.K, g.R, pa, one ? da : nullptr};
-        const OuterArgs b{u, nullptr, dy, order, table, g.M, g.N, g.R, pb, one ? db : nullptr};
+        const bool here = sums_in_place(g.M);
+        const int32_t *first = reinterpret_cast<const int32_t *>(w + o.first);
+        unsigned *count = reinterpret_cast<unsigned *>(w + o.count);
+        const OuterArgs a{v, sx, qx, order, table, g.M, g.K, g.R, pa, here ? da : nullptr, first, count};
+        const OuterArgs b{u, nullptr, dy, order, table, g.M, g.N, g.R, pb, here ? db : nullptr, first, count};
         dy_bf16 ? run_outer<X_BF16>(a, b, slabs, st) : run_outer<X_F32>(a, b, slabs, st);
     }
-    if (one_slab(g.M))
+    if (sums_in_place(g.M))
         return;
     const int64_t sa = (int64_t)g.R * g.K, sb = (int64_t)g.R * g.N;
     hipLaunchKernelGGL(adapter_sum_kernel, dim3((unsigned)((sa + 1023) / 1024 + (sb + 1023) / 1024), (unsigned)g.L),
