@@ -464,33 +464,30 @@ template <int X, int W> void run_shrink(const ShrinkArgs &a, hipStream_t st)
 
 // ------------------------------------------------------------------ expand
 
-struct ExpandArgs {
-    AdapterEpilogue ad;
-    int64_t M, C;
-    float *out;             // [M, C], added to
-    int had;                // rotation block of the sums (up to 128), or 0
-    float cb;
-};
-
 // out[m, c] += sum_r p[m, r] q[id, c, r], for products of so few tiles that
-// adding the term in their epilogues would leave it to a few compute units: 16
-// tokens and 64 columns per wave.  QT: q as one bf16 term (1), as three (4), or
-// fp32 (0).  ROTATE: the sums go through LDS and are rotated in blocks along
-// their rows before they are written (the rotation of dX, which the product's
-// own epilogue cannot do before the term is added; a launch of its own cost 5 us
-// of 107 at 333 tokens, 4096 x 4096, rank 64 in fp32).
-template <int QT, bool ROTATE> __global__ __launch_bounds__(256) void adapter_expand_kernel(ExpandArgs a)
+// adding the term in their epilogues would leave it to a few compute units: block
+// (bx, by) has 16 tokens by 256 columns, 64 per wave.  QT: q as one bf16 term (1),
+// as three (4), or fp32 (0).  DX: the sums go through LDS (kExpandTile floats) and
+// are rotated in blocks along their rows before they are written (the rotation of
+// dX, which the product's own epilogue cannot do before the term is added; a
+// launch of its own cost 5 us of 107 at 333 tokens, 4096 x 4096, rank 64 in fp32).
+// Reading q bounds it: three terms took 8 us there, their six pairs 13 us.
+// A row's pitch keeps the four column groups of a write on banks of their own.
+constexpr int kExpandPitch = 256 + 4, kExpandTile = 16 * kExpandPitch;
+
+template <int QT, bool DX>
+__device__ __forceinline__ void expand(const AdapterTermArgs &a, int64_t bx, int64_t by, float *tile)
 {
     const int lane = __lane_id(), w = threadIdx.x / kWave, R = a.ad.R;
-    const int64_t m = (int64_t)blockIdx.y * 16 + lane % 16;
-    const int64_t c0 = (int64_t)blockIdx.x * 256 + w * 64;
+    const int64_t m = by * 16 + lane % 16;
+    const int64_t c0 = bx * 256 + w * 64;
     const int id = id_of(a.ad.ids, m, a.M, a.ad.L);
     f32x4 acc[4];
 #pragma unroll
     for (int b = 0; b < 4; b++) {
         const int64_t c = c0 + 16 * b + 4 * (lane / 16);
         acc[b] = f32x4{0, 0, 0, 0};
-        if ((ROTATE ? m < a.M : id >= 0) && c < a.C)
+        if ((DX ? m < a.M : id >= 0) && c < a.C)
             acc[b] = *reinterpret_cast<const f32x4 *>(a.out + m * a.C + c);
     }
     constexpr int kTerms = QT == 1 ? 1 : 3;
@@ -507,7 +504,7 @@ template <int QT, bool ROTATE> __global__ __launch_bounds__(256) void adapter_ex
 #pragma unroll
             for (int t = 0; t < kTerms; t++)
                 f.p.t[t] = load_frag<X_BF16>(
-                    a.ad.terms, (((int64_t)blockIdx.y * steps + k0 / 32 * kTerms + t) * 64 + lane) * 8, ok).t[0];
+                    a.ad.terms, ((by * steps + k0 / 32 * kTerms + t) * 64 + lane) * 8, ok).t[0];
 #pragma unroll
             for (int b = 0; b < 4; b++) {
                 const int64_t c = c0 + 16 * b + lane % 16;
@@ -544,14 +541,11 @@ template <int QT, bool ROTATE> __global__ __launch_bounds__(256) void adapter_ex
                 use(f[i]);
         }
     });
-    if constexpr (ROTATE) {
-        // 16 rows of 256 columns; a row's pitch keeps the four column groups of
-        // a write on banks of their own.
-        constexpr int kPitch = 256 + 4;
-        __shared__ float tile[16 * kPitch];
+    if constexpr (DX) {
 #pragma unroll
         for (int b = 0; b < 4; b++)
-            *reinterpret_cast<f32x4 *>(tile + (lane % 16) * kPitch + w * 64 + 16 * b + 4 * (lane / 16)) = acc[b];
+            *reinterpret_cast<f32x4 *>(tile + (lane % 16) * kExpandPitch + w * 64 + 16 * b + 4 * (lane / 16)) =
+                acc[b];
         __syncthreads();
         // Eight consecutive values per lane, 32 lanes per row.  (All lanes take
         // part in the exchange; blocks lie inside a row's C columns or outside.)
@@ -559,9 +553,10 @@ template <int QT, bool ROTATE> __global__ __launch_bounds__(256) void adapter_ex
         for (int i = 0; i < 2; i++) {
             const int chunk = i * 256 + threadIdx.x, row = chunk / 32, col = chunk % 32 * 8;
             float v[8];
-            load8<false>(tile, row * kPitch + col, v);
-            fwht8_lanes(v, a.had, a.cb);
-            const int64_t om = (int64_t)blockIdx.y * 16 + row, oc = (int64_t)blockIdx.x * 256 + col;
+            load8<false>(tile, row * kExpandPitch + col, v);
+            if (a.had)
+                fwht8_lanes(v, a.had, a.cb);
+            const int64_t om = by * 16 + row, oc = bx * 256 + col;
             if (om < a.M && oc < a.C)
                 store8(a.out, om * a.C + oc, v);
         }
@@ -575,6 +570,11 @@ template <int QT, bool ROTATE> __global__ __launch_bounds__(256) void adapter_ex
                 *reinterpret_cast<f32x4 *>(a.out + m * a.C + c) = acc[b];
         }
     }
+}
+
+template <int QT> __global__ __launch_bounds__(256) void adapter_expand_kernel(AdapterTermArgs a)
+{
+    expand<QT, false>(a, blockIdx.x, blockIdx.y, nullptr);
 }
 
 // ------------------------------------------------------- grouping of tokens
@@ -1085,33 +1085,63 @@ __device__ __forceinline__ void outer_product(const OuterArgs &a, int column_blo
 }
 
 // Both gradients in one launch: the first `blocks` column blocks are A's (from
-// the INT8 codes), the others B's (from dY, of type X).
-template <int X, int RB>
-__global__ __launch_bounds__(256) void adapter_outer_kernel(OuterArgs a, OuterArgs b, int blocks)
+// the INT8 codes), the others B's (from dY, of type X).  QT >= 0: the rows of
+// workgroups after the slabs' add dX's term to the product meanwhile (333 tokens,
+// 4096 x 4096, rank 64 in fp32: 77 us for the call against 84 us with a launch of
+// its own).
+template <int X, int RB, int QT>
+__global__ __launch_bounds__(256) void adapter_outer_kernel(OuterArgs a, OuterArgs b, int blocks, int slabs,
+                                                            AdapterTermArgs e)
 {
     constexpr int kX = terms_of(X) * TokenTile<outer_cols(X)>::kSize;
     constexpr int kCodes = TokenTile<outer_cols(X_I8)>::kSize;
-    __shared__ __attribute__((aligned(16)))
-    uint16_t smem[(kX > kCodes ? kX : kCodes) + 3 * TokenTile<RB * 16>::kSize];
+    constexpr int kOuter = (kX > kCodes ? kX : kCodes) + 3 * TokenTile<RB * 16>::kSize;
+    constexpr int kSize = QT >= 0 && 2 * kExpandTile > kOuter ? 2 * kExpandTile : kOuter;
+    __shared__ __attribute__((aligned(16))) uint16_t smem[kSize];
+    if constexpr (QT >= 0) {
+        if ((int)blockIdx.y >= slabs) {
+            const int64_t i = (int64_t)((int)blockIdx.y - slabs) * gridDim.x + blockIdx.x;
+            const int64_t across = (e.C + 255) / 256;
+            if (i < across * ((e.M + 15) / 16))
+                expand<QT, true>(e, i % across, i / across, reinterpret_cast<float *>(smem));
+            return;
+        }
+    }
     if ((int)blockIdx.x < blocks)
         outer_product<X_I8, false, RB>(a, blockIdx.x, smem);
     else
         outer_product<X, true, RB>(b, blockIdx.x - blocks, smem);
 }
 
-template <int X> void run_outer(const OuterArgs &a, const OuterArgs &b, int slabs, hipStream_t st)
+template <int X, int QT>
+void run_outer(const OuterArgs &a, const OuterArgs &b, int slabs, const AdapterTermArgs &e, hipStream_t st)
 {
     auto column_blocks = [](int64_t c, int cols) { return (c + cols - 1) / cols; };
-    const int blocks = (int)column_blocks(a.C, outer_cols(X_I8));
-    const dim3 grid((unsigned)(blocks + column_blocks(b.C, outer_cols(X))), (unsigned)slabs), block(256);
+    const int64_t blocks = column_blocks(a.C, outer_cols(X_I8)), wide = blocks + column_blocks(b.C, outer_cols(X));
+    const int64_t terms = QT < 0 ? 0 : ((e.C + 255) / 256 * ((e.M + 15) / 16) + wide - 1) / wide;
+    auto go = [&](auto kernel) {
+        hipLaunchKernelGGL(kernel, dim3((unsigned)wide, (unsigned)(slabs + terms)), dim3(256), 0, st, a, b,
+                           (int)blocks, slabs, e);
+    };
     if (a.R <= 16)
-        hipLaunchKernelGGL((adapter_outer_kernel<X, 1>), grid, block, 0, st, a, b, blocks);
+        go(adapter_outer_kernel<X, 1, QT>);
     else if (a.R <= 32)
-        hipLaunchKernelGGL((adapter_outer_kernel<X, 2>), grid, block, 0, st, a, b, blocks);
+        go(adapter_outer_kernel<X, 2, QT>);
     else if (a.R <= 64)
-        hipLaunchKernelGGL((adapter_outer_kernel<X, 4>), grid, block, 0, st, a, b, blocks);
+        go(adapter_outer_kernel<X, 4, QT>);
     else
-        hipLaunchKernelGGL((adapter_outer_kernel<X, 8>), grid, block, 0, st, a, b, blocks);
+        go(adapter_outer_kernel<X, 8, QT>);
+}
+
+template <int X>
+void run_outer(const OuterArgs &a, const OuterArgs &b, int slabs, const AdapterTermArgs *dx, hipStream_t st)
+{
+    if (!dx)
+        run_outer<X, -1>(a, b, slabs, AdapterTermArgs{}, st);
+    else if (dx->ad.bf16)
+        run_outer<X, 1>(a, b, slabs, *dx, st);
+    else
+        run_outer<X, 4>(a, b, slabs, *dx, st);
 }
 
 // out[l] = the sum of l's slabs, in order; zeros for an adapter without tokens.
@@ -1162,26 +1192,13 @@ const uint16_t *launch_adapter_u(const AdapterArgs &g, const int8_t *qx, const f
     return terms;
 }
 
-template <bool ROTATE> static void run_expand(const ExpandArgs &e, int qt, hipStream_t st)
+void launch_adapter_expand(const AdapterTermArgs &e, hipStream_t st)
 {
     const dim3 grid((unsigned)((e.C + 255) / 256), (unsigned)((e.M + 15) / 16));
-    if (qt == 1)
-        hipLaunchKernelGGL((adapter_expand_kernel<1, ROTATE>), grid, dim3(256), 0, st, e);
-    else if (qt == 4)
-        hipLaunchKernelGGL((adapter_expand_kernel<4, ROTATE>), grid, dim3(256), 0, st, e);
-    else if constexpr (!ROTATE)
-        hipLaunchKernelGGL((adapter_expand_kernel<0, false>), grid, dim3(256), 0, st, e);
-}
-
-void launch_adapter_expand(const AdapterEpilogue &ad, bool dx, int64_t M, int64_t C, int had, float cb,
-                           float *out, hipStream_t st)
-{
-    const int qt = ad.bf16 ? 1 : dx ? 4 : 0;
-    const ExpandArgs e{ad, M, C, out, had, cb};
-    if (dx && had)
-        run_expand<true>(e, qt, st);
+    if (e.ad.bf16)
+        hipLaunchKernelGGL(adapter_expand_kernel<1>, grid, dim3(256), 0, st, e);
     else
-        run_expand<false>(e, qt, st);
+        hipLaunchKernelGGL(adapter_expand_kernel<0>, grid, dim3(256), 0, st, e);
 }
 
 void launch_adapter_group(const int32_t *ids, int64_t M, int L, int32_t *order, int32_t *start,
@@ -1267,7 +1284,7 @@ AdapterEpilogue launch_adapter_bwd_v(const AdapterArgs &g, const void *dy, bool 
 
 void launch_adapter_bwd_w(const AdapterArgs &g, const void *dy, bool dy_bf16, const int8_t *qx,
                           const float *sx, const float *u, const int32_t *order, float *da, float *db,
-                          void *ws, hipStream_t st)
+                          const AdapterTermArgs *dx, void *ws, hipStream_t st)
 {
     char *w = static_cast<char *>(ws);
     const BwdLayout o = bwd_layout(g.M, g.N, g.K, g.L, g.R);
@@ -1281,7 +1298,7 @@ void launch_adapter_bwd_w(const AdapterArgs &g, const void *dy, bool dy_bf16, co
         unsigned *count = reinterpret_cast<unsigned *>(w + o.count);
         const OuterArgs a{v, sx, qx, order, table, g.M, g.K, g.R, pa, here ? da : nullptr, first, count};
         const OuterArgs b{u, nullptr, dy, order, table, g.M, g.N, g.R, pb, here ? db : nullptr, first, count};
-        dy_bf16 ? run_outer<X_BF16>(a, b, slabs, st) : run_outer<X_F32>(a, b, slabs, st);
+        dy_bf16 ? run_outer<X_BF16>(a, b, slabs, dx, st) : run_outer<X_F32>(a, b, slabs, dx, st);
     }
     if (sums_in_place(g.M))
         return;

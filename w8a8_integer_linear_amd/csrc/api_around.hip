@@ -260,19 +260,30 @@ int qlin_adapter_bwd(const void *dy, int dy_dtype, const int8_t *qg1, const floa
     const qlin::AdapterArgs g{a, b, w_dtype == QLIN_BF16, scale, ids, M, N, K, (int)L, (int)R};
     const qlin::AdapterEpilogue va =
         qlin::launch_adapter_bwd_v(g, dy, dy_dtype == QLIN_BF16, start, da, db, w.count, w.rest, s);
-    // The adapters' gradients come before the product: they read dY again, while
-    // the product with B has just left what fits of it in the infinity cache.
-    qlin::launch_adapter_bwd_w(g, dy, dy_dtype == QLIN_BF16, qx, sx, u, order, da, db, w.rest, s);
-    if (any && dx) {
-        qlin::ProductArgs p{QLIN_OP_DX, qg1, qw, M, N, K, sg1, nullptr, nullptr, dx, false};
-        if (qlin_product_ws_bytes(QLIN_OP_DX, M, N, K))
-            p.split_ws = w.product;
-        p.had = had_block;
-        p.had_scale = had_block ? hadamard_scale(had_block) : 1.0f;
-        qlin::launch_product_adapter(p, va, s);
-        if (had_block > 128)
-            qlin::launch_hadamard(dx, false, M, K, had_block, hadamard_scale(had_block), dx, s);
+    const bool bf = dy_dtype == QLIN_BF16;
+    if (!any || !dx) {
+        qlin::launch_adapter_bwd_w(g, dy, bf, qx, sx, u, order, da, db, nullptr, w.rest, s);
+        return finish();
     }
+    qlin::ProductArgs p{QLIN_OP_DX, qg1, qw, M, N, K, sg1, nullptr, nullptr, dx, false};
+    if (qlin_product_ws_bytes(QLIN_OP_DX, M, N, K))
+        p.split_ws = w.product;
+    const float cb = had_block ? hadamard_scale(had_block) : 1.0f;
+    if (qlin::adapter_term_apart(M, K)) {
+        // The product, then its term with the gradients.
+        qlin::launch_product(p, s);
+        const qlin::AdapterTermArgs term{va, M, K, dx, had_block >= 2 && had_block <= 128 ? had_block : 0, cb};
+        qlin::launch_adapter_bwd_w(g, dy, bf, qx, sx, u, order, da, db, &term, w.rest, s);
+    } else {
+        // The gradients come first: they read dY again, while the product with B
+        // has just left what fits of it in the infinity cache.
+        qlin::launch_adapter_bwd_w(g, dy, bf, qx, sx, u, order, da, db, nullptr, w.rest, s);
+        p.had = had_block;
+        p.had_scale = cb;
+        qlin::launch_product_adapter(p, va, s);
+    }
+    if (had_block > 128)
+        qlin::launch_hadamard(dx, false, M, K, had_block, cb, dx, s);
     return finish();
 }
 

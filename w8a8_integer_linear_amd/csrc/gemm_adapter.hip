@@ -50,15 +50,12 @@ void launch_product_adapter(const ProductArgs &a, const AdapterEpilogue &ad, hip
     }
     GemmParams p = gemm_params(a);
     p.ad = ad;
-    if (adapter_term_apart(p.R, p.S)) {
-        ProductArgs b = a;
-        b.had = 0;
-        launch_product(b, st);
-        launch_adapter_expand(ad, a.op == 1, p.R, p.S, a.had >= 2 && a.had <= 128 ? a.had : 0,
-                              a.had_scale, static_cast<float *>(a.out), st);
-        return;
-    }
     if (a.op == 0) {
+        if (adapter_term_apart(p.R, p.S)) {
+            launch_product(a, st);
+            launch_adapter_expand({ad, p.R, p.S, static_cast<float *>(a.out), 0, 1.0f}, st);
+            return;
+        }
         ad.bf16 ? run<false, EPI_FWD_ADAPTER_BF16>(p, st) : run<false, EPI_FWD_ADAPTER_F32>(p, st);
     } else {
         // (A block of 1: no rotation, or one that follows in a launch of its own.)

@@ -66,14 +66,22 @@ struct AdapterEpilogue {
     bool bf16;
 };
 // A forward or dX product (no workspace mode, contraction within the int32
-// bound) with that term added.
+// bound) with that term added; a dX product only where adapter_term_apart is
+// false.
 void launch_product_adapter(const ProductArgs &p, const AdapterEpilogue &ad, hipStream_t st);
 // Whether that term has a launch of its own, for outputs of this size.
 bool adapter_term_apart(int64_t rows, int64_t cols);
-// The term added to outputs [M, C] in memory, of a forward or (dx) of a dX
-// product, whose sums are then rotated in blocks of `had` (up to 128; 0: not).
-void launch_adapter_expand(const AdapterEpilogue &ad, bool dx, int64_t M, int64_t C, int had, float cb,
-                           float *out, hipStream_t st);
+// The term added to outputs [M, C] in memory: a forward product's in a launch of
+// its own; dX's, whose sums are then rotated in blocks of had (2 .. 128; 0: not),
+// with the adapters' gradients (launch_adapter_bwd_w).
+struct AdapterTermArgs {
+    AdapterEpilogue ad;
+    int64_t M, C;
+    float *out;
+    int had;
+    float cb;
+};
+void launch_adapter_expand(const AdapterTermArgs &e, hipStream_t st);
 
 // Whether the product kernels can address every operand byte of this shape
 // with their 32-bit buffer offsets (for contractions past the int32 bound,
@@ -176,6 +184,6 @@ AdapterEpilogue launch_adapter_bwd_v(const AdapterArgs &g, const void *dy, bool 
                                      void *ws, hipStream_t st);
 void launch_adapter_bwd_w(const AdapterArgs &g, const void *dy, bool dy_bf16, const int8_t *qx,
                           const float *sx, const float *u, const int32_t *order, float *da,
-                          float *db, void *ws, hipStream_t st);
+                          float *db, const AdapterTermArgs *dx, void *ws, hipStream_t st);
 
 } // namespace qlin
