@@ -13,6 +13,7 @@ import torch
 
 HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(HERE, "libqlin.so")
+MARSHAL_PATH = os.path.join(os.path.dirname(LIB_PATH), "_marshal.so")
 
 QLIN_OK, QLIN_EINVAL, QLIN_EUNSUPPORTED, QLIN_EDEVICE = 0, 1, 2, 3
 QLIN_F32, QLIN_BF16 = 0, 1
@@ -115,8 +116,8 @@ def _stream(stream):
     if stream is not None:
         return stream.cuda_stream
     # The current stream's handle, without the Stream object that
-    # torch.cuda.current_stream() makes (3 us of a call of 12).
-    return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device())
+    # torch.cuda.current_stream() makes (3 us).
+    return torch._C._cuda_getCurrentRawStream(torch._C._cuda_getDevice())
 
 
 def _need(t, name, dtype, shape=None):
@@ -132,6 +133,20 @@ def _need(t, name, dtype, shape=None):
     if not t.is_contiguous():
         raise ValueError(f"{name} must be contiguous")
     raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
+
+
+def _addr(*args):
+    """_addr(t, name, dtype, *shape): the address of a tensor that _need accepts (no
+    sizes: of any shape), checked by compiled code; _need raises for others."""
+    global _addr
+    if not os.path.exists(MARSHAL_PATH):
+        raise ImportError(
+            f"{MARSHAL_PATH} is missing: build it with `python -c 'import __graft_entry__ as g; "
+            "g.build()'`")
+    from . import _marshal
+    _marshal.set_refuse(_need)
+    _addr = _marshal.address
+    return _addr(*args)
 
 
 def _opt(t, name, dtype, shape):
@@ -430,15 +445,14 @@ def _on_stream(f):
 
 
 def _workspace(workspace, need, like, zero):
-    """A call's workspace: the caller's, or a fresh one."""
+    """A call's workspace: the caller's, or a fresh one of need() bytes.  Returns
+    (tensor, address, bytes)."""
     if workspace is None:
-        make = torch.zeros if zero else torch.empty
-        return make(need, dtype=torch.uint8, device=like.device) if need else None
-    return _need(workspace, "workspace", torch.uint8)
-
-
-def _bytes(workspace):
-    return 0 if workspace is None else workspace.numel()
+        n = need()
+        if not n:
+            return None, None, 0
+        workspace = (torch.zeros if zero else torch.empty)(n, dtype=torch.uint8, device=like.device)
+    return workspace, _addr(workspace, "workspace", torch.uint8), workspace.numel()
 
 
 @_on_stream
@@ -448,23 +462,25 @@ def qlin_rmsnorm_quant(x, gamma, eps, residual=None, had_block=0, h=None, q=None
     (q, s, h, rstd, y): h is x itself without a residual, y (bf16 values of the
     codes) None unless given or wanted."""
     rows, cols = x.shape
-    _need(x, "x", x.dtype)
-    code = _dtype_code(x)
-    _need(gamma, "gamma", torch.float32, (cols,))
+    code, dtype = _dtype_code(x), x.dtype
+    px = _addr(x, "x", dtype)
+    pg = _addr(gamma, "gamma", torch.float32, cols)
+    pr = ph = py = None
     if residual is not None:
-        _need(residual, "residual", x.dtype, (rows, cols))
-        h = _empty((rows, cols), x.dtype, x) if h is None else _need(h, "h", x.dtype, (rows, cols))
-    q = _empty((rows, cols), torch.int8, x) if q is None else _need(q, "q", torch.int8, (rows, cols))
-    s = _empty((rows,), torch.float32, x) if s is None else _need(s, "s", torch.float32, (rows,))
-    rstd = (_empty((rows,), torch.float32, x) if rstd is None
-            else _need(rstd, "rstd", torch.float32, (rows,)))
+        pr = _addr(residual, "residual", dtype, rows, cols)
+        h = _empty((rows, cols), dtype, x) if h is None else h
+        ph = _addr(h, "h", dtype, rows, cols)
+    q = _empty((rows, cols), torch.int8, x) if q is None else q
+    s = _empty((rows,), torch.float32, x) if s is None else s
+    rstd = _empty((rows,), torch.float32, x) if rstd is None else rstd
     if y is None and want_y:
         y = _empty((rows, cols), torch.bfloat16, x)
-    _opt(y, "y", torch.bfloat16, (rows, cols))
+    if y is not None:
+        py = _addr(y, "y", torch.bfloat16, rows, cols)
     _check("qlin_rmsnorm_quant", lib().qlin_rmsnorm_quant(
-        _ptr(x), _ptr(residual), code, rows, cols, _ptr(gamma), float(eps), int(had_block),
-        None if residual is None else _ptr(h), _ptr(q), _ptr(s), _ptr(rstd), _ptr(y),
-        _stream(stream)))
+        px, pr, code, rows, cols, pg, float(eps), int(had_block), ph,
+        _addr(q, "q", torch.int8, rows, cols), _addr(s, "s", torch.float32, rows),
+        _addr(rstd, "rstd", torch.float32, rows), py, _stream(stream)))
     return q, s, x if residual is None else h, rstd, y
 
 
@@ -477,29 +493,29 @@ def qlin_rmsnorm_bwd(dn, h, rstd, gamma, dres=None, dh=None, dgamma=None, worksp
                      stream=None):
     """Backward of the norm.  Returns (dh, dgamma)."""
     rows, cols = h.shape
-    _need(dn, "dn", dn.dtype, (rows, cols))
-    _need(h, "h", h.dtype)
+    dtype = h.dtype
+    pn, ph = _addr(dn, "dn", dn.dtype, rows, cols), _addr(h, "h", dtype)
     dn_code, code = _dtype_code(dn), _dtype_code(h)
-    _need(rstd, "rstd", torch.float32, (rows,))
-    _need(gamma, "gamma", torch.float32, (cols,))
-    _opt(dres, "dres", h.dtype, (rows, cols))
-    dh = _empty((rows, cols), h.dtype, h) if dh is None else _need(dh, "dh", h.dtype, (rows, cols))
-    dgamma = (_empty((cols,), torch.float32, h) if dgamma is None
-              else _need(dgamma, "dgamma", torch.float32, (cols,)))
-    workspace = _workspace(workspace, qlin_rmsnorm_bwd_ws_bytes(rows, cols), h, zero=False)
+    pr = _addr(rstd, "rstd", torch.float32, rows)
+    pg = _addr(gamma, "gamma", torch.float32, cols)
+    pd = None if dres is None else _addr(dres, "dres", dtype, rows, cols)
+    dh = _empty((rows, cols), dtype, h) if dh is None else dh
+    dgamma = _empty((cols,), torch.float32, h) if dgamma is None else dgamma
+    po, pq = _addr(dh, "dh", dtype, rows, cols), _addr(dgamma, "dgamma", torch.float32, cols)
+    workspace, pw, size = _workspace(workspace, lambda: qlin_rmsnorm_bwd_ws_bytes(rows, cols), h,
+                                     zero=False)
     _check("qlin_rmsnorm_bwd", lib().qlin_rmsnorm_bwd(
-        _ptr(dn), dn_code, _ptr(h), _ptr(dres), code, _ptr(rstd), _ptr(gamma), rows, cols,
-        _ptr(dh), _ptr(dgamma), _ptr(workspace), _bytes(workspace), _stream(stream)))
+        pn, dn_code, ph, pd, code, pr, pg, rows, cols, po, pq, pw, size, _stream(stream)))
     return dh, dgamma
 
 
 def _adapters(a, b, scale, ids, M, N, K):
+    """(L, R, type code, addresses of a, b, scale and ids)"""
     L, R = a.shape[:2]
-    _need(a, "a", a.dtype, (L, R, K))
-    _need(b, "b", a.dtype, (L, N, R))
-    _need(scale, "scale", torch.float32, (L,))
-    _need(ids, "ids", torch.int32, (M,))
-    return L, R, _dtype_code(a)
+    dtype = a.dtype
+    pa, pb = _addr(a, "a", dtype, L, R, K), _addr(b, "b", dtype, L, N, R)
+    return (L, R, _dtype_code(a), pa, pb, _addr(scale, "scale", torch.float32, L),
+            _addr(ids, "ids", torch.int32, M))
 
 
 def qlin_adapter_fwd_ws_bytes(M, N, K, L, R):
@@ -512,19 +528,17 @@ def qlin_adapter_fwd(qx, sx, qw, sw, a, b, scale, ids, bias=None, y=None, u=None
     """The shared projection with each token's adapter.  Returns (y, u)."""
     M, K = qx.shape
     N = qw.shape[0]
-    _need(qx, "qx", torch.int8)
-    _need(qw, "qw", torch.int8, (N, K))
-    _need(sx, "sx", torch.float32, (M,))
-    _need(sw, "sw", torch.float32, (N,))
-    _opt(bias, "bias", torch.float32, (N,))
-    L, R, code = _adapters(a, b, scale, ids, M, N, K)
-    y = _empty((M, N), torch.float32, qx) if y is None else _need(y, "y", torch.float32, (M, N))
-    u = _empty((M, R), torch.float32, qx) if u is None else _need(u, "u", torch.float32, (M, R))
-    workspace = _workspace(workspace, 0 if workspace is not None else
-                           qlin_adapter_fwd_ws_bytes(M, N, K, L, R), qx, zero=True)
+    px, pw = _addr(qx, "qx", torch.int8), _addr(qw, "qw", torch.int8, N, K)
+    psx, psw = _addr(sx, "sx", torch.float32, M), _addr(sw, "sw", torch.float32, N)
+    pbias = None if bias is None else _addr(bias, "bias", torch.float32, N)
+    L, R, code, pa, pb, ps, pi = _adapters(a, b, scale, ids, M, N, K)
+    y = _empty((M, N), torch.float32, qx) if y is None else y
+    u = _empty((M, R), torch.float32, qx) if u is None else u
+    py, pu = _addr(y, "y", torch.float32, M, N), _addr(u, "u", torch.float32, M, R)
+    workspace, pws, size = _workspace(workspace, lambda: qlin_adapter_fwd_ws_bytes(M, N, K, L, R),
+                                      qx, zero=True)
     _check("qlin_adapter_fwd", lib().qlin_adapter_fwd(
-        _ptr(qx), _ptr(sx), _ptr(qw), _ptr(sw), _ptr(bias), _ptr(a), _ptr(b), code, _ptr(scale),
-        _ptr(ids), M, N, K, L, R, _ptr(u), _ptr(y), _ptr(workspace), _bytes(workspace),
+        px, psx, pw, psw, pbias, pa, pb, code, ps, pi, M, N, K, L, R, pu, py, pws, size,
         _stream(stream)))
     return y, u
 
@@ -534,13 +548,12 @@ def qlin_adapter_group(ids, L, order=None, start=None, stream=None):
     """Tokens grouped by adapter, for qlin_adapter_bwd.  Returns (order, start)."""
     M, = ids.shape
     L = int(L)
-    _need(ids, "ids", torch.int32)
-    order = (_empty((M,), torch.int32, ids) if order is None
-             else _need(order, "order", torch.int32, (M,)))
-    start = (_empty((L + 1,), torch.int32, ids) if start is None
-             else _need(start, "start", torch.int32, (L + 1,)))
+    pi = _addr(ids, "ids", torch.int32)
+    order = _empty((M,), torch.int32, ids) if order is None else order
+    start = _empty((L + 1,), torch.int32, ids) if start is None else start
     _check("qlin_adapter_group", lib().qlin_adapter_group(
-        _ptr(ids), M, L, _ptr(order), _ptr(start), _stream(stream)))
+        pi, M, L, _addr(order, "order", torch.int32, M), _addr(start, "start", torch.int32, L + 1),
+        _stream(stream)))
     return order, start
 
 
@@ -555,33 +568,27 @@ def qlin_adapter_bwd(dy, qg1, sg1, qw, qx, sx, u, a, b, scale, ids, order, start
     Returns (dx, da, db); dx is None with want_dx=False."""
     M, N = dy.shape
     K = qx.shape[1]
-    _need(dy, "dy", dy.dtype)
-    dy_code = _dtype_code(dy)
-    _need(qx, "qx", torch.int8, (M, K))
-    _need(sx, "sx", torch.float32, (M,))
-    L, R, code = _adapters(a, b, scale, ids, M, N, K)
-    _need(u, "u", torch.float32, (M, R))
-    _need(order, "order", torch.int32, (M,))
-    _need(start, "start", torch.int32, (L + 1,))
+    pdy, dy_code = _addr(dy, "dy", dy.dtype), _dtype_code(dy)
+    px, psx = _addr(qx, "qx", torch.int8, M, K), _addr(sx, "sx", torch.float32, M)
+    L, R, code, pa, pb, ps, pi = _adapters(a, b, scale, ids, M, N, K)
+    pu = _addr(u, "u", torch.float32, M, R)
+    po, pst = _addr(order, "order", torch.int32, M), _addr(start, "start", torch.int32, L + 1)
+    pg = psg = pw = pdx = None
     if want_dx:
-        _need(qg1, "qg1", torch.int8, (M, N))
-        _need(sg1, "sg1", torch.float32, (M,))
-        _need(qw, "qw", torch.int8, (N, K))
-        dx = (_empty((M, K), torch.float32, dy) if dx is None
-              else _need(dx, "dx", torch.float32, (M, K)))
+        pg, psg = _addr(qg1, "qg1", torch.int8, M, N), _addr(sg1, "sg1", torch.float32, M)
+        pw = _addr(qw, "qw", torch.int8, N, K)
+        dx = _empty((M, K), torch.float32, dy) if dx is None else dx
+        pdx = _addr(dx, "dx", torch.float32, M, K)
     else:
-        qg1 = sg1 = qw = dx = None
-    da = (_empty((L, R, K), torch.float32, dy) if da is None
-          else _need(da, "da", torch.float32, (L, R, K)))
-    db = (_empty((L, N, R), torch.float32, dy) if db is None
-          else _need(db, "db", torch.float32, (L, N, R)))
-    workspace = _workspace(workspace, 0 if workspace is not None else
-                           qlin_adapter_bwd_ws_bytes(M, N, K, L, R), dy, zero=True)
+        dx = None
+    da = _empty((L, R, K), torch.float32, dy) if da is None else da
+    db = _empty((L, N, R), torch.float32, dy) if db is None else db
+    pda, pdb = _addr(da, "da", torch.float32, L, R, K), _addr(db, "db", torch.float32, L, N, R)
+    workspace, pws, size = _workspace(workspace, lambda: qlin_adapter_bwd_ws_bytes(M, N, K, L, R),
+                                      dy, zero=True)
     _check("qlin_adapter_bwd", lib().qlin_adapter_bwd(
-        _ptr(dy), dy_code, _ptr(qg1), _ptr(sg1), _ptr(qw), _ptr(qx), _ptr(sx), _ptr(u), _ptr(a),
-        _ptr(b), code, _ptr(scale), _ptr(ids), _ptr(order), _ptr(start), M, N, K, L, R,
-        int(had_block), _ptr(dx), _ptr(da), _ptr(db), _ptr(workspace), _bytes(workspace),
-        _stream(stream)))
+        pdy, dy_code, pg, psg, pw, px, psx, pu, pa, pb, code, ps, pi, po, pst, M, N, K, L, R,
+        int(had_block), pdx, pda, pdb, pws, size, _stream(stream)))
     return dx, da, db
 
 

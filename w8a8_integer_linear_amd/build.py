@@ -1,4 +1,5 @@
-"""Builds libqlin.so (the HIP kernels and the C ABI) for gfx950 with hipcc.
+"""Builds libqlin.so (the HIP kernels and the C ABI) for gfx950 with hipcc, and
+_marshal.so (the binding's argument checks) with the host compiler.
 
 Every source is compiled to an object in parallel, then linked into a shared
 library next to this file.  Flags: IEEE fp32 arithmetic without contraction
@@ -9,11 +10,13 @@ import concurrent.futures as cf
 import os
 import shutil
 import subprocess
+import sysconfig
 
 HERE = os.path.dirname(os.path.abspath(__file__))
 CSRC = os.path.join(HERE, "csrc")
 ROOT = os.path.dirname(HERE)
 LIB = os.path.join(HERE, "libqlin.so")
+MARSHAL = os.path.join(HERE, "_marshal.so")
 BUILD_DIR = os.path.join(ROOT, "_build")
 SOURCES = ["api.hip", "api_around.hip", "quant.hip", "gemm.hip", "gemm_adapter.hip", "sgd.hip",
            "norm.hip", "adapter.hip", "adamw.hip", "stream.hip", "mfma_ceiling.hip"]
@@ -45,11 +48,32 @@ def _compile(src, verbose):
     return obj
 
 
+def _build_marshal(verbose):
+    import torch
+    from torch.utils import cpp_extension
+    libs = os.path.join(os.path.dirname(torch.__file__), "lib")
+    tmp = MARSHAL + ".tmp"
+    cmd = [shutil.which("g++") or "c++", "-O2", "-std=c++17", "-fPIC", "-shared", "-Wall",
+           f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}",
+           f"-I{sysconfig.get_paths()['include']}",
+           *[f"-isystem{p}" for p in cpp_extension.include_paths()],
+           os.path.join(CSRC, "marshal.cpp"), f"-L{libs}", "-ltorch_python", "-ltorch_cpu", "-lc10",
+           "-o", tmp]
+    if verbose:
+        print(" ".join(cmd), flush=True)
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError(f"g++ failed on marshal.cpp:\n{r.stdout}\n{r.stderr}")
+    os.replace(tmp, MARSHAL)
+
+
 def build(verbose=False):
-    """Compile and link libqlin.so (always rebuilds)."""
+    """Compile and link libqlin.so and _marshal.so (always rebuilds)."""
     os.makedirs(BUILD_DIR, exist_ok=True)
     with cf.ThreadPoolExecutor(max_workers=min(len(SOURCES), 8)) as ex:
+        marshal = ex.submit(_build_marshal, verbose)
         objs = list(ex.map(lambda s: _compile(s, verbose), SOURCES))
+        marshal.result()
     tmp = LIB + ".tmp"
     cmd = [hipcc(), f"--offload-arch={ARCH}", "-shared", "-fPIC", *objs, "-o", tmp]
     if verbose:

@@ -1,0 +1,93 @@
+// The binding's argument checks, compiled: a call of few tokens takes the GPU
+// less time than a dozen tensors' checks take the interpreter (the projection
+// with adapters at seven tokens: 8.8 us of host time per call instead of 12.7 us).
+#define PY_SSIZE_T_CLEAN
+#include <Python.h>
+
+#include <torch/csrc/Dtype.h>
+#include <torch/csrc/autograd/python_variable.h>
+
+namespace {
+
+PyObject *refuse = nullptr;     // the binding's own check, which names the fault
+
+// The address of a contiguous GPU tensor of this dtype and, if any sizes are
+// given, of this shape; false if it is not one.
+bool fits(PyObject *o, PyObject *dtype, PyObject *const *dims, Py_ssize_t n, const void *&address)
+{
+    if (!THPVariable_Check(o) || !THPDtype_Check(dtype))
+        return false;
+    const at::Tensor &t = THPVariable_Unpack(o);
+    if (!t.is_cuda() || t.layout() != at::kStrided ||
+        t.scalar_type() != reinterpret_cast<THPDtype *>(dtype)->scalar_type || !t.is_contiguous())
+        return false;
+    if (n > 0) {
+        if (t.dim() != n)
+            return false;
+        for (Py_ssize_t i = 0; i < n; i++) {
+            const long long d = PyLong_AsLongLong(dims[i]);
+            if (d != t.size(i)) {
+                PyErr_Clear();
+                return false;
+            }
+        }
+    }
+    address = t.const_data_ptr();
+    return true;
+}
+
+// address(tensor, name, dtype, *sizes)
+PyObject *address(PyObject *, PyObject *const *args, Py_ssize_t n)
+{
+    if (n < 3) {
+        PyErr_SetString(PyExc_TypeError, "address(tensor, name, dtype, *sizes)");
+        return nullptr;
+    }
+    try {
+        const void *p = nullptr;
+        if (fits(args[0], args[2], args + 3, n - 3, p))
+            return PyLong_FromVoidPtr(const_cast<void *>(p));
+    } catch (const std::exception &e) {
+        PyErr_SetString(PyExc_RuntimeError, e.what());
+        return nullptr;
+    }
+    PyObject *shape = Py_None;
+    Py_INCREF(shape);
+    if (n > 3) {
+        Py_DECREF(shape);
+        shape = PyTuple_New(n - 3);
+        if (!shape)
+            return nullptr;
+        for (Py_ssize_t i = 3; i < n; i++) {
+            Py_INCREF(args[i]);
+            PyTuple_SET_ITEM(shape, i - 3, args[i]);
+        }
+    }
+    PyObject *r = PyObject_CallFunctionObjArgs(refuse, args[0], args[1], args[2], shape, nullptr);
+    Py_DECREF(shape);
+    if (r) {
+        Py_DECREF(r);
+        PyErr_SetString(PyExc_ValueError, "unsupported tensor");
+    }
+    return nullptr;
+}
+
+PyObject *set_refuse(PyObject *, PyObject *f)
+{
+    Py_INCREF(f);
+    Py_XSETREF(refuse, f);
+    Py_RETURN_NONE;
+}
+
+PyMethodDef methods[] = {
+    {"address", reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(address)), METH_FASTCALL,
+     "address(tensor, name, dtype, *sizes)"},
+    {"set_refuse", set_refuse, METH_O, "set_refuse(function)"},
+    {nullptr, nullptr, 0, nullptr},
+};
+PyModuleDef module = {PyModuleDef_HEAD_INIT, "_marshal", nullptr, -1, methods,
+                      nullptr, nullptr, nullptr, nullptr};
+
+} // namespace
+
+PyMODINIT_FUNC PyInit__marshal() { return PyModule_Create(&module); }
