@@ -1,9 +1,10 @@
 """Low-rank adapters beside the shared projection, forward and backward, against
 the formulas in 64 bits.
 
-Bounds: an fp32 operand is kept to 2^-17 (two bf16 terms), a product of two such
-to 2^-15 with the dropped lo lo; a sum of n terms is within n 2^-24 of the terms'
-magnitudes.  The magnitudes go through the same products with absolute values."""
+Bounds: an fp32 operand kept to 2^-17 or better (two bf16 terms; the kernels use
+three), a product of two such to 2^-15 with the dropped lo lo; a sum of n terms is
+within n 2^-24 of the terms' magnitudes.  The magnitudes go through the same
+products with absolute values."""
 import pytest
 
 from tests.gpu_util import announce, torch_cuda
