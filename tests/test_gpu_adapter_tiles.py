@@ -28,6 +28,12 @@ def test_backward(M, N, K, L, R, had, w, dy):
     small.test_backward(M, N, K, L, R, had, w, dy)
 
 
+@pytest.mark.parametrize("dy", ["f32", "bf16"])
+def test_backward_of_many_ranks(dy):
+    """Enough tokens and ranks that 32 ranks share the read of dY."""
+    small.test_backward(4112, 64, 2064, 2, 128, 16, "bf16", dy)
+
+
 @pytest.mark.parametrize("w", ["f32", "bf16"])
 def test_backward_of_mixed_tokens(w):
     """Every 16-token block of the product holds several adapters."""

@@ -410,8 +410,11 @@ template <int W> __global__ __launch_bounds__(256) void adapter_shrink_few_kerne
     }
 }
 
-// Most tokens of the kernel above: it reads an adapter once per token.
-constexpr int64_t kFewTokens = 32;
+// Most waves (tokens times ranks) of the kernel above, which reads an adapter once
+// per token, but all adapters at once (4096 codes, eight adapters in bf16: 64
+// tokens of rank 16, 35 us for the call against 42 us; 64 of rank 64, 43 us
+// against 48 us; 512 of rank 16, 41 us against 39 us).
+constexpr int64_t kFewWaves = 4096;
 
 // Workgroups that a product of fewer units (32 tokens by a group of ranks) than
 // compute units is split up to, fewest stages of a split's, and most units that
@@ -447,16 +450,18 @@ template <int X, int W, int RB> void go_shrink(ShrinkArgs a, hipStream_t st)
 template <int X, int W> void run_shrink(const ShrinkArgs &a, hipStream_t st)
 {
     if constexpr (X == X_I8) {
-        if (a.M <= kFewTokens) {
+        if (a.M * a.R <= kFewWaves) {
             hipLaunchKernelGGL(adapter_shrink_few_kernel<W>, dim3((unsigned)(a.M * a.R / 4)), dim3(256), 0,
                                st, a);
             return;
         }
     }
-    // Ranks above 16 share x's stage where w's fits beside it, unless that
-    // leaves compute units without a workgroup.
+    // 32 ranks share x's stage where w's fits beside it and two workgroups per
+    // compute unit are left (5376 codes, bf16, a product of 16 columns: 12000
+    // tokens of rank 64, 80 us for the call against 89 us; 4200 of rank 64, 62 us
+    // against 60 us; 12000 of rank 32, 68 us against 67 us).
     if constexpr (W == X_BF16) {
-        if (a.R > 16 && a.M >= 32 * 128)
+        if ((a.M + 31) / 32 * ((a.R + 31) / 32) >= 2 * kCus)
             return go_shrink<X, W, 2>(a, st);
     }
     go_shrink<X, W, 1>(a, st);

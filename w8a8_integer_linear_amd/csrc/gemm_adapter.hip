@@ -25,9 +25,9 @@ template <bool BKM, int EPI> void run(GemmParams &p, hipStream_t st)
 } // namespace
 
 // Few tiles: added in the epilogues, the term would be the work of as few compute
-// units (333 tokens, 4096 x 4096, rank 64 in fp32: 147 us for the backward call
-// against 125 us with the term in a launch of its own; 611 tokens, 4096 -> 14336,
-// rank 32, 168 tiles: 72 us against 90 us).
+// units (backward of 333 tokens, 4096 x 4096, rank 64 in fp32: 141 us against 77
+// us with the term apart; forward of 611 tokens, 4096 -> 14336, rank 32, 168
+// tiles: 73 us against 98 us).
 bool adapter_term_apart(int64_t rows, int64_t cols)
 {
     return ((rows + 255) / 256) * ((cols + 255) / 256) < 128;
