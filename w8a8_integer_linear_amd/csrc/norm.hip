@@ -8,7 +8,7 @@
 // the row's two reductions (the sum of squares, the absmax) run across lanes.
 // HBM traffic bounds it, except for a few rows, where the launch does: 12000 rows
 // of 5376 in fp32 with a residual and the codes' values as bf16 beside them, 968
-// MB, take 174 us (5.6 TB/s); 3 rows of 4096 take 3.4 us in the kernel and 8.4 us
+// MB, take 174 us (5.6 TB/s); 3 rows of 4096 take 3.4 us in the kernel and 5.6 us
 // as a call.
 //
 // Backward, one row, with xh = h * rstd and g = dn * gamma: dh = dres + rstd
