@@ -254,6 +254,11 @@ void run_norm_dt(const NormArgs &a, hipStream_t st)
         run_norm_h<BF16, -1>(a, st);
 }
 
+// Rows of one launch with up to 1024 threads each: a grid's dimension holds fewer
+// than 2^32 threads (a larger one starts only what is left of it modulo 2^32, and
+// reports no error).
+constexpr int64_t kLaunchRows = (int64_t)1 << 21;
+
 // --------------------------------------------------------------- backward
 
 struct NormBwdArgs {
@@ -483,11 +488,20 @@ void launch_rmsnorm_quant(const void *x, const void *res, bool bf16, int64_t row
                           const float *gamma, float eps, int had, float cb, void *h, int8_t *q,
                           float *s, float *rstd, void *y, hipStream_t st)
 {
-    const NormArgs a{x, res, rows, cols, gamma, eps, had, cb, h, q, s, rstd, static_cast<uint16_t *>(y)};
-    if (bf16)
-        run_norm_dt<true>(a, st);
-    else
-        run_norm_dt<false>(a, st);
+    const int64_t size = bf16 ? 2 : 4;
+    auto from = [](auto *p, int64_t byte) {
+        return p ? (decltype(p))((uintptr_t)p + (uintptr_t)byte) : p;
+    };
+    for (int64_t r0 = 0; r0 < rows; r0 += kLaunchRows) {
+        const int64_t n = rows - r0 < kLaunchRows ? rows - r0 : kLaunchRows, at = r0 * cols;
+        const NormArgs a{from(x, at * size), from(res, at * size), n, cols, gamma, eps, had, cb,
+                         from(h, at * size), q + at, s + r0, rstd + r0,
+                         static_cast<uint16_t *>(from(y, at * 2))};
+        if (bf16)
+            run_norm_dt<true>(a, st);
+        else
+            run_norm_dt<false>(a, st);
+    }
 }
 
 // Rows of partial column sums that a backward call writes.
