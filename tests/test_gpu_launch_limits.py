@@ -24,3 +24,37 @@ def test_norm_of_2_24_rows():
                                        want_y=True)
         for a, b in zip(got, want):
             assert torch.equal(a[part], b)
+
+
+def test_norm_backward_of_2_22_long_rows():
+    """(69 GB each for h, which serves as dn too, and dh.)"""
+    torch = torch_cuda()
+    import w8a8_integer_linear_amd as qlin
+    rows, cols = (1 << 22) + 3, 8208
+    if torch.cuda.mem_get_info()[0] < 180 << 30:
+        pytest.skip("needs 180 GB of the card's memory")
+    announce("rmsnorm_bwd", rows, cols)
+    g = torch.Generator(device="cuda").manual_seed(1)
+    piece = torch.randn((1 << 14, cols), generator=g, device="cuda").to(torch.bfloat16)
+    h = torch.empty((rows, cols), dtype=torch.bfloat16, device="cuda")
+    rstd = torch.empty(rows, device="cuda")
+    for at in range(0, rows, 1 << 14):
+        n = min(1 << 14, rows - at)
+        h[at:at + n] = piece[:n]
+        rstd[at:at + n] = torch.rand(n, generator=g, device="cuda") + 0.5
+    gamma = torch.rand(cols, generator=g, device="cuda") + 0.5
+    dh, dgamma = qlin.qlin_rmsnorm_bwd(h, h, rstd, gamma)
+    for at in (0, (1 << 21) - 5, 1 << 21, (1 << 22) - 5, rows - 5):
+        part = h[at:at + 5]
+        want, _ = qlin.qlin_rmsnorm_bwd(part, part, rstd[at:at + 5].clone(), gamma)
+        assert torch.equal(dh[at:at + 5], want)
+    # The sum over the rows, whose pieces repeat: terms of one sign, added by 64
+    # runs of rows one after another and then the 64.
+    scale = torch.zeros(1 << 14, dtype=torch.float64, device="cuda")
+    for at in range(0, rows, 1 << 14):
+        n = min(1 << 14, rows - at)
+        scale[:n] += rstd[at:at + n]
+    want = (piece.double().square() * scale[:, None]).sum(0)
+    assert ((dgamma - want).abs() <= want * (rows / 64 + 64 + 4) * 2.0 ** -24).all()
+    del h, dh
+    torch.cuda.empty_cache()

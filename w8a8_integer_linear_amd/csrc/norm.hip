@@ -365,12 +365,13 @@ __global__ __launch_bounds__(256, 2) void rmsnorm_bwd_kernel(NormBwdArgs a)
 }
 
 // Rows too long for the kernel above: each row is read twice (its dot
-// product, then dh), and the column sums are a pass of their own.
+// product, then dh), and the column sums are a pass of their own.  Workgroup i
+// has row r0 + i.
 template <bool DNBF, bool BF16>
-__global__ __launch_bounds__(1024) void rmsnorm_bwd_long_kernel(NormBwdArgs a)
+__global__ __launch_bounds__(1024) void rmsnorm_bwd_long_kernel(NormBwdArgs a, int64_t r0)
 {
     __shared__ float red[16];
-    const int64_t nch = a.cols / 8, row = blockIdx.x, base = row * a.cols;
+    const int64_t nch = a.cols / 8, row = r0 + blockIdx.x, base = row * a.cols;
     const float rstd = a.rstd[row];
     float dot = 0.0f;
     for (int64_t c = threadIdx.x; c < nch; c += 1024) {
@@ -476,8 +477,11 @@ void run_bwd(const NormBwdArgs &a, int n, hipStream_t st)
         }
         return;
     }
-    hipLaunchKernelGGL((rmsnorm_bwd_long_kernel<DNBF, BF16>), dim3((unsigned)a.rows), dim3(1024), 0, st,
-                       a);
+    for (int64_t r0 = 0; r0 < a.rows; r0 += kLaunchRows) {
+        const int64_t rows = a.rows - r0 < kLaunchRows ? a.rows - r0 : kLaunchRows;
+        hipLaunchKernelGGL((rmsnorm_bwd_long_kernel<DNBF, BF16>), dim3((unsigned)rows), dim3(1024), 0, st,
+                           a, r0);
+    }
     hipLaunchKernelGGL((rmsnorm_dgamma_kernel<DNBF, BF16>),
                        dim3((unsigned)((a.cols / 8 + 255) / 256), (unsigned)n), dim3(256), 0, st, a);
 }
