@@ -1,5 +1,7 @@
 """Row and chunk counts whose threads no single launch can hold (2^32 per grid
 dimension): the calls around the projection answer them like any other."""
+import ctypes
+
 import pytest
 
 from tests.gpu_util import announce, torch_cuda
@@ -58,3 +60,32 @@ def test_norm_backward_of_2_22_long_rows():
     assert ((dgamma - want).abs() <= want * (rows / 64 + 64 + 4) * 2.0 ** -24).all()
     del h, dh
     torch.cuda.empty_cache()
+
+
+def test_adamw_of_2_24_chunks():
+    """A list of 2^24 + 3 chunks.  The image says so by hand: its second tensor has
+    the last chunk, its first one all the others, of which only the first lies
+    within the memory that the first tensor's size admits."""
+    torch = torch_cuda()
+    import w8a8_integer_linear_amd as qlin
+    from w8a8_integer_linear_amd import _native
+    chunks = (1 << 24) + 3
+    announce("adamw_tensors", chunks)
+    g = torch.Generator(device="cuda").manual_seed(1)
+    ts = [dict(p=torch.randn(n, generator=g, device="cuda"), g=torch.randn(n, generator=g, device="cuda"),
+               m=torch.zeros(n, device="cuda"), v=torch.zeros(n, device="cuda")) for n in (4096, 1000)]
+    want = [{k: t.clone() for k, t in d.items()} for d in ts]
+    plan, small = qlin.qlin_adamw_tensors_plan(ts), qlin.qlin_adamw_tensors_plan(want)
+    image = torch.zeros(2 * 80 + 4 * chunks, dtype=torch.uint8, device="cuda")
+    image[:160] = plan.image[:160]
+    entry = image[80:160].cpu()
+    ctypes.c_int64.from_address(entry.data_ptr() + 64).value = chunks - 1      # its first chunk
+    image[80:160] = entry.cuda()
+    image[-4:] = torch.tensor([1, 0, 0, 0], dtype=torch.uint8, device="cuda")
+    step = (1e-3, 0.9, 0.999, 1e-8, 1, 1)
+    _native._check("qlin_adamw_tensors", _native.lib().qlin_adamw_tensors(
+        image.data_ptr(), 2, chunks, *step, _native._stream(None)))
+    qlin.qlin_adamw_tensors(small, *step)
+    for a, b in zip(ts, want):
+        for k in "pmv":
+            assert torch.equal(a[k], b[k])

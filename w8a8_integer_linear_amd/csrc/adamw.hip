@@ -41,6 +41,7 @@ struct StepArgs {
     const int32_t *chunk_tensor;
     float b1, b2, eps, a1, a2, c1, c2, lr;
     uint32_t seed_lo, seed_hi, step_lo, step_hi;
+    uint32_t chunk0;        // the launch's first chunk
 };
 
 // Eight e4m3 codes at a byte pointer (8-byte aligned) as floats.
@@ -373,8 +374,9 @@ __device__ __forceinline__ void step_either(const StepArgs &a, const TensorEntry
 
 __global__ __launch_bounds__(256) void adamw_tensors_kernel(StepArgs a)
 {
-    const TensorEntry t = a.tensors[a.chunk_tensor[blockIdx.x]];
-    const int64_t c0 = ((int64_t)blockIdx.x - t.chunk0) * kTensorChunk;
+    const uint32_t chunk = a.chunk0 + blockIdx.x;
+    const TensorEntry t = a.tensors[a.chunk_tensor[chunk]];
+    const int64_t c0 = ((int64_t)chunk - t.chunk0) * kTensorChunk;
     switch (t.flags) {
     case 0: return step_either<false, false, false>(a, t, c0);
     case 1: return step_either<true, false, false>(a, t, c0);
@@ -407,7 +409,13 @@ void launch_adamw_tensors(const void *image, int64_t count, int64_t chunks, cons
     a.seed_hi = (uint32_t)(seed >> 32);
     a.step_lo = (uint32_t)step;
     a.step_hi = (uint32_t)(step >> 32);
-    hipLaunchKernelGGL(adamw_tensors_kernel, dim3((unsigned)chunks), dim3(256), 0, st, a);
+    // Chunks of one launch: a grid's dimension holds fewer than 2^32 threads.
+    constexpr int64_t kLaunchChunks = (int64_t)1 << 23;
+    for (int64_t c = 0; c < chunks; c += kLaunchChunks) {
+        const int64_t n = chunks - c < kLaunchChunks ? chunks - c : kLaunchChunks;
+        a.chunk0 = (uint32_t)c;
+        hipLaunchKernelGGL(adamw_tensors_kernel, dim3((unsigned)n), dim3(256), 0, st, a);
+    }
 }
 
 } // namespace qlin
