@@ -514,6 +514,7 @@ size_t qlin_rmsnorm_bwd_ws_bytes(int64_t rows, int64_t cols);
 #define QLIN_MAX_RANK 128
 #define QLIN_MAX_ADAPTERS 1023          /* of the grouped and backward calls */
 #define QLIN_MAX_ADAPTER_ROWS 1048560
+#define QLIN_MAX_ADAPTER_SIZE 17179852800   /* of the backward call: see there */
 int qlin_adapter_fwd(const int8_t *qx, const float *sx, const int8_t *qw, const float *sw,
                      const float *bias, const void *a, const void *b, int w_dtype,
                      const float *scale, const int32_t *ids, int64_t M, int64_t N, int64_t K,
@@ -545,7 +546,8 @@ int qlin_adapter_group(const int32_t *ids, int64_t M, int64_t L, int32_t *order,
  *          gave them for the same ids.
  *   dx     may be NULL (then qg1, sg1 and qw may be too): adapter gradients only.
  * The sums over tokens are fp32, in a fixed order.  Limits as in the forward
- * call, L <= QLIN_MAX_ADAPTERS; had_block as in qlin_bwd_dx.
+ * call, L <= QLIN_MAX_ADAPTERS; R, rounded up to a multiple of 32, times N + K at
+ * most QLIN_MAX_ADAPTER_SIZE; had_block as in qlin_bwd_dx.
  * workspace: qlin_adapter_bwd_ws_bytes bytes, under the same rules.
  */
 int qlin_adapter_bwd(const void *dy, int dy_dtype, const int8_t *qg1, const float *sg1,

@@ -49,6 +49,14 @@ bool adapter_shape_ok(int64_t M, int64_t N, int64_t K, int64_t L, int64_t R)
            K <= kMaxRows && L >= 1 && L <= INT32_MAX && R >= 8 && R <= QLIN_MAX_RANK && R % 8 == 0;
 }
 
+// Whether the launches of a backward call hold its gradients: the preparation has
+// a workgroup of 256 per 32 x 32 of A and B, the sums one per 1024 values, and a
+// grid's dimension fewer than 2^32 threads.
+bool gradients_fit(int64_t N, int64_t K, int64_t R)
+{
+    return (R + 31) / 32 * 32 * (N + K) <= QLIN_MAX_ADAPTER_SIZE;
+}
+
 int check_adapter(const void *a, const void *b, int w_dtype, const float *scale, const int32_t *ids,
                   int64_t M, int64_t N, int64_t K, int64_t L, int64_t R)
 {
@@ -215,7 +223,8 @@ int qlin_adapter_group(const int32_t *ids, int64_t M, int64_t L, int32_t *order,
 
 size_t qlin_adapter_bwd_ws_bytes(int64_t M, int64_t N, int64_t K, int64_t L, int64_t R)
 {
-    if (!adapter_shape_ok(M, N, K, L, R) || N > QLIN_MAX_CONTRACTION || L > QLIN_MAX_ADAPTERS)
+    if (!adapter_shape_ok(M, N, K, L, R) || N > QLIN_MAX_CONTRACTION || L > QLIN_MAX_ADAPTERS ||
+        !gradients_fit(N, K, R))
         return 0;
     return product_part(QLIN_OP_DX, M, N, K) + qlin::adapter_bwd_bytes(M, N, K, L, R);
 }
@@ -241,7 +250,7 @@ int qlin_adapter_bwd(const void *dy, int dy_dtype, const int8_t *qg1, const floa
         !array_ok(u, any) || !array_ok(order, any) || !array_ok(start, true) || !array_ok(da, true) ||
         !array_ok(db, true) || (dx && !array_ok(sg1, any)))
         return QLIN_EINVAL;
-    if (st != QLIN_OK || sa != QLIN_OK || L > QLIN_MAX_ADAPTERS)
+    if (st != QLIN_OK || sa != QLIN_OK || L > QLIN_MAX_ADAPTERS || !gradients_fit(N, K, R))
         return QLIN_EUNSUPPORTED;
     const size_t need = qlin_adapter_bwd_ws_bytes(M, N, K, L, R);
     if (!workspace || !aligned16(workspace) || ws_bytes < need)
