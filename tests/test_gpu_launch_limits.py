@@ -89,3 +89,31 @@ def test_adamw_of_2_24_chunks():
     for a, b in zip(ts, want):
         for k in "pmv":
             assert torch.equal(a[k], b[k])
+
+
+def test_few_tokens_of_2_28_outputs():
+    """The projection of a few tokens, alone and with adapters, whose outputs are more
+    than one launch of the weight-streaming kernel has, against pieces of it."""
+    torch = torch_cuda()
+    import w8a8_integer_linear_amd as qlin
+    M, N, K, R = 2, (1 << 28) + 64, 16, 8
+    announce("few tokens", M, N, K)
+    g = torch.Generator(device="cuda").manual_seed(1)
+    codes = lambda *s: torch.randint(-127, 128, s, generator=g, device="cuda", dtype=torch.int8)  # noqa: E731
+    qx, qw = codes(M, K), codes(N, K)
+    sx, sw = torch.rand(M, generator=g, device="cuda"), torch.rand(N, generator=g, device="cuda")
+    a = torch.randn((1, R, K), generator=g, device="cuda").to(torch.bfloat16)
+    b = torch.randn((1, N, R), generator=g, device="cuda", dtype=torch.bfloat16)
+    scale, ids = torch.ones(1, device="cuda"), torch.tensor([0, -1], dtype=torch.int32, device="cuda")
+    y = qlin.qlin_fwd(qx, sx, qw, sw)
+    z, u = qlin.qlin_adapter_fwd(qx, sx, qw, sw, a, b, scale, ids)
+    assert torch.equal(y[1], z[1]) and (u[1] == 0).all()
+    step = 5_000_000 // 16 * 16
+    for at in range(0, N, step):
+        part = slice(at, min(N, at + step))
+        assert torch.equal(y[:, part], qlin.qlin_fwd(qx, sx, qw[part], sw[part]))
+        low = u[:1].double() @ b[0, part].double().T
+        size = u[:1].double().abs() @ b[0, part].double().abs().T
+        # R products and sums, then the sum with the projection's part
+        bound = (R + 8) * 2.0 ** -24 * size + 2.0 ** -23 * (y[:1, part].double().abs() + size)
+        assert ((z[:1, part] - (y[:1, part].double() + low)).abs() <= bound).all()

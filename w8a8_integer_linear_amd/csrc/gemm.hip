@@ -113,13 +113,8 @@ void launch_product(const ProductArgs &a, hipStream_t st)
     GemmParams p = gemm_params(a);
     if (a.op == 0) {
         if (a.M <= 16 && a.ws_mode == 0) {
-            const unsigned grid = (unsigned)(a.N / 16);
-            auto go = [&](auto kernel) {
-                hipLaunchKernelGGL(kernel, dim3(grid), dim3(256), 0, st, a.a, a.srow, a.b,
-                                   a.scol, a.bias, (int)a.M, (int)a.N, (int)a.K, a.out,
-                                   AdapterEpilogue{});
-            };
-            const bool wide = grid > (unsigned)kRound;
+            auto go = [&](auto kernel) { run_skinny(kernel, a, AdapterEpilogue{}, st); };
+            const bool wide = a.N / 16 > kRound;
             if (a.raw)
                 wide ? go(skinny_fwd_kernel<true, 1024>) : go(skinny_fwd_kernel<true, 4096>);
             else

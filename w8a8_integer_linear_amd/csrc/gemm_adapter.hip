@@ -36,12 +36,8 @@ bool adapter_term_apart(int64_t rows, int64_t cols)
 void launch_product_adapter(const ProductArgs &a, const AdapterEpilogue &ad, hipStream_t st)
 {
     if (a.op == 0 && a.M <= 16) {
-        const unsigned grid = (unsigned)(a.N / 16);
-        auto go = [&](auto kernel) {
-            hipLaunchKernelGGL(kernel, dim3(grid), dim3(256), 0, st, a.a, a.srow, a.b, a.scol, a.bias,
-                               (int)a.M, (int)a.N, (int)a.K, a.out, ad);
-        };
-        const bool wide = grid > (unsigned)kRound;
+        auto go = [&](auto kernel) { run_skinny(kernel, a, ad, st); };
+        const bool wide = a.N / 16 > kRound;
         if (ad.bf16)
             wide ? go(skinny_fwd_kernel<false, 1024, X_BF16>) : go(skinny_fwd_kernel<false, 4096, X_BF16>);
         else

@@ -1470,6 +1470,24 @@ __global__ __launch_bounds__(256) void skinny_fwd_kernel(const int8_t *__restric
     }
 }
 
+// Launches the kernel above, whose grid's dimension holds fewer than 2^32 threads,
+// in pieces of at most 2^27 output columns.
+template <typename Kernel>
+void run_skinny(Kernel kernel, const ProductArgs &a, AdapterEpilogue ad, hipStream_t st)
+{
+    constexpr int64_t kPiece = (int64_t)1 << 27;
+    for (int64_t n0 = 0; n0 < a.N; n0 += kPiece) {
+        const int64_t n = a.N - n0 < kPiece ? a.N - n0 : kPiece;
+        // (Outputs and float or int32 columns are 4 bytes; the row stride stays N.)
+        hipLaunchKernelGGL(kernel, dim3((unsigned)(n / 16)), dim3(256), 0, st, a.a, a.srow,
+                           a.b + n0 * a.K, a.scol ? a.scol + n0 : nullptr, a.bias ? a.bias + n0 : nullptr,
+                           (int)a.M, (int)a.N, (int)a.K,
+                           static_cast<void *>(static_cast<char *>(a.out) + n0 * 4), ad);
+        if (ad.q)
+            ad.q = static_cast<const char *>(ad.q) + kPiece * ad.R * (ad.bf16 ? 2 : 4);
+    }
+}
+
 // Operands and sizes of a product's launch.
 inline void set_operands(GemmParams &p, const ProductArgs &a)
 {
