@@ -583,7 +583,8 @@ size_t qlin_adapter_bwd_ws_bytes(int64_t M, int64_t N, int64_t K, int64_t L, int
  * zero; bf16 parameters are rounded stochastically.  The uniforms are Philox
  * 4x32-10 with key seed and counter (index >> 3, step), as in qlin_sgd_requant,
  * with the counter's top bit set for the parameters.  A block whose largest
- * value is below 2^-100 holds zeros; one with a NaN has a NaN scale.
+ * value is below 2^-100 holds zeros; one with a NaN or an infinity has a NaN
+ * scale, so that all its 256 values are NaN from then on.
  */
 typedef struct qlin_tensor {
     void *p;

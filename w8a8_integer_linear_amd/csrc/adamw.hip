@@ -313,13 +313,18 @@ __device__ __forceinline__ void step_chunk(const StepArgs &a, const TensorEntry 
         auto most = [](float x, float y) { return max_nan(x, y); };
         am = row16_all(am, most);
         av = row16_all(av, most);
-        // (A NaN is kept: it makes the block's scale NaN.)
-        const bool zm = am < kTinyBlock, zv = av < kTinyBlock;
-        im = zm ? 0.0f : (1.0f / am) * kE4m3Max;
-        iv = zv ? 0.0f : (1.0f / av) * kE4m3Max;
+        // A block with a NaN or an infinity gets a NaN scale: 448 / inf would leave
+        // its finite values as zeros, which times an infinite scale are NaN, but one
+        // step later and with a scale that does not say so.
+        auto scale_of = [](float top, float &inv) {
+            const bool zero = top < kTinyBlock;
+            inv = zero ? 0.0f : (1.0f / top) * kE4m3Max;
+            return zero ? 0.0f : top < __builtin_inff() ? top * (1.0f / kE4m3Max) : __builtin_nanf("");
+        };
+        const float cm = scale_of(am, im), cv = scale_of(av, iv);
         if (threadIdx.x % 16 == 0) {
-            gstore(t.ms, blk * 4, zm ? 0.0f : am * (1.0f / kE4m3Max));
-            gstore(t.vs, blk * 4, zv ? 0.0f : av * (1.0f / kE4m3Max));
+            gstore(t.ms, blk * 4, cm);
+            gstore(t.vs, blk * 4, cv);
         }
     }
 #pragma unroll
@@ -345,8 +350,8 @@ __device__ __forceinline__ void step_chunk(const StepArgs &a, const TensorEntry 
         }
         if constexpr (S8) {
             // (The largest value's product with 448 / a may exceed 448 by a few
-            // ulps; both conversions still give 448.  A block with a NaN has a
-            // NaN scale, and its codes do not matter.)
+            // ulps; both conversions still give 448.  The codes of a block with
+            // a NaN scale do not matter.)
             uint32_t x[4];
             uniforms8(a, u, 0u, x);
 #pragma unroll
