@@ -4,7 +4,8 @@
 //   m' = b1 m + a1 g         v' = b2 v + (a2 g) g        r' = sqrt(v')
 //   p' = p (1 - lr wd) - c1 (m' / (r' c2 + eps))
 //
-// with a1 = 1 - b1, a2 = 1 - b2, c1 = lr / (1 - b1^t), c2 = 1 / sqrt(1 - b2^t).
+// with a1 = 1 - b1, a2 = 1 - b2, c1 = lr / (1 - b1^t), c2 = 1 / sqrt(1 - b2^t); c1,
+// c2 and eps come times 2^24, which the quotient leaves as it is.
 //
 // 8-bit moments.  The second moment is held as its root r: e4m3 spans 2^17 in
 // r, hence 2^34 in v, inside one block.  Its codes are rounded stochastically:

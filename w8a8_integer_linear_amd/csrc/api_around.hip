@@ -422,16 +422,19 @@ int qlin_adamw_tensors(const void *image, int64_t count, int64_t chunks, double 
         return QLIN_EUNSUPPORTED;
     if (chunks == 0)
         return QLIN_OK;
-    // Step constants, each computed in double and rounded once.
-    const double t = (double)step;
+    // Step constants, each computed in double and rounded once.  The step's quotient
+    // has both its sides times 2^24 (c1 and c2, eps): the reciprocal instruction takes
+    // a subnormal denominator for zero, and an element that never had a gradient would
+    // get 0 / 0 where eps is one.
+    const double t = (double)step, up = 0x1p24;
     qlin::AdamTensorConsts k;
     k.b1 = (float)beta1;
     k.b2 = (float)beta2;
-    k.eps = (float)eps;
+    k.eps = (float)(eps * up);
     k.a1 = (float)(1.0 - beta1);
     k.a2 = (float)(1.0 - beta2);
-    k.c1 = (float)(lr / (1.0 - pow(beta1, t)));
-    k.c2 = (float)(1.0 / sqrt(1.0 - pow(beta2, t)));
+    k.c1 = (float)(lr * up / (1.0 - pow(beta1, t)));
+    k.c2 = (float)(up / sqrt(1.0 - pow(beta2, t)));
     k.lr = (float)lr;
     qlin::launch_adamw_tensors(image, count, chunks, k, seed, step, as_stream(stream));
     return finish();
