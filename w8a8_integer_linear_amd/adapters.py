@@ -15,9 +15,10 @@ Step order:
             qlin_rmsnorm_bwd(dx, h, rstd, dres)       -> dh, dgamma
   update    qlin_adamw_tensors(a, b, gamma)           one launch
 
-The adapters read the projection's saved codes, so the layer holds its input
-once, in one byte per element.  Buffers are kept per token count: steps of a
-token count seen before allocate nothing.
+The adapters read the projection's saved codes, so a pass holds its input
+once, in one byte per element.  Outputs and what a forward pass saves are
+ordinary tensors; the layer itself keeps its parameters, their gradients and
+moments, and one workspace, however many token counts it has seen.
 """
 import torch
 
@@ -72,65 +73,55 @@ class AdaptedLinearW8A8:
         self.dgamma = torch.zeros_like(self.gamma)
         self.state_bits = state_bits
         self._plan = None
-        self._buffers = {}
+        self.saved = None               # what the last forward left for its backward
+        self._buffers = {}              # the same, by its token count and type
+        self._ws = torch.zeros(0, dtype=torch.uint8, device=self.a.device)
 
-    def _for(self, M, x):
-        """The buffers of steps with M tokens of x's type."""
-        key = (M, x.dtype)
-        if key not in self._buffers:
-            dev, N, K, L, R = x.device, self.N, self.K, self.L, self.R
-            f32 = dict(dtype=torch.float32, device=dev)
-            self._buffers[key] = dict(
-                h=torch.empty((M, K), dtype=x.dtype, device=dev),
-                qx=torch.empty((M, K), dtype=torch.int8, device=dev),
-                sx=torch.empty(M, **f32), rstd=torch.empty(M, **f32),
-                y=torch.empty((M, N), **f32), u=torch.empty((M, R), **f32),
-                ws=torch.zeros(nat.qlin_adapter_fwd_ws_bytes(M, N, K, L, R), dtype=torch.uint8,
-                               device=dev))
-        return self._buffers[key]
+    def _workspace(self, need):
+        """One workspace for all token counts and both directions, grown to need
+        bytes (zero-filled) and never smaller."""
+        if need > self._ws.numel():
+            self._ws = torch.zeros(need, dtype=torch.uint8, device=self._ws.device)
+        return self._ws
 
-    def _for_backward(self, c, M, x_dtype):
-        if "dx" not in c:
-            dev, N, K, L, R = c["y"].device, self.N, self.K, self.L, self.R
-            f32 = dict(dtype=torch.float32, device=dev)
-            i32 = dict(dtype=torch.int32, device=dev)
-            need = nat.qlin_adapter_bwd_ws_bytes(M, N, K, L, R)
-            if need > c["ws"].numel():
-                c["ws"] = torch.zeros(need, dtype=torch.uint8, device=dev)
-            c.update(qg=torch.empty((M, N), dtype=torch.int8, device=dev), sg=torch.empty(M, **f32),
-                     dx=torch.empty((M, K), **f32), dh=torch.empty((M, K), dtype=x_dtype, device=dev),
-                     order=torch.empty(M, **i32), start=torch.empty(L + 1, **i32),
-                     norm_ws=torch.empty(nat.qlin_rmsnorm_bwd_ws_bytes(M, K), dtype=torch.uint8,
-                                         device=dev))
-        return c
-
-    def forward(self, x, ids, residual=None):
+    def forward(self, x, ids, residual=None, save=True):
         """x, residual: [M, K] (fp32 or bf16); ids: [M] int32, the adapter of each
         token, -1 for none.  Returns (y [M, N] fp32, h): the projection with the
-        adapters, and the residual stream x + residual."""
+        adapters, and the residual stream x + residual (x itself without one).
+        y and h are the caller's.  What backward needs of this pass is left in
+        self.saved, or self.saved is left alone (save=False: serving); h and ids are
+        part of it and stay as they are until then."""
         M = x.shape[0]
-        c = self._for(M, x)
-        _, _, h, _, _ = nat.qlin_rmsnorm_quant(
-            x, self.gamma, self.eps, residual=residual, had_block=self.had,
-            h=c["h"] if residual is not None else None, q=c["qx"], s=c["sx"], rstd=c["rstd"])
-        y, _ = nat.qlin_adapter_fwd(c["qx"], c["sx"], self.qw, self.sw, self.a, self.b, self.scale,
-                                    ids, bias=self.bias, y=c["y"], u=c["u"], workspace=c["ws"])
-        self._saved = (M, x.dtype, h, ids)
+        qx, sx, h, rstd, _ = nat.qlin_rmsnorm_quant(x, self.gamma, self.eps, residual=residual,
+                                                    had_block=self.had)
+        need = nat.qlin_adapter_fwd_ws_bytes(M, self.N, self.K, self.L, self.R)
+        y, u = nat.qlin_adapter_fwd(qx, sx, self.qw, self.sw, self.a, self.b, self.scale, ids,
+                                    bias=self.bias, workspace=self._workspace(need))
+        if save:
+            self.saved = dict(h=h, rstd=rstd, qx=qx, sx=sx, u=u, ids=ids)
+            self._buffers = {(M, x.dtype): self.saved}
         return y, h
 
-    def backward(self, dy, dres=None):
+    def backward(self, dy, dres=None, saved=None):
         """dy: [M, N] (fp32 or bf16); dres: [M, K] of the stream's type, the gradient
-        that reaches h past the projection.  Returns dh, the gradient of x and of
-        the residual; keeps da, db and dgamma for the update."""
-        M, x_dtype, h, ids = self._saved
-        c = self._for_backward(self._buffers[(M, x_dtype)], M, x_dtype)
-        nat.qlin_quantize_rows(dy, prescale=self.sw, q=c["qg"], s=c["sg"])
-        nat.qlin_adapter_group(ids, self.L, order=c["order"], start=c["start"])
-        nat.qlin_adapter_bwd(dy, c["qg"], c["sg"], self.qw, c["qx"], c["sx"], c["u"], self.a, self.b,
-                             self.scale, ids, c["order"], c["start"], had_block=self.had, dx=c["dx"],
-                             da=self.da, db=self.db, workspace=c["ws"])
-        dh, _ = nat.qlin_rmsnorm_bwd(c["dx"], h, c["rstd"], self.gamma, dres=dres, dh=c["dh"],
-                                     dgamma=self.dgamma, workspace=c["norm_ws"])
+        that reaches h past the projection.  saved: what the forward pass in question
+        left in self.saved, by default the last one's (with other forward passes in
+        between, keep it and hand it over).  Returns dh, the gradient of x and of the
+        residual; keeps da, db and dgamma for the update."""
+        c = self.saved if saved is None else saved
+        if c is None:
+            raise RuntimeError("backward needs a forward pass before it (save=True)")
+        M = c["h"].shape[0]
+        # (The gradient's codes stay beside the rest.)
+        c["qg"], c["sg"] = nat.qlin_quantize_rows(dy, prescale=self.sw)
+        order, start = nat.qlin_adapter_group(c["ids"], self.L)
+        need = nat.qlin_adapter_bwd_ws_bytes(M, self.N, self.K, self.L, self.R)
+        dx, _, _ = nat.qlin_adapter_bwd(
+            dy, c["qg"], c["sg"], self.qw, c["qx"], c["sx"], c["u"], self.a, self.b, self.scale,
+            c["ids"], order, start, had_block=self.had, da=self.da, db=self.db,
+            workspace=self._workspace(need))
+        dh, _ = nat.qlin_rmsnorm_bwd(dx, c["h"], c["rstd"], self.gamma, dres=dres,
+                                     dgamma=self.dgamma)
         return dh
 
     def adamw_step(self, lr, seed, step, betas=(0.9, 0.999), eps=1e-8, weight_decay=0.0):
