@@ -89,3 +89,65 @@ def test_backward_needs_a_forward():
     layer.forward(x, ids, residual=res, save=False)
     with pytest.raises(RuntimeError):
         layer.backward(dy)
+
+
+def _long(torch, M, seed):
+    """A layer whose products split their contraction (their workgroups meet in the
+    workspace), and a batch for it."""
+    layer, _ = _layer(torch, K=2048, N=512)
+    g = torch.Generator().manual_seed(seed)
+    x = torch.randn((M, 2048), generator=g).cuda()
+    ids = torch.randint(-1, 2, (M,), generator=g, dtype=torch.int32).cuda()
+    return layer, x, ids, torch.randn((M, 512), generator=g).cuda()
+
+
+def test_streams_do_not_share_a_workspace():
+    torch = torch_cuda()
+    announce("two streams")
+    layer, xa, ids, _ = _long(torch, 400, 1)
+    xb = xa.flip(0).contiguous()
+    want = [layer.forward(x, ids)[0] for x in (xa, xb)]
+    torch.cuda.synchronize()
+    side = [torch.cuda.Stream() for _ in range(2)]
+    got = ([], [])
+    for _ in range(20):
+        for k, x in enumerate((xa, xb)):
+            with torch.cuda.stream(side[k]):
+                got[k].append(layer.forward(x, ids, save=False)[0])
+    torch.cuda.synchronize()
+    for k in range(2):
+        for y in got[k]:
+            assert torch.equal(y, want[k])
+
+
+def test_graphs_keep_their_workspace():
+    """Graphs captured before and after eager calls, which grow the layer's workspace
+    between the replays."""
+    torch = torch_cuda()
+    announce("graphs of the layer")
+    layer, x, ids, dy = _long(torch, 400, 2)
+    graphs = []
+
+    def capture():
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph):
+            y, _ = layer.forward(x, ids)
+            dh = layer.backward(dy)
+        graphs.append((graph, y, dh))
+
+    capture()
+    for k, M in enumerate((100, 900, 2000)):
+        _, big, many, grad = _long(torch, M, 3)
+        x.copy_(torch.randn(x.shape, device="cuda"))
+        layer.forward(big, many)
+        layer.backward(grad)
+        want = [layer.forward(x, ids)[0], layer.backward(dy), layer.da.clone(), layer.db.clone()]
+        torch.cuda.synchronize()
+        for graph, y, dh in graphs:
+            for t in (y, dh, layer.da, layer.db):
+                t.zero_()
+            graph.replay()
+            torch.cuda.synchronize()
+            for a, b in zip((y, dh, layer.da, layer.db), want):
+                assert torch.equal(a, b)
+        capture()

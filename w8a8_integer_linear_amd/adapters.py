@@ -18,7 +18,9 @@ Step order:
 The adapters read the projection's saved codes, so a pass holds its input
 once, in one byte per element.  Outputs and what a forward pass saves are
 ordinary tensors; the layer itself keeps its parameters, their gradients and
-moments, and one workspace, however many token counts it has seen.
+moments, and one workspace per stream, however many token counts it has seen.
+Forward passes may run on several streams at once; the gradients are one set, so
+backward passes may not.
 """
 import torch
 
@@ -75,14 +77,20 @@ class AdaptedLinearW8A8:
         self._plan = None
         self.saved = None               # what the last forward left for its backward
         self._buffers = {}              # the same, by its token count and type
-        self._ws = torch.zeros(0, dtype=torch.uint8, device=self.a.device)
+        self._ws = {}                   # workspaces by stream
 
     def _workspace(self, need):
-        """One workspace for all token counts and both directions, grown to need
-        bytes (zero-filled) and never smaller."""
-        if need > self._ws.numel():
-            self._ws = torch.zeros(need, dtype=torch.uint8, device=self._ws.device)
-        return self._ws
+        """The current stream's workspace, for all token counts and both directions,
+        grown to need bytes (zero-filled) and never smaller: calls that share one must
+        not overlap in time, and streams do.  In a graph's capture None: the call makes
+        one of the graph's own, which no later growth frees under its replays."""
+        if torch.cuda.is_current_stream_capturing():
+            return None
+        stream = nat._stream(None)
+        ws = self._ws.get(stream)
+        if ws is None or ws.numel() < need:
+            ws = self._ws[stream] = torch.zeros(need, dtype=torch.uint8, device=self.a.device)
+        return ws
 
     def forward(self, x, ids, residual=None, save=True):
         """x, residual: [M, K] (fp32 or bf16); ids: [M] int32, the adapter of each
