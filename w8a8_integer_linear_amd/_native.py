@@ -135,18 +135,29 @@ def _need(t, name, dtype, shape=None):
     raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
 
 
-def _addr(*args):
-    """_addr(t, name, dtype, *shape): the address of a tensor that _need accepts (no
-    sizes: of any shape), checked by compiled code; _need raises for others."""
-    global _addr
+def _load_compiled():
+    """Puts the compiled _addr and _new in the places of the ones below."""
+    global _addr, _new
     if not os.path.exists(MARSHAL_PATH):
         raise ImportError(
             f"{MARSHAL_PATH} is missing: build it with `python -c 'import __graft_entry__ as g; "
             "g.build()'`")
     from . import _marshal
     _marshal.set_refuse(_need)
-    _addr = _marshal.address
+    _addr, _new = _marshal.address, _marshal.empty
+
+
+def _addr(*args):
+    """_addr(t, name, dtype, *shape): the address of a tensor that _need accepts (no
+    sizes: of any shape), checked by compiled code; _need raises for others."""
+    _load_compiled()
     return _addr(*args)
+
+
+def _new(*args):
+    """_new(like, dtype, *shape): a tensor on like's device, allocated by compiled code."""
+    _load_compiled()
+    return _new(*args)
 
 
 def _opt(t, name, dtype, shape):
@@ -451,7 +462,9 @@ def _workspace(workspace, need, like, zero):
         n = need()
         if not n:
             return None, None, 0
-        workspace = (torch.zeros if zero else torch.empty)(n, dtype=torch.uint8, device=like.device)
+        workspace = _new(like, torch.uint8, n)
+        if zero:
+            workspace.zero_()
     return workspace, _addr(workspace, "workspace", torch.uint8), workspace.numel()
 
 
@@ -468,13 +481,13 @@ def qlin_rmsnorm_quant(x, gamma, eps, residual=None, had_block=0, h=None, q=None
     pr = ph = py = None
     if residual is not None:
         pr = _addr(residual, "residual", dtype, rows, cols)
-        h = _empty((rows, cols), dtype, x) if h is None else h
+        h = _new(x, dtype, rows, cols) if h is None else h
         ph = _addr(h, "h", dtype, rows, cols)
-    q = _empty((rows, cols), torch.int8, x) if q is None else q
-    s = _empty((rows,), torch.float32, x) if s is None else s
-    rstd = _empty((rows,), torch.float32, x) if rstd is None else rstd
+    q = _new(x, torch.int8, rows, cols) if q is None else q
+    s = _new(x, torch.float32, rows) if s is None else s
+    rstd = _new(x, torch.float32, rows) if rstd is None else rstd
     if y is None and want_y:
-        y = _empty((rows, cols), torch.bfloat16, x)
+        y = _new(x, torch.bfloat16, rows, cols)
     if y is not None:
         py = _addr(y, "y", torch.bfloat16, rows, cols)
     _check("qlin_rmsnorm_quant", lib().qlin_rmsnorm_quant(
@@ -484,6 +497,7 @@ def qlin_rmsnorm_quant(x, gamma, eps, residual=None, had_block=0, h=None, q=None
     return q, s, x if residual is None else h, rstd, y
 
 
+@functools.lru_cache(maxsize=1024)
 def qlin_rmsnorm_bwd_ws_bytes(rows, cols):
     return int(lib().qlin_rmsnorm_bwd_ws_bytes(int(rows), int(cols)))
 
@@ -499,8 +513,8 @@ def qlin_rmsnorm_bwd(dn, h, rstd, gamma, dres=None, dh=None, dgamma=None, worksp
     pr = _addr(rstd, "rstd", torch.float32, rows)
     pg = _addr(gamma, "gamma", torch.float32, cols)
     pd = None if dres is None else _addr(dres, "dres", dtype, rows, cols)
-    dh = _empty((rows, cols), dtype, h) if dh is None else dh
-    dgamma = _empty((cols,), torch.float32, h) if dgamma is None else dgamma
+    dh = _new(h, dtype, rows, cols) if dh is None else dh
+    dgamma = _new(h, torch.float32, cols) if dgamma is None else dgamma
     po, pq = _addr(dh, "dh", dtype, rows, cols), _addr(dgamma, "dgamma", torch.float32, cols)
     workspace, pw, size = _workspace(workspace, lambda: qlin_rmsnorm_bwd_ws_bytes(rows, cols), h,
                                      zero=False)
@@ -518,6 +532,7 @@ def _adapters(a, b, scale, ids, M, N, K):
             _addr(ids, "ids", torch.int32, M))
 
 
+@functools.lru_cache(maxsize=1024)
 def qlin_adapter_fwd_ws_bytes(M, N, K, L, R):
     return int(lib().qlin_adapter_fwd_ws_bytes(int(M), int(N), int(K), int(L), int(R)))
 
@@ -532,8 +547,8 @@ def qlin_adapter_fwd(qx, sx, qw, sw, a, b, scale, ids, bias=None, y=None, u=None
     psx, psw = _addr(sx, "sx", torch.float32, M), _addr(sw, "sw", torch.float32, N)
     pbias = None if bias is None else _addr(bias, "bias", torch.float32, N)
     L, R, code, pa, pb, ps, pi = _adapters(a, b, scale, ids, M, N, K)
-    y = _empty((M, N), torch.float32, qx) if y is None else y
-    u = _empty((M, R), torch.float32, qx) if u is None else u
+    y = _new(qx, torch.float32, M, N) if y is None else y
+    u = _new(qx, torch.float32, M, R) if u is None else u
     py, pu = _addr(y, "y", torch.float32, M, N), _addr(u, "u", torch.float32, M, R)
     workspace, pws, size = _workspace(workspace, lambda: qlin_adapter_fwd_ws_bytes(M, N, K, L, R),
                                       qx, zero=True)
@@ -549,14 +564,15 @@ def qlin_adapter_group(ids, L, order=None, start=None, stream=None):
     M, = ids.shape
     L = int(L)
     pi = _addr(ids, "ids", torch.int32)
-    order = _empty((M,), torch.int32, ids) if order is None else order
-    start = _empty((L + 1,), torch.int32, ids) if start is None else start
+    order = _new(ids, torch.int32, M) if order is None else order
+    start = _new(ids, torch.int32, L + 1) if start is None else start
     _check("qlin_adapter_group", lib().qlin_adapter_group(
         pi, M, L, _addr(order, "order", torch.int32, M), _addr(start, "start", torch.int32, L + 1),
         _stream(stream)))
     return order, start
 
 
+@functools.lru_cache(maxsize=1024)
 def qlin_adapter_bwd_ws_bytes(M, N, K, L, R):
     return int(lib().qlin_adapter_bwd_ws_bytes(int(M), int(N), int(K), int(L), int(R)))
 
@@ -577,12 +593,12 @@ def qlin_adapter_bwd(dy, qg1, sg1, qw, qx, sx, u, a, b, scale, ids, order, start
     if want_dx:
         pg, psg = _addr(qg1, "qg1", torch.int8, M, N), _addr(sg1, "sg1", torch.float32, M)
         pw = _addr(qw, "qw", torch.int8, N, K)
-        dx = _empty((M, K), torch.float32, dy) if dx is None else dx
+        dx = _new(dy, torch.float32, M, K) if dx is None else dx
         pdx = _addr(dx, "dx", torch.float32, M, K)
     else:
         dx = None
-    da = _empty((L, R, K), torch.float32, dy) if da is None else da
-    db = _empty((L, N, R), torch.float32, dy) if db is None else db
+    da = _new(dy, torch.float32, L, R, K) if da is None else da
+    db = _new(dy, torch.float32, L, N, R) if db is None else db
     pda, pdb = _addr(da, "da", torch.float32, L, R, K), _addr(db, "db", torch.float32, L, N, R)
     workspace, pws, size = _workspace(workspace, lambda: qlin_adapter_bwd_ws_bytes(M, N, K, L, R),
                                       dy, zero=True)

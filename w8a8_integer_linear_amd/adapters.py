@@ -100,6 +100,8 @@ class AdaptedLinearW8A8:
         self.saved, or self.saved is left alone (save=False: serving); h and ids are
         part of it and stay as they are until then."""
         M = x.shape[0]
+        if save:    # (the last pass's memory may serve this one)
+            self.saved, self._buffers = None, {}
         qx, sx, h, rstd, _ = nat.qlin_rmsnorm_quant(x, self.gamma, self.eps, residual=residual,
                                                     had_block=self.had)
         need = nat.qlin_adapter_fwd_ws_bytes(M, self.N, self.K, self.L, self.R)

@@ -1,15 +1,19 @@
 // The binding's argument checks, compiled: a call of few tokens takes the GPU
 // less time than a dozen tensors' checks take the interpreter (the projection
-// with adapters at seven tokens: 8.8 us of host time per call instead of 12.7 us).
+// with adapters at seven tokens: 8.8 us of host time per call instead of 12.7 us);
+// and the allocation of outputs, 0.8 us each instead of 2.2 us.
 #define PY_SSIZE_T_CLEAN
 #include <Python.h>
 
+#include <ATen/ops/empty.h>
 #include <torch/csrc/Dtype.h>
+#include <torch/csrc/Exceptions.h>
 #include <torch/csrc/autograd/python_variable.h>
 
 namespace {
 
 PyObject *refuse = nullptr;     // the binding's own check, which names the fault
+constexpr Py_ssize_t kMostDims = 4;
 
 // The address of a contiguous GPU tensor of this dtype and, if any sizes are
 // given, of this shape; false if it is not one.
@@ -72,6 +76,26 @@ PyObject *address(PyObject *, PyObject *const *args, Py_ssize_t n)
     return nullptr;
 }
 
+// empty(like, dtype, *sizes): a new tensor on like's device.
+PyObject *empty(PyObject *, PyObject *const *args, Py_ssize_t n)
+{
+    if (n < 2 || n > 2 + kMostDims || !THPVariable_Check(args[0]) || !THPDtype_Check(args[1])) {
+        PyErr_SetString(PyExc_TypeError, "empty(tensor, dtype, *sizes)");
+        return nullptr;
+    }
+    int64_t sizes[kMostDims];
+    for (Py_ssize_t i = 2; i < n; i++) {
+        sizes[i - 2] = PyLong_AsLongLong(args[i]);
+        if (sizes[i - 2] == -1 && PyErr_Occurred())
+            return nullptr;
+    }
+    HANDLE_TH_ERRORS        // (the allocator's errors keep their types)
+    const at::TensorOptions options =
+        THPVariable_Unpack(args[0]).options().dtype(reinterpret_cast<THPDtype *>(args[1])->scalar_type);
+    return THPVariable_Wrap(at::empty(at::IntArrayRef(sizes, (size_t)(n - 2)), options));
+    END_HANDLE_TH_ERRORS
+}
+
 PyObject *set_refuse(PyObject *, PyObject *f)
 {
     Py_INCREF(f);
@@ -82,6 +106,8 @@ PyObject *set_refuse(PyObject *, PyObject *f)
 PyMethodDef methods[] = {
     {"address", reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(address)), METH_FASTCALL,
      "address(tensor, name, dtype, *sizes)"},
+    {"empty", reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(empty)), METH_FASTCALL,
+     "empty(like, dtype, *sizes)"},
     {"set_refuse", set_refuse, METH_O, "set_refuse(function)"},
     {nullptr, nullptr, 0, nullptr},
 };
