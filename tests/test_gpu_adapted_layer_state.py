@@ -151,3 +151,32 @@ def test_graphs_keep_their_workspace():
             for a, b in zip((y, dh, layer.da, layer.db), want):
                 assert torch.equal(a, b)
         capture()
+
+
+@pytest.mark.parametrize("bits", [32, 8])
+def test_weight_decay_may_change(bits):
+    """Without gradients a step is the decay alone: p (1 - lr wd), two roundings.  With
+    them, the moments go on as without any decay."""
+    torch = torch_cuda()
+    announce("weight decay", bits)
+    layer, plain = (_layer(torch, bits=bits)[0] for _ in range(2))
+    lr, step = 1e-2, 0
+    for decay in (0.0, 0.5, 0.5, 0.25, 0.0):
+        step += 1
+        before = [t.clone() for t in (layer.a, layer.b, layer.gamma)]
+        layer.adamw_step(lr, seed=3, step=step, weight_decay=decay)
+        plain.adamw_step(lr, seed=3, step=step)
+        for p, old, wd in zip((layer.a, layer.b, layer.gamma), before, (decay, decay, 0.0)):
+            want = old.double() * (1 - lr * wd)
+            assert ((p.double() - want).abs() <= 4 * 2.0 ** -24 * want.abs()).all()
+    g = torch.Generator(device="cuda").manual_seed(1)
+    for decay in (0.1, 0.0, 0.2):
+        step += 1
+        for a, b in zip((layer.da, layer.db, layer.dgamma), (plain.da, plain.db, plain.dgamma)):
+            a.normal_(generator=g)
+            b.copy_(a)
+        layer.adamw_step(lr, seed=3, step=step, weight_decay=decay)
+        plain.adamw_step(lr, seed=3, step=step)
+    for t, u in zip(layer._trained, plain._trained):
+        for k in set(t) - {"p", "g", "weight_decay"}:
+            assert torch.equal(t[k].float(), u[k].float()) and (t[k].float() != 0).any()

@@ -136,17 +136,19 @@ class AdaptedLinearW8A8:
 
     def adamw_step(self, lr, seed, step, betas=(0.9, 0.999), eps=1e-8, weight_decay=0.0):
         """One AdamW step over the adapters and gamma (step >= 1).  The moments are
-        allocated, zeroed, on the first call, which also fixes weight_decay (of the
-        adapters; gamma has none)."""
+        allocated, zeroed, on the first call.  weight_decay is of the adapters (gamma
+        has none); another value than the last step's makes a new plan."""
         if self._plan is None:
-            self._plan = nat.qlin_adamw_tensors_plan([
-                self._with_moments(self.a, self.da, weight_decay),
-                self._with_moments(self.b, self.db, weight_decay),
-                self._with_moments(self.gamma, self.dgamma, 0.0)])
+            self._trained = [self._with_moments(p, g) for p, g in (
+                (self.a, self.da), (self.b, self.db), (self.gamma, self.dgamma))]
+        if self._plan is None or weight_decay != self._decay:
+            for t, decay in zip(self._trained, (weight_decay, weight_decay, 0.0)):
+                t["weight_decay"] = decay
+            self._plan, self._decay = nat.qlin_adamw_tensors_plan(self._trained), weight_decay
         nat.qlin_adamw_tensors(self._plan, lr, betas[0], betas[1], eps, seed, step)
 
-    def _with_moments(self, p, g, weight_decay):
-        t = dict(p=p, g=g, weight_decay=weight_decay)
+    def _with_moments(self, p, g):
+        t = dict(p=p, g=g)
         if self.state_bits == 32:
             t["m"], t["v"] = (torch.zeros(p.shape, dtype=torch.float32, device=p.device)
                               for _ in range(2))
