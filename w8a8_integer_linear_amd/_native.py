@@ -610,10 +610,26 @@ def qlin_adapter_bwd(dy, qg1, sg1, qw, qx, sx, u, a, b, scale, ids, order, start
 
 class AdamWPlan:
     """The device image of a list of tensors (qlin_adamw_tensors_plan); holds
-    the tensors, whose addresses are in the image."""
+    the tensors, whose addresses are in the image (new values of a gradient go into
+    the same tensor; other tensors need another plan)."""
 
     def __init__(self, image, count, chunks, tensors):
         self.image, self.count, self.chunks, self.tensors = image, count, chunks, tensors
+        self._streams = set()
+
+    def used_on(self, stream):
+        """Keeps the memory of the image and of every tensor, which the plan may be the
+        last to hold, from being given away before the steps on this stream have run.
+        (The allocator remembers a stream until the memory is freed: once is enough.)"""
+        if stream in self._streams or self.image is None:
+            return
+        current = torch.cuda.current_stream()
+        for t in self.tensors:
+            for v in t.values():
+                if isinstance(v, torch.Tensor):
+                    v.record_stream(current)
+        self.image.record_stream(current)
+        self._streams.add(stream)
 
 
 def qlin_adamw_tensors_plan(tensors):
@@ -659,8 +675,7 @@ def qlin_adamw_tensors_plan(tensors):
 @_on_stream
 def qlin_adamw_tensors(plan, lr, beta1, beta2, eps, seed, step, stream=None):
     """One AdamW step over the plan's tensors, in place (step >= 1)."""
-    if stream is not None and plan.image is not None:
-        plan.image.record_stream(stream)    # the plan may be dropped before the step has run
+    handle = _stream(stream)
+    plan.used_on(handle)
     _check("qlin_adamw_tensors", lib().qlin_adamw_tensors(
-        _ptr(plan.image), plan.count, plan.chunks, lr, beta1, beta2, eps, int(seed), int(step),
-        _stream(stream)))
+        _ptr(plan.image), plan.count, plan.chunks, lr, beta1, beta2, eps, int(seed), int(step), handle))
