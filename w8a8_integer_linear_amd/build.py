@@ -73,7 +73,6 @@ def build(verbose=False):
     with cf.ThreadPoolExecutor(max_workers=min(len(SOURCES), 8)) as ex:
         marshal = ex.submit(_build_marshal, verbose)
         objs = list(ex.map(lambda s: _compile(s, verbose), SOURCES))
-        marshal.result()
     tmp = LIB + ".tmp"
     cmd = [hipcc(), f"--offload-arch={ARCH}", "-shared", "-fPIC", *objs, "-o", tmp]
     if verbose:
@@ -82,6 +81,8 @@ def build(verbose=False):
     if r.returncode != 0:
         raise RuntimeError(f"link failed:\n{r.stdout}\n{r.stderr}")
     os.replace(tmp, LIB)
+    # (Last: the library needs neither torch's headers nor Python's.)
+    marshal.result()
     return LIB
 
 
