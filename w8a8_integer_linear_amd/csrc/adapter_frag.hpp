@@ -59,15 +59,8 @@ __device__ __forceinline__ Frag<terms_of(X)> load_frag(const void *p, int64_t id
         if (ok)
             f.t[0] = *reinterpret_cast<const bf16x8 *>(static_cast<const uint16_t *>(p) + idx);
         return f;
-    } else if constexpr (X == X_I8) {
-        i32x2 w = {0, 0};
-        if (ok)
-            w = *reinterpret_cast<const i32x2 *>(static_cast<const int8_t *>(p) + idx);
-        float v[8];
-        codes_to_float(w, v);
-        f.t[0] = round8(v);
-        return f;
     } else {
+        static_assert(X == X_F32, "codes are read through LDS");
         float v[8] = {0, 0, 0, 0, 0, 0, 0, 0};
         if (ok)
             load8<false>(p, idx, v);

@@ -4,8 +4,10 @@
 // Forward, one row: h = rnd(x + residual) (in the stream's own type), rstd =
 // 1 / sqrt(mean(h^2) + eps), n = (h * rstd) * gamma, g = rotate(n), s = max|g|
 // / 127, q = rne(g / s).  A row's values stay in registers from the loads to
-// the codes, so x and the residual are read once and h and q written once;
-// the row's two reductions (the sum of squares, the absmax) run across lanes.
+// the codes, so x and the residual are read once and h and q written once (above
+// 32768 columns a lane has 64 of them or more and some go through scratch memory:
+// up to 46 registers' worth, above 65536 columns 172 to 692); the row's two
+// reductions (the sum of squares, the absmax) run across lanes.
 // HBM traffic bounds it, except for a few rows, where the launch does: 12000 rows
 // of 5376 in fp32 with a residual and the codes' values as bf16 beside them, 968
 // MB, take 174 us (5.6 TB/s); 3 rows of 4096 take 3.4 us in the kernel and 5.6 us
@@ -28,24 +30,22 @@ namespace {
 
 constexpr float kInf = __builtin_inff();
 
-// Reduction over the WPR waves that share a row; every thread gets the result.
-// red holds one float per wave of the workgroup and is written again only
-// after the next barrier that all its readers have passed (two arrays take
-// turns for consecutive reductions).
+// Reduction over the workgroup's WPR waves, which share a row; every thread gets
+// the result.  red holds one float per wave and is written again only after the
+// next barrier that all its readers have passed (two arrays take turns for
+// consecutive reductions).
 template <int WPR, typename Op>
 __device__ __forceinline__ float row_reduce(float v, float *red, Op op)
 {
     v = wave_all(v, op);
-    if constexpr (WPR > 1) {
-        const int w = threadIdx.x / kWave;
-        if (__lane_id() == 0)
-            red[w] = v;
-        lds_barrier();
-        v = red[0];
+    const int w = threadIdx.x / kWave;
+    if (__lane_id() == 0)
+        red[w] = v;
+    lds_barrier();
+    v = red[0];
 #pragma unroll
-        for (int i = 1; i < WPR; i++)
-            v = op(v, red[i]);
-    }
+    for (int i = 1; i < WPR; i++)
+        v = op(v, red[i]);
     return v;
 }
 
@@ -69,17 +69,14 @@ struct NormArgs {
     uint16_t *y;        // bf16 values of the codes, or null
 };
 
-// WPR waves per row, J chunks of eight elements per lane.
+// One row per workgroup of WPR waves, J chunks of eight elements per lane.
 template <bool BF16, int WPR, int J, int HAD>
-__global__ __launch_bounds__(WPR > 4 ? WPR *kWave : 4 * kWave) void rmsnorm_quant_kernel(NormArgs a)
+__global__ __launch_bounds__(WPR *kWave) void rmsnorm_quant_kernel(NormArgs a)
 {
-    constexpr int kThreads = WPR * kWave;              // of one row
-    constexpr int kRowsPer = WPR > 4 ? 1 : 4 / WPR;    // rows of a workgroup
-    __shared__ float red[2][kRowsPer * WPR];
-    const int t = threadIdx.x % kThreads;
-    const int64_t row = (int64_t)blockIdx.x * kRowsPer + threadIdx.x / kThreads;
-    if (WPR == 1 && row >= a.rows)
-        return;
+    constexpr int kThreads = WPR * kWave;
+    __shared__ float red[2][WPR];
+    const int t = threadIdx.x;
+    const int64_t row = blockIdx.x;
     const int64_t nch = a.cols / 8, base = row * a.cols;
     auto chunk = [&](int j) {
         const int64_t c = t + (int64_t)j * kThreads;
@@ -214,10 +211,8 @@ __global__ __launch_bounds__(WPR > 4 ? WPR *kWave : 4 * kWave) void rmsnorm_quan
 template <bool BF16, int WPR, int J, int HAD>
 void run_norm(const NormArgs &a, hipStream_t st)
 {
-    constexpr int kRowsPer = WPR > 4 ? 1 : 4 / WPR;
-    const unsigned grid = (unsigned)((a.rows + kRowsPer - 1) / kRowsPer);
-    hipLaunchKernelGGL((rmsnorm_quant_kernel<BF16, WPR, J, HAD>), dim3(grid),
-                       dim3(kRowsPer * WPR * kWave), 0, st, a);
+    hipLaunchKernelGGL((rmsnorm_quant_kernel<BF16, WPR, J, HAD>), dim3((unsigned)a.rows),
+                       dim3(WPR * kWave), 0, st, a);
 }
 
 template <bool BF16, int HAD>
