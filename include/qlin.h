@@ -548,7 +548,8 @@ int qlin_adapter_group(const int32_t *ids, int64_t M, int64_t L, int32_t *order,
  * The sums over tokens are fp32, in a fixed order.  Limits as in the forward
  * call, L <= QLIN_MAX_ADAPTERS; R, rounded up to a multiple of 32, times N + K at
  * most QLIN_MAX_ADAPTER_SIZE; had_block as in qlin_bwd_dx.
- * workspace: qlin_adapter_bwd_ws_bytes bytes, under the same rules.
+ * workspace: qlin_adapter_bwd_ws_bytes bytes, under the same rules (the size is
+ * that of fp32 matrices for either w_dtype).
  */
 int qlin_adapter_bwd(const void *dy, int dy_dtype, const int8_t *qg1, const float *sg1,
                      const int8_t *qw, const int8_t *qx, const float *sx, const float *u,

@@ -411,9 +411,15 @@ template <int W> __global__ __launch_bounds__(256) void adapter_shrink_few_kerne
 }
 
 // Most waves (tokens times ranks) of the kernel above, which reads an adapter once
-// per token, but all adapters at once (4096 codes, eight adapters in bf16: 64
-// tokens of rank 16, 35 us for the call against 42 us; 64 of rank 64, 43 us
-// against 48 us; 512 of rank 16, 41 us against 39 us).
+// per token, but all adapters at once.  us for the call, 4096 -> 4096 in bf16, this
+// kernel / the tiles of 32 tokens:
+//                                        1024      4096      8192     16384
+//   rank 16, nine requests in a row      39/47     40/42     45/44     59/53
+//   rank 64, nine requests in a row      63/75     49/55     48/49     53/48
+//   rank 16, 8 adapters in any order     45/58     48/58     54/62     73/77
+//   rank 16, 256 adapters in any order   56/102    61/101    70/108    97/128
+// (The host knows neither the number of distinct adapters nor their order: the bound
+// is where no case loses, and mixed tokens above it pay up to half as much again.)
 constexpr int64_t kFewWaves = 4096;
 
 // Workgroups that a product of fewer units (32 tokens by a group of ranks) than
@@ -1215,10 +1221,11 @@ void launch_adapter_group(const int32_t *ids, int64_t M, int L, int32_t *order, 
 
 static int64_t slabs_of(int64_t M, int64_t L) { return M / kSlab + (M < L ? M : L); }
 
-// So few tokens, hence slabs of one adapter, that the last to arrive adds them up
-// (333 tokens, 4096 x 4096, rank 64, five adapters in fp32: 84 us for the call
-// against 91.5 us with the sums in a launch of their own; 12000 tokens of three
-// adapters: 497 us against 463 us).  No tokens at all: the launch writes the zeros.
+// So few tokens, hence slabs of one adapter, that the last to arrive adds them up.
+// us for the call, 4096 x 4096, five adapters, added up in place / in a launch of
+// their own, by tokens: rank 16 in bf16 333: 49/51, 700: 59/61, 1024: 65/66, 1500:
+// 74/77, 2048: 93/90, 4096: 109/101; rank 64 in fp32 333: 59/64, 700: 74/78, 1024:
+// 94/88, 1500: 112/111, 2048: 156/146.  No tokens at all: the launch writes the zeros.
 static bool sums_in_place(int64_t M) { return M > 0 && M <= 4 * kSlab; }
 
 // Column blocks of both gradients (a gradient's with the fewest columns each).

@@ -25,9 +25,18 @@ template <bool BKM, int EPI> void run(GemmParams &p, hipStream_t st)
 } // namespace
 
 // Few tiles: added in the epilogues, the term would be the work of as few compute
-// units (backward of 333 tokens, 4096 x 4096, rank 64 in fp32: 141 us against 77
-// us with the term apart; forward of 611 tokens, 4096 -> 14336, rank 32, 168
-// tiles: 73 us against 98 us).
+// units.  One bound for both directions and every rank; us for the call with the
+// term apart / in the epilogues, contraction 4096, by tiles (611 and 2048 tokens):
+//                              48      84        120       128       144       192
+//   forward, rank 16, bf16   50/52   57/55   63/58 (108)  74/62     67/59     72/60
+//   forward, rank 64, fp32   66/73   77/76   85/80 (108) 110/88     95/82    105/84
+//   dX, rank 16, bf16                66/72     79/80      91/89     81/80     88/82
+//   dX, rank 64, bf16                91/101   109/109    133/121   116/111   133/114
+//   dX, rank 64, fp32                87/125   100/133    126/146   106/136   119/140
+// (32 tiles, 333 tokens, dX: 49/65, 63/97, 60/126.)  So the forward changes sides at
+// about 84 tiles, dX at about 130, but dX with fp32 adapters of rank 64, whose six
+// pairs of terms the epilogues read, only at about 256 (192/183): between the bound
+// and there it takes up to half as long again as with the term apart.
 bool adapter_term_apart(int64_t rows, int64_t cols)
 {
     return ((rows + 255) / 256) * ((cols + 255) / 256) < 128;

@@ -11,7 +11,10 @@
 // HBM traffic bounds it, except for a few rows, where the launch does: 12000 rows
 // of 5376 in fp32 with a residual and the codes' values as bf16 beside them, 968
 // MB, take 174 us (5.6 TB/s); 3 rows of 4096 take 3.4 us in the kernel and 5.6 us
-// as a call.
+// as a call.  Long rows, 64 M elements in bf16 with a residual: 5.5 TB/s up to 16384
+// columns, 4.2 at 65536, 1.3 at 131072 (the scratch memory's traffic).  Short ones
+// leave lanes without columns: 120000 rows of 512 take 261 us, 1.7 TB/s, as long as
+// as many rows of 128.
 //
 // Backward, one row, with xh = h * rstd and g = dn * gamma: dh = dres + rstd
 // (g - xh mean(g xh)), and dgamma += dn * xh per column.  A workgroup walks
@@ -360,8 +363,9 @@ __global__ __launch_bounds__(256, 2) void rmsnorm_bwd_kernel(NormBwdArgs a)
 }
 
 // Rows too long for the kernel above: each row is read twice (its dot
-// product, then dh), and the column sums are a pass of their own.  Workgroup i
-// has row r0 + i.
+// product, then dh), and the column sums are a pass of their own (64 M elements, dn
+// in fp32 and the rest in bf16: 12288 columns 211 us, 3.0 TB/s of what a single pass
+// would move; 131072 columns 276 us).  Workgroup i has row r0 + i.
 template <bool DNBF, bool BF16>
 __global__ __launch_bounds__(1024) void rmsnorm_bwd_long_kernel(NormBwdArgs a, int64_t r0)
 {
