@@ -39,10 +39,9 @@ constexpr float kE4m3Max = 448.0f;
 
 struct StepArgs {
     const TensorEntry *tensors;
-    const int32_t *chunk_tensor;
+    const int32_t *chunk_tensor;        // of the launch's chunks
     float b1, b2, eps, a1, a2, c1, c2, lr;
     uint32_t seed_lo, seed_hi, step_lo, step_hi;
-    uint32_t chunk0;        // the launch's first chunk
 };
 
 // Eight e4m3 codes at a byte pointer (8-byte aligned) as floats.
@@ -378,11 +377,10 @@ __device__ __forceinline__ void step_either(const StepArgs &a, const TensorEntry
         step_chunk<PB, GB, S8, false>(a, t, c0);
 }
 
-__global__ __launch_bounds__(256) void adamw_tensors_kernel(StepArgs a)
+__device__ __forceinline__ void step_tensors(const StepArgs &a, uint32_t chunk0)
 {
-    const uint32_t chunk = a.chunk0 + blockIdx.x;
-    const TensorEntry t = a.tensors[a.chunk_tensor[chunk]];
-    const int64_t c0 = ((int64_t)chunk - t.chunk0) * kTensorChunk;
+    const TensorEntry t = a.tensors[a.chunk_tensor[blockIdx.x]];
+    const int64_t c0 = ((int64_t)(chunk0 + blockIdx.x) - t.chunk0) * kTensorChunk;
     switch (t.flags) {
     case 0: return step_either<false, false, false>(a, t, c0);
     case 1: return step_either<true, false, false>(a, t, c0);
@@ -395,6 +393,17 @@ __global__ __launch_bounds__(256) void adamw_tensors_kernel(StepArgs a)
     }
 }
 
+static_assert(sizeof(StepArgs) == 64, "the arguments are one cache line");
+
+__global__ __launch_bounds__(256) void adamw_tensors_kernel(StepArgs a) { step_tensors(a, 0); }
+
+// The same from chunk chunk0 on, for lists that take several launches.  (A kernel of
+// its own: the argument past the first 64 bytes costs a short list 0.35 us of 17.)
+__global__ __launch_bounds__(256) void adamw_tensors_from_kernel(StepArgs a, uint32_t chunk0)
+{
+    step_tensors(a, chunk0);
+}
+
 } // namespace
 
 void launch_adamw_tensors(const void *image, int64_t count, int64_t chunks, const AdamTensorConsts &k,
@@ -402,7 +411,7 @@ void launch_adamw_tensors(const void *image, int64_t count, int64_t chunks, cons
 {
     StepArgs a;
     a.tensors = static_cast<const TensorEntry *>(image);
-    a.chunk_tensor = reinterpret_cast<const int32_t *>(a.tensors + count);
+    const int32_t *chunk_tensor = reinterpret_cast<const int32_t *>(a.tensors + count);
     a.b1 = k.b1;
     a.b2 = k.b2;
     a.eps = k.eps;
@@ -418,9 +427,12 @@ void launch_adamw_tensors(const void *image, int64_t count, int64_t chunks, cons
     // Chunks of one launch: a grid's dimension holds fewer than 2^32 threads.
     constexpr int64_t kLaunchChunks = (int64_t)1 << 23;
     for (int64_t c = 0; c < chunks; c += kLaunchChunks) {
-        const int64_t n = chunks - c < kLaunchChunks ? chunks - c : kLaunchChunks;
-        a.chunk0 = (uint32_t)c;
-        hipLaunchKernelGGL(adamw_tensors_kernel, dim3((unsigned)n), dim3(256), 0, st, a);
+        const dim3 grid((unsigned)(chunks - c < kLaunchChunks ? chunks - c : kLaunchChunks));
+        a.chunk_tensor = chunk_tensor + c;
+        if (c == 0)
+            hipLaunchKernelGGL(adamw_tensors_kernel, grid, dim3(256), 0, st, a);
+        else
+            hipLaunchKernelGGL(adamw_tensors_from_kernel, grid, dim3(256), 0, st, a, (uint32_t)c);
     }
 }
 
