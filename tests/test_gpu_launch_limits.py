@@ -117,3 +117,47 @@ def test_few_tokens_of_2_28_outputs():
         # R products and sums, then the sum with the projection's part
         bound = (R + 8) * 2.0 ** -24 * size + 2.0 ** -23 * (y[:1, part].double().abs() + size)
         assert ((z[:1, part] - (y[:1, part].double() + low)).abs() <= bound).all()
+
+
+def test_rotation_of_2_35_values():
+    """In place, 137 GB; the rows repeat a few."""
+    torch = torch_cuda()
+    import w8a8_integer_linear_amd as qlin
+    rows, cols, piece = (1 << 24) + 1, 2048, 1 << 12
+    if torch.cuda.mem_get_info()[0] < 150 << 30:
+        pytest.skip("needs 150 GB of the card's memory")
+    announce("hadamard", rows, cols)
+    x = torch.empty((rows, cols), device="cuda")
+    few = torch.randn((piece, cols), generator=torch.Generator(device="cuda").manual_seed(1), device="cuda")
+    for at in range(0, rows, piece):
+        x[at:at + piece] = few[:min(piece, rows - at)]
+    qlin.qlin_hadamard(x, 512, y=x)
+    want = qlin.qlin_hadamard(few, 512)
+    for at in range(0, rows, piece):
+        assert torch.equal(x[at:at + piece], want[:min(piece, rows - at)])
+    del x
+    torch.cuda.empty_cache()
+
+
+def test_weight_of_2_35_values():
+    torch = torch_cuda()
+    import w8a8_integer_linear_amd as qlin
+    rows, cols, piece = (1 << 24) + 1, 2048, 1 << 12
+    if torch.cuda.mem_get_info()[0] < 190 << 30:
+        pytest.skip("needs 190 GB of the card's memory")
+    announce("dequantize_weight", rows, cols)
+    g = torch.Generator(device="cuda").manual_seed(1)
+    few = torch.randint(-127, 128, (piece, cols), generator=g, device="cuda", dtype=torch.int8)
+    sw = torch.rand(piece, generator=g, device="cuda")
+    q, s = torch.empty((rows, cols), dtype=torch.int8, device="cuda"), torch.empty(rows, device="cuda")
+    for at in range(0, rows, piece):
+        n = min(piece, rows - at)
+        q[at:at + n], s[at:at + n] = few[:n], sw[:n]
+    for had in (0, 64):
+        w = qlin.qlin_dequantize_weight(q, s, had_block=had)
+        want = qlin.qlin_dequantize_weight(few, sw, had_block=had)
+        for at in range(0, rows, piece):
+            assert torch.equal(w[at:at + piece], want[:min(piece, rows - at)])
+        del w
+    del q
+    torch.cuda.empty_cache()

@@ -111,7 +111,7 @@ int qlin_dequantize_weight(const int8_t *qw, const float *sw, int64_t N, int64_t
     if (N > 0 && (overlap(w, sat_mul(N, K, 4), qw, sat_mul(N, K)) ||
                   overlap(w, sat_mul(N, K, 4), sw, sat_mul(N, 4))))
         return QLIN_EINVAL;
-    if (sat_mul(N, K) / 8 / 256 >= ((int64_t)1 << 31))
+    if (sat_mul(N, K) / 8 / 256 >= ((int64_t)1 << 31) || K > (int64_t)1 << 34)
         return QLIN_EUNSUPPORTED;
     if (N == 0)
         return QLIN_OK;

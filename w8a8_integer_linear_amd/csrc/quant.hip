@@ -775,14 +775,26 @@ __global__ __launch_bounds__(256) void dequant_weight_kernel(const int8_t *__res
         store8(w, c * 8, v);
 }
 
+// f(first of n elements, n) for launches of the two kernels above, which have a lane
+// per eight elements, of at most `most` of them: a grid's dimension holds fewer than
+// 2^32 threads (and starts only the remainder of more, with no error).
+template <typename F> static void for_pieces(int64_t n, int64_t most, F f)
+{
+    for (int64_t at = 0; at < n; at += most)
+        f(at, n - at < most ? n - at : most);
+}
+constexpr int64_t kLaunchElems = (int64_t)1 << 34;
+
 void launch_dequantize_weight(const int8_t *q, const float *sw, int64_t rows, int64_t cols,
                               int blk, float cb, float *w, hipStream_t st)
 {
-    const int64_t nch = rows * cols / 8;
-    const unsigned grid = (unsigned)((nch + 255) / 256);
     auto go = [&](auto h) {
-        hipLaunchKernelGGL((dequant_weight_kernel<decltype(h)::value>), dim3(grid), dim3(256), 0,
-                           st, q, sw, nch, cols, blk, cb, w);
+        // (Whole rows; a row is no longer than a launch.)
+        for_pieces(rows * cols, kLaunchElems / cols * cols, [&](int64_t at, int64_t n) {
+            hipLaunchKernelGGL((dequant_weight_kernel<decltype(h)::value>),
+                               dim3((unsigned)((n / 8 + 255) / 256)), dim3(256), 0, st, q + at,
+                               sw + at / cols, n / 8, cols, blk, cb, w + at);
+        });
     };
     switch (blk) {
     case 0: return go(std::integral_constant<int, 0>());
@@ -797,11 +809,14 @@ void launch_dequantize_weight(const int8_t *q, const float *sw, int64_t rows, in
 void launch_hadamard(const void *x, bool bf16, int64_t rows, int64_t cols, int blk, float cb,
                      float *y, hipStream_t st)
 {
-    const int64_t nch = rows * cols / 8;
-    const unsigned grid = (unsigned)((nch + 255) / 256);
     auto go = [&](auto bf, auto h) {
-        hipLaunchKernelGGL((hadamard_kernel<decltype(bf)::value, decltype(h)::value>), dim3(grid),
-                           dim3(256), 0, st, x, nch, blk, cb, y);
+        // (A piece's end is a block's.)
+        for_pieces(rows * cols, kLaunchElems, [&](int64_t at, int64_t n) {
+            const void *from = static_cast<const char *>(x) + at * (bf16 ? 2 : 4);
+            hipLaunchKernelGGL((hadamard_kernel<decltype(bf)::value, decltype(h)::value>),
+                               dim3((unsigned)((n / 8 + 255) / 256)), dim3(256), 0, st, from, n / 8, blk,
+                               cb, y + at);
+        });
     };
     auto with_block = [&](auto bf) {
         switch (blk) {
