@@ -317,7 +317,8 @@ size_t qlin_product_ws_bytes(int op, int64_t M, int64_t N, int64_t K);
  *   hi(seed)), i = n*K + k.  The result depends only on (inputs, lr, seed,
  *   step), so a run resumed at the same step reproduces it exactly.
  *   bias [N] and db [N] (both or neither): bias = fl(bias - fl(lr * db)).
- * K in [16, QLIN_MAX_ROW], a multiple of 16.
+ * K in [16, QLIN_MAX_ROW], a multiple of 16; 0 <= N < 2^24, above K = 16384 N < 2^22
+ * (a launch's rows; QLIN_EUNSUPPORTED otherwise).
  */
 int qlin_sgd_requant(int8_t *qw, float *sw, const float *dw, int64_t N, int64_t K,
                      float lr, uint64_t seed, uint64_t step, float *bias, const float *db,
@@ -337,7 +338,7 @@ int qlin_sgd_requant(int8_t *qw, float *sw, const float *dw, int64_t N, int64_t 
  * weight starts as the absmax weight s q (within the rounding of sw).  An
  * all-zero row gives g = sw = 0: callers reject it (a zero direction).
  *   q [N, K] int8, s [N] fp32 inputs; g, sw [N] fp32 outputs.
- *   N >= 0; K in [16, QLIN_WN_MAX_ROW], a multiple of 16.
+ *   0 <= N < 2^24; K in [16, QLIN_WN_MAX_ROW], a multiple of 16.
  */
 #define QLIN_WN_MAX_ROW 32768
 int qlin_wn_init(const int8_t *q, const float *s, int64_t N, int64_t K, float *g, float *sw,
@@ -360,7 +361,8 @@ int qlin_wn_init(const int8_t *q, const float *s, int64_t N, int64_t K, float *g
  *   q [N, K] int8, s, g, sw [N] fp32: read and overwritten (sw is only
  *   written).  dw [N, K] fp32.  bias, db [N] (both or neither): bias =
  *   fl(bias - fl(lr db)).
- *   N >= 0; K in [16, QLIN_WN_MAX_ROW], a multiple of 16; lr finite.
+ *   N as in qlin_sgd_requant; K in [16, QLIN_WN_MAX_ROW], a multiple of 16; lr
+ *   finite.
  */
 int qlin_wn_sgd_requant(int8_t *q, float *s, float *g, float *sw, const float *dw, int64_t N,
                         int64_t K, float lr, uint64_t seed, uint64_t step, float *bias,
@@ -388,7 +390,7 @@ int qlin_wn_sgd_requant(int8_t *q, float *s, float *g, float *sw, const float *d
  *   beta1, beta2 in [0, 1); eps > 0; weight_decay >= 0; all finite.
  *   bias, db, bias_m, bias_v: all four or none; the float bias [N] takes the
  *            same float update with its own moments [N].
- * N >= 0; K a multiple of 16, at most QLIN_MAX_ROW.
+ * N as in qlin_sgd_requant; K a multiple of 16, at most QLIN_MAX_ROW.
  */
 int qlin_adamw_requant(int8_t *qw, float *sw, const float *dw, float *m, float *v, int64_t N,
                        int64_t K, float lr, float beta1, float beta2, float eps,

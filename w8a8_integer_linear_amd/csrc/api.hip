@@ -14,6 +14,13 @@ namespace {
 
 constexpr int kAbiVersion = 1;
 
+// Whether one launch holds a weight update's rows of `threads` threads each: fewer
+// than 2^32 (of more, only the remainder would start, with no error).
+bool rows_fit(int64_t N, int64_t threads) { return N < ((int64_t)1 << 32) / threads; }
+
+// Threads of a row in the updates (sgd.hip).
+int64_t update_threads(int64_t K) { return K <= 16384 ? 256 : 1024; }
+
 // Longest contraction qlin_product_ws accepts (chunked into int32-exact pieces).
 constexpr int64_t kMaxLongContraction = ((int64_t)1 << 31) - 1;
 
@@ -419,7 +426,7 @@ int qlin_sgd_requant(int8_t *qw, float *sw, const float *dw, int64_t N, int64_t 
         return QLIN_EINVAL;
     if (!isfinite(lr))
         return QLIN_EINVAL;
-    if (K > QLIN_MAX_ROW || N > kMaxRows)
+    if (K > QLIN_MAX_ROW || !rows_fit(N, update_threads(K)))
         return QLIN_EUNSUPPORTED;
     if (N == 0)
         return QLIN_OK;
@@ -438,7 +445,7 @@ int qlin_wn_init(const int8_t *q, const float *s, int64_t N, int64_t K, float *g
     const int64_t n4 = sat_mul(N, 4);
     if (any && (overlap(g, n4, sw, n4) || overlap(g, n4, s, n4) || overlap(sw, n4, s, n4)))
         return QLIN_EINVAL;
-    if (K > QLIN_WN_MAX_ROW || N > kMaxRows)
+    if (K > QLIN_WN_MAX_ROW || !rows_fit(N, 256))
         return QLIN_EUNSUPPORTED;
     if (N == 0)
         return QLIN_OK;
@@ -462,7 +469,7 @@ int qlin_wn_sgd_requant(int8_t *q, float *s, float *g, float *sw, const float *d
     const int64_t n4 = sat_mul(N, 4);
     if (any && (overlap(g, n4, sw, n4) || overlap(g, n4, s, n4) || overlap(sw, n4, s, n4)))
         return QLIN_EINVAL;
-    if (K > QLIN_WN_MAX_ROW || N > kMaxRows)
+    if (K > QLIN_WN_MAX_ROW || !rows_fit(N, update_threads(K)))
         return QLIN_EUNSUPPORTED;
     if (N == 0)
         return QLIN_OK;
@@ -492,7 +499,7 @@ int qlin_adamw_requant(int8_t *qw, float *sw, const float *dw, float *m, float *
     const int64_t nf = sat_mul(N, K, 4);
     if (any && (overlap(m, nf, v, nf) || overlap(m, nf, dw, nf) || overlap(v, nf, dw, nf)))
         return QLIN_EINVAL;
-    if (K > QLIN_MAX_ROW || N > kMaxRows)
+    if (K > QLIN_MAX_ROW || !rows_fit(N, update_threads(K)))
         return QLIN_EUNSUPPORTED;
     if (N == 0)
         return QLIN_OK;
