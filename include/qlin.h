@@ -605,6 +605,100 @@ int qlin_adamw_tensors_plan(const qlin_tensor *tensors, int64_t count, void *ima
 int qlin_adamw_tensors(const void *image, int64_t count, int64_t chunks, double lr, double beta1,
                        double beta2, double eps, uint64_t seed, uint64_t step, void *stream);
 
+/* ------------------------------------------- inside a feed-forward block */
+
+/* Activations: z, max(z, 0), z s(z) with the logistic function s, z Phi(z) with the
+ * normal distribution function Phi, and its tanh form
+ * z / 2 (1 + tanh(sqrt(2 / pi) (z + 0.044715 z^3))). */
+enum {
+    QLIN_ACT_NONE = 0, QLIN_ACT_RELU = 1, QLIN_ACT_SILU = 2, QLIN_ACT_GELU = 3,
+    QLIN_ACT_GELU_TANH = 4
+};
+#define QLIN_CK_BLOCK 32                /* outputs that share a checkpoint's scale */
+#define QLIN_MAX_BLOCK_ROWS 67108864    /* weight rows of the calls below */
+
+/*
+ * Forward product of a feed-forward block with its activation:
+ *
+ *   z = qlin_fwd's output (sx sw (qx . qw^T) + bias, to the bit)       [M, N]
+ *   y = act(z) + residual                                              [M, N]
+ *
+ *   bias       [N] fp32 or NULL.
+ *   residual   [M, N] of res_dtype (QLIN_F32, QLIN_BF16) or NULL; added after the
+ *              activation, in fp32.  It may be y itself if both have one type.
+ *   y          [M, N] output of y_dtype, rounded once.
+ *   ck, ck_s   both or neither: the checkpoint of z that qlin_act_bwd takes.  ck
+ *              [M, N] int8 codes, ck_s [M, ceil(N / QLIN_CK_BLOCK)] fp32: each
+ *              row's z in blocks of QLIN_CK_BLOCK, s = fl(max|z| / 127), c =
+ *              rne(fl(z / s)), a zero block s = 0, c = 0.  A block that holds a
+ *              NaN or an infinity has a scale that is not finite.
+ * y is NaN where z is.  Shapes, limits and the workspace as in qlin_product_ws
+ * (a workspace of either call serves the other if it is large enough; calls that
+ * share one must not overlap in time); K <= QLIN_MAX_CONTRACTION, N <=
+ * QLIN_MAX_BLOCK_ROWS.
+ */
+int qlin_fwd_act(const int8_t *qx, const float *sx, const int8_t *qw, const float *sw,
+                 const float *bias, int act, const void *residual, int res_dtype, int64_t M,
+                 int64_t N, int64_t K, void *y, int y_dtype, int8_t *ck, float *ck_s,
+                 void *workspace, size_t ws_bytes, void *stream);
+size_t qlin_fwd_act_ws_bytes(int64_t M, int64_t N, int64_t K);
+
+/*
+ * Both projections of a gated block in one product, the activation of the one and
+ * the product with the other in its epilogue:
+ *
+ *   z = [g | u] = sx sw (qx . qw^T) + bias,   y = act(g) u             [M, F]
+ *
+ *   qw [2 F, K], sw, bias [2 F]: the gate's rows, then the other projection's.
+ *   ck [M, 2 F], ck_s [M, 2 ceil(F / QLIN_CK_BLOCK)]: the checkpoint of z, each
+ *   half in blocks of its own.
+ * Everything else as in qlin_fwd_act with N = 2 F; F a multiple of 16.
+ */
+int qlin_fwd_gated(const int8_t *qx, const float *sx, const int8_t *qw, const float *sw,
+                   const float *bias, int act, int64_t M, int64_t F, int64_t K, void *y,
+                   int y_dtype, int8_t *ck, float *ck_s, void *workspace, size_t ws_bytes,
+                   void *stream);
+size_t qlin_fwd_gated_ws_bytes(int64_t M, int64_t F, int64_t K);
+
+/*
+ * Backward of qlin_fwd_act (gated 0) or qlin_fwd_gated (gated 1) from their
+ * checkpoint, z^ = ck_s ck, up to the gradient's quantization:
+ *
+ *   dz = dy act'(z^)                                                   [M, F]
+ *   dz = [dy u^ act'(g^) | dy act(g^)]                                 [M, 2 F]
+ *   s1[m] = max over n of |dz sw[n]| / 127,  s2[n] = max over m of |dz sx[m]| / 127
+ *   db[n] = sum over m of dz
+ *
+ * With N = F or 2 F:
+ *   dy      [M, F] of dy_dtype; the residual's gradient is dy itself.
+ *   sw, s1  [N] and [M] fp32, both or neither; sx, s2 [M] and [N] fp32, both or
+ *           neither: the scales qlin_quantize_grad defines, for
+ *           qlin_quantize_grad_scaled.
+ *   db      [N] fp32 or NULL: the bias's gradient.
+ *   dz      [M, N] output of dz_dtype.
+ * s1, s2 and db are those of the fp32 values that dz rounds; sums are fp32 in a
+ * fixed order.  relu's derivative at 0 is 0.  A row (column) of dz with a NaN or an
+ * infinity has an s1 (s2) that is not finite.  M >= 0; F a multiple of 16, N <=
+ * QLIN_MAX_BLOCK_ROWS.  No rows: s2 and db are zeros.
+ * workspace: qlin_act_bwd_ws_bytes bytes, any contents.
+ */
+int qlin_act_bwd(const void *dy, int dy_dtype, const int8_t *ck, const float *ck_s, int act,
+                 int gated, const float *sw, const float *sx, int64_t M, int64_t F, void *dz,
+                 int dz_dtype, float *s1, float *s2, float *db, void *workspace, size_t ws_bytes,
+                 void *stream);
+size_t qlin_act_bwd_ws_bytes(int64_t M, int64_t F, int gated);
+
+/*
+ * The codes of qlin_quantize_grad for scales that are known (s1 and s2 of
+ * qlin_act_bwd, or of another call on the same gradient):
+ *   q1 = rne(fl(fl(dy sw[n]) / s1[m])),  q2 = rne(fl(fl(dy sx[m]) / s2[n])),
+ * [M, N] int8 each.  The scales have to be at least |dy sw| / 127.49 and |dy sx| /
+ * 127.49, which those of the fp32 values of a dy rounded to bf16 are.
+ */
+int qlin_quantize_grad_scaled(const void *dy, int dtype, int64_t M, int64_t N, const float *sw,
+                              const float *sx, const float *s1, const float *s2, int8_t *q1,
+                              int8_t *q2, void *stream);
+
 #ifdef __cplusplus
 }
 #endif

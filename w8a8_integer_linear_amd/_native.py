@@ -20,6 +20,8 @@ QLIN_F32, QLIN_BF16 = 0, 1
 QLIN_OP_FWD, QLIN_OP_DX, QLIN_OP_DW = 0, 1, 2
 MAX_CONTRACTION = 131071
 MAX_RANK, MAX_ADAPTERS = 128, 1023
+ACTIVATIONS = {"none": 0, "relu": 1, "silu": 2, "gelu": 3, "gelu_tanh": 4}
+CK_BLOCK = 32
 
 # Exported symbols and their C signatures (kept in step with include/qlin.h).
 _vp, _i64, _i32, _f32, _u64 = (ctypes.c_void_p, ctypes.c_int64, ctypes.c_int, ctypes.c_float,
@@ -77,6 +79,15 @@ SIGNATURES = {
     "qlin_adamw_tensors_plan_bytes": ([_tensors, _i64], _size),
     "qlin_adamw_tensors_plan": ([_tensors, _i64, _vp, _size], _i32),
     "qlin_adamw_tensors": ([_vp, _i64, _i64, _f64, _f64, _f64, _f64, _u64, _u64, _vp], _i32),
+    "qlin_fwd_act": ([_vp] * 5 + [_i32, _vp, _i32] + [_i64] * 3 + [_vp, _i32, _vp, _vp, _vp, _size, _vp],
+                     _i32),
+    "qlin_fwd_act_ws_bytes": ([_i64] * 3, _size),
+    "qlin_fwd_gated": ([_vp] * 5 + [_i32] + [_i64] * 3 + [_vp, _i32, _vp, _vp, _vp, _size, _vp], _i32),
+    "qlin_fwd_gated_ws_bytes": ([_i64] * 3, _size),
+    "qlin_act_bwd": ([_vp, _i32, _vp, _vp, _i32, _i32, _vp, _vp, _i64, _i64, _vp, _i32] + [_vp] * 4
+                     + [_size, _vp], _i32),
+    "qlin_act_bwd_ws_bytes": ([_i64, _i64, _i32], _size),
+    "qlin_quantize_grad_scaled": ([_vp, _i32, _i64, _i64] + [_vp] * 7, _i32),
 }
 MFMA_CEILING_FRAG_BYTES = 24 * 1024
 NOALLOC_SCRATCH_BYTES = 4096 + 160 * 262144
@@ -679,3 +690,150 @@ def qlin_adamw_tensors(plan, lr, beta1, beta2, eps, seed, step, stream=None):
     plan.used_on(handle)
     _check("qlin_adamw_tensors", lib().qlin_adamw_tensors(
         _ptr(plan.image), plan.count, plan.chunks, lr, beta1, beta2, eps, int(seed), int(step), handle))
+
+
+# ---------------------------------------------- inside a feed-forward block
+
+def _on_device(f):
+    """Runs f on its first tensor's device, which all its tensors have to be on."""
+    @functools.wraps(f)
+    def call(first, *args, **kw):
+        device = first.get_device() if isinstance(first, torch.Tensor) else -1
+        for t in (*args, *kw.values()):
+            if isinstance(t, torch.Tensor) and t.get_device() != device:
+                raise ValueError(f"the tensors are on different devices ({t.device} and {first.device})")
+        if device < 0 or device == torch._C._cuda_getDevice():
+            return f(first, *args, **kw)
+        with torch.cuda.device(device):
+            return f(first, *args, **kw)
+    return call
+
+
+def _act_code(act):
+    code = ACTIVATIONS.get(act)
+    if code is None:
+        raise ValueError(f"act is one of {sorted(ACTIVATIONS)}, got {act!r}")
+    return code
+
+
+def _forward(name, gated, qx, sx, qw, sw, bias, act, residual, y, dtype, ck, ck_s, save, workspace, stream):
+    code = _act_code(act)
+    M, K = qx.shape
+    N = qw.shape[0]
+    if gated and N % 2:
+        raise ValueError(f"qw has the gate's rows and as many others, got {N}")
+    F = N // 2 if gated else N
+    px, pw = _addr(qx, "qx", torch.int8), _addr(qw, "qw", torch.int8, N, K)
+    psx, psw = _addr(sx, "sx", torch.float32, M), _addr(sw, "sw", torch.float32, N)
+    pb = None if bias is None else _addr(bias, "bias", torch.float32, N)
+    y = _new(qx, dtype, M, F) if y is None else y
+    py, y_code = _addr(y, "y", y.dtype, M, F), _dtype_code(y)
+    pck = pcs = None
+    if save or ck is not None or ck_s is not None:
+        per = (N // F) * -(-F // CK_BLOCK) if F else 0
+        ck = _new(qx, torch.int8, M, N) if ck is None else ck
+        ck_s = _new(qx, torch.float32, M, per) if ck_s is None else ck_s
+        pck, pcs = _addr(ck, "ck", torch.int8, M, N), _addr(ck_s, "ck_s", torch.float32, M, per)
+    need = qlin_fwd_gated_ws_bytes if gated else qlin_fwd_act_ws_bytes
+    workspace, pws, size = _workspace(workspace, lambda: need(M, F, K), qx, zero=True)
+    if gated:
+        status = lib().qlin_fwd_gated(px, psx, pw, psw, pb, code, M, F, K, py, y_code, pck, pcs, pws, size,
+                                      _stream(stream))
+    else:
+        pr, r_code = None, 0
+        if residual is not None:
+            pr, r_code = _addr(residual, "residual", residual.dtype, M, N), _dtype_code(residual)
+        status = lib().qlin_fwd_act(px, psx, pw, psw, pb, code, pr, r_code, M, N, K, py, y_code, pck, pcs,
+                                    pws, size, _stream(stream))
+    _check(name, status)
+    return y, ck, ck_s
+
+
+@functools.lru_cache(maxsize=1024)
+def qlin_fwd_act_ws_bytes(M, N, K):
+    return int(lib().qlin_fwd_act_ws_bytes(int(M), int(N), int(K)))
+
+
+@_on_device
+@_on_stream
+def qlin_fwd_act(qx, sx, qw, sw, bias=None, act="none", residual=None, y=None, dtype=torch.bfloat16, ck=None,
+                 ck_s=None, save=False, workspace=None, stream=None):
+    """act(z) + residual with z = qlin_fwd(...), rounded once to y's type (dtype where
+    y is not given).  save, or ck and ck_s: keeps the 8-bit checkpoint of z for
+    qlin_act_bwd.  Returns (y, ck, ck_s); ck and ck_s are None without a checkpoint."""
+    return _forward("qlin_fwd_act", False, qx, sx, qw, sw, bias, act, residual, y, dtype, ck, ck_s, save,
+                    workspace, stream)
+
+
+@functools.lru_cache(maxsize=1024)
+def qlin_fwd_gated_ws_bytes(M, F, K):
+    return int(lib().qlin_fwd_gated_ws_bytes(int(M), int(F), int(K)))
+
+
+@_on_device
+@_on_stream
+def qlin_fwd_gated(qx, sx, qw, sw, bias=None, act="silu", y=None, dtype=torch.bfloat16, ck=None, ck_s=None,
+                   save=False, workspace=None, stream=None):
+    """act(g) u with [g | u] = qlin_fwd(...); qw [2 F, K] has the gate's rows first.
+    Everything else as in qlin_fwd_act."""
+    return _forward("qlin_fwd_gated", True, qx, sx, qw, sw, bias, act, None, y, dtype, ck, ck_s, save,
+                    workspace, stream)
+
+
+@functools.lru_cache(maxsize=1024)
+def qlin_act_bwd_ws_bytes(M, F, gated=False):
+    return int(lib().qlin_act_bwd_ws_bytes(int(M), int(F), int(gated)))
+
+
+@_on_device
+@_on_stream
+def qlin_act_bwd(dy, ck, ck_s, act, gated=False, sw=None, sx=None, dz=None, dtype=torch.bfloat16, s1=None,
+                 s2=None, db=None, want_db=False, workspace=None, stream=None):
+    """Backward of qlin_fwd_act or qlin_fwd_gated from their checkpoint.  Returns (dz,
+    s1, s2, db): dz of the given tensor's type or of dtype, the scales of its two
+    quantizations (s1 where sw is given, s2 where sx is, for
+    qlin_quantize_grad_scaled), db where it is given or wanted."""
+    code = _act_code(act)
+    M, F = dy.shape
+    N = 2 * F if gated else F
+    per = (2 if gated else 1) * -(-F // CK_BLOCK)
+    pdy, dy_code = _addr(dy, "dy", dy.dtype), _dtype_code(dy)
+    pck, pcs = _addr(ck, "ck", torch.int8, M, N), _addr(ck_s, "ck_s", torch.float32, M, per)
+    dz = _new(dy, dtype, M, N) if dz is None else dz
+    pdz, dz_code = _addr(dz, "dz", dz.dtype, M, N), _dtype_code(dz)
+    psw = psx = p1 = p2 = pdb = None
+    if sw is not None:
+        s1 = _new(dy, torch.float32, M) if s1 is None else s1
+        psw, p1 = _addr(sw, "sw", torch.float32, N), _addr(s1, "s1", torch.float32, M)
+    elif s1 is not None:
+        raise ValueError("s1 needs sw")
+    if sx is not None:
+        s2 = _new(dy, torch.float32, N) if s2 is None else s2
+        psx, p2 = _addr(sx, "sx", torch.float32, M), _addr(s2, "s2", torch.float32, N)
+    elif s2 is not None:
+        raise ValueError("s2 needs sx")
+    if db is None and want_db:
+        db = _new(dy, torch.float32, N)
+    if db is not None:
+        pdb = _addr(db, "db", torch.float32, N)
+    workspace, pws, size = _workspace(workspace, lambda: qlin_act_bwd_ws_bytes(M, F, bool(gated)), dy,
+                                      zero=False)
+    _check("qlin_act_bwd", lib().qlin_act_bwd(
+        pdy, dy_code, pck, pcs, code, int(bool(gated)), psw, psx, M, F, pdz, dz_code, p1, p2, pdb, pws, size,
+        _stream(stream)))
+    return dz, s1, s2, db
+
+
+@_on_device
+@_on_stream
+def qlin_quantize_grad_scaled(dy, sw, sx, s1, s2, q1=None, q2=None, stream=None):
+    """qlin_quantize_grad's codes for known scales.  Returns (q1, q2)."""
+    M, N = dy.shape
+    pdy, code = _addr(dy, "dy", dy.dtype), _dtype_code(dy)
+    q1 = _new(dy, torch.int8, M, N) if q1 is None else q1
+    q2 = _new(dy, torch.int8, M, N) if q2 is None else q2
+    _check("qlin_quantize_grad_scaled", lib().qlin_quantize_grad_scaled(
+        pdy, code, M, N, _addr(sw, "sw", torch.float32, N), _addr(sx, "sx", torch.float32, M),
+        _addr(s1, "s1", torch.float32, M), _addr(s2, "s2", torch.float32, N),
+        _addr(q1, "q1", torch.int8, M, N), _addr(q2, "q2", torch.int8, M, N), _stream(stream)))
+    return q1, q2

@@ -1,0 +1,259 @@
+// Backward of a feed-forward block's activation and gate from the 8-bit checkpoint of
+// their input, up to the scales of the gradient's two quantizations: one pass over
+// dy and the checkpoint that writes dz and leaves row maxima, column maxima and
+// column sums as partials, and a small launch that reduces them.
+#include <type_traits>
+
+#include "act.hpp"
+#include "common.hpp"
+#include "launch.hpp"
+#include "lowp.hpp"
+
+namespace qlin {
+
+namespace {
+
+constexpr int kCols = 512;      // outputs of a wave's window: eight per lane
+constexpr int kWaves = 4;       // of a workgroup, one window, other rows
+constexpr int kBatch = 4;       // rows a lane loads before it uses any of them
+constexpr int kGroups = 1024;   // workgroups aimed at: four per compute unit
+
+struct Args {
+    ActBackward a;
+    int64_t N;                  // F, or 2 F with a gate
+    int64_t per, all;           // checkpoint scales of a half and of a row
+    float *rowpart;             // [windows, M]
+    float *colpart;             // [2 groups, N]: maxima, then sums, of a row group
+};
+
+// dz of one row's eight outputs, the gate's (and, with a gate, the other half's in
+// d[8 ..]).
+template <int ACT, bool GATED>
+__device__ __forceinline__ void dz8(const float dy[8], i32x2 cg, float sg, i32x2 cu, float su,
+                                    float *d)
+{
+    float g[8], u[8];
+    codes_to_float(cg, g);
+    if constexpr (GATED)
+        codes_to_float(cu, u);
+#pragma unroll
+    for (int e = 0; e < 8; e++) {
+        float value, slope;
+        act_slope<ACT>(g[e] * sg, value, slope);
+        if constexpr (GATED) {
+            d[e] = dy[e] * (u[e] * su) * slope;
+            d[8 + e] = dy[e] * value;
+        } else {
+            d[e] = dy[e] * slope;
+        }
+    }
+}
+
+template <int ACT, bool GATED, bool DY_BF16, bool DZ_BF16>
+__global__ __launch_bounds__(256) void act_bwd_kernel(Args p)
+{
+    constexpr int H = GATED ? 2 : 1, E = 8 * H;
+    __shared__ float red[2][kWaves - 1][E][kWave];
+    const int lane = __lane_id();
+    const int wave = __builtin_amdgcn_readfirstlane((int)(threadIdx.x / kWave));
+    const int64_t F = p.a.F, N = p.N, M = p.a.M;
+    const int64_t win = blockIdx.x;
+    const int c0 = lane * 8;
+    const int64_t left = F - win * kCols;
+    const bool ok = c0 < left;          // then all eight are (F is a multiple of 16)
+    // Lanes past the last output read it again; what they compute goes nowhere.
+    const uint32_t c = ok ? c0 : (uint32_t)left - 8;
+    float w[E], mx[E], sm[E];
+#pragma unroll
+    for (int e = 0; e < E; e++) {
+        w[e] = p.a.sw ? p.a.sw[win * kCols + c + (e >= 8 ? F : 0) + e % 8] : 0.0f;
+        if (!ok)
+            w[e] = 0.0f;
+        mx[e] = sm[e] = 0.0f;
+    }
+    const int64_t step = (int64_t)gridDim.y * kWaves * kBatch;
+    for (int64_t rb = ((int64_t)blockIdx.y * kWaves + wave) * kBatch; rb < M; rb += step) {
+        Raw8<DY_BF16> dy[kBatch];
+        i32x2 q[kBatch][H];
+        float s[kBatch][H], px[kBatch];
+#pragma unroll
+        for (int u = 0; u < kBatch; u++) {
+            const int64_t r = rb + u < M ? rb + u : M - 1;
+            dy[u] = load_raw8<DY_BF16>(static_cast<const char *>(p.a.dy) + (r * F + win * kCols) * (DY_BF16 ? 2 : 4), c);
+#pragma unroll
+            for (int h = 0; h < H; h++) {
+                q[u][h] = *reinterpret_cast<const i32x2 *>(p.a.ck + r * N + h * F + win * kCols + c);
+                s[u][h] = (p.a.ck_s + r * p.all + h * p.per + win * (kCols / kCkBlock))[c / kCkBlock];
+            }
+            px[u] = p.a.sx ? p.a.sx[r] : 0.0f;
+        }
+        float rm[kBatch];
+#pragma unroll
+        for (int u = 0; u < kBatch; u++) {
+            rm[u] = 0.0f;
+            if (rb + u >= M)
+                continue;
+            float v[8], d[E];
+            unpack8<DY_BF16>(dy[u], v);
+            dz8<ACT, GATED>(v, q[u][0], s[u][0], q[u][H - 1], s[u][H - 1], d);
+#pragma unroll
+            for (int e = 0; e < E; e++) {
+                sm[e] = sm[e] + d[e];
+                mx[e] = max_nan(mx[e], __builtin_fabsf(d[e] * px[u]));
+                rm[u] = max_nan(rm[u], __builtin_fabsf(d[e] * w[e]));
+            }
+            if (ok) {
+#pragma unroll
+                for (int h = 0; h < H; h++) {
+                    const int64_t at = (rb + u) * N + h * F + win * kCols;
+                    if constexpr (DZ_BF16)
+                        *reinterpret_cast<i32x4 *>(static_cast<uint16_t *>(p.a.dz) + at + c) = pack_bf16x8(d + 8 * h);
+                    else
+                        store8(static_cast<float *>(p.a.dz) + at, c, d + 8 * h);
+                }
+            }
+        }
+        if (p.a.sw) {
+            float m = 0.0f;
+#pragma unroll
+            for (int u = 0; u < kBatch; u++) {
+                const float t = wave_all(ok ? rm[u] : 0.0f, [](float a, float b) { return max_nan(a, b); });
+                m = lane == u ? t : m;
+            }
+            if (lane < kBatch && rb + lane < M)
+                p.rowpart[win * M + rb + lane] = m;
+        }
+    }
+    if (wave > 0) {
+#pragma unroll
+        for (int e = 0; e < E; e++) {
+            red[0][wave - 1][e][lane] = mx[e];
+            red[1][wave - 1][e][lane] = sm[e];
+        }
+    }
+    __syncthreads();
+    if (wave > 0 || !ok)
+        return;
+#pragma unroll
+    for (int k = 0; k < kWaves - 1; k++)
+#pragma unroll
+        for (int e = 0; e < E; e++) {
+            mx[e] = max_nan(mx[e], red[0][k][e][lane]);
+            sm[e] = sm[e] + red[1][k][e][lane];
+        }
+    float *out = p.colpart + 2 * (int64_t)blockIdx.y * N + win * kCols;
+#pragma unroll
+    for (int h = 0; h < H; h++) {
+        store8(out + h * F, c, mx + 8 * h);
+        store8(out + N + h * F, c, sm + 8 * h);
+    }
+}
+
+// Partials -> s1, s2 and db.  The first ceil(N / 64) workgroups own 64 columns each,
+// their 16 waves every 16th row group, combined through LDS in a fixed order; the
+// workgroups after them own 1024 rows each.
+__global__ __launch_bounds__(1024) void act_bwd_scales_kernel(const float *__restrict__ rowpart, int wins,
+                                                              const float *__restrict__ colpart, int groups,
+                                                              int64_t M, int64_t N, float *__restrict__ s1,
+                                                              float *__restrict__ s2, float *__restrict__ db)
+{
+    const int64_t cblocks = (N + 63) / 64;
+    if ((int64_t)blockIdx.x >= cblocks) {
+        const int64_t r = ((int64_t)blockIdx.x - cblocks) * 1024 + threadIdx.x;
+        if (r < M) {
+            float m = 0.0f;
+            for (int k = 0; k < wins; k++)
+                m = max_nan(m, rowpart[k * M + r]);
+            s1[r] = m / 127.0f;
+        }
+        return;
+    }
+    __shared__ float red_max[16][64], red_sum[16][64];
+    const int lc = threadIdx.x % 64, sl = threadIdx.x / 64;
+    const int64_t c = (int64_t)blockIdx.x * 64 + lc;
+    float m = 0.0f, sum = 0.0f;
+    if (c < N) {
+#pragma unroll 4
+        for (int g = sl; g < groups; g += 16) {
+            m = max_nan(m, colpart[(2 * (int64_t)g) * N + c]);
+            sum = sum + colpart[(2 * (int64_t)g + 1) * N + c];
+        }
+    }
+    red_max[sl][lc] = m;
+    red_sum[sl][lc] = sum;
+    __syncthreads();
+    if (sl == 0 && c < N) {
+#pragma unroll
+        for (int i = 1; i < 16; i++) {
+            m = max_nan(m, red_max[i][lc]);
+            sum = sum + red_sum[i][lc];
+        }
+        if (s2)
+            s2[c] = m / 127.0f;
+        if (db)
+            db[c] = sum;
+    }
+}
+
+// Windows of a row and row groups: about kGroups workgroups, at most one per
+// kWaves * kBatch rows.
+struct Shape {
+    int64_t wins, groups;
+};
+Shape shape_of(int64_t M, int64_t F)
+{
+    const int64_t wins = (F + kCols - 1) / kCols, most = (M + kWaves * kBatch - 1) / (kWaves * kBatch);
+    const int64_t groups = (kGroups + wins - 1) / wins;
+    return {wins, groups < most ? groups : most};
+}
+
+} // namespace
+
+size_t act_bwd_bytes(int64_t M, int64_t F, bool gated)
+{
+    const Shape s = shape_of(M, F);
+    const int64_t rows = (s.wins * M + 3) / 4 * 4;      // (16-byte steps)
+    return (size_t)(rows + 2 * s.groups * F * (gated ? 2 : 1)) * 4;
+}
+
+void launch_act_bwd(const ActBackward &a, void *ws, hipStream_t st)
+{
+    const Shape sh = shape_of(a.M, a.F);
+    Args p{};
+    p.a = a;
+    p.N = a.gated ? 2 * a.F : a.F;
+    p.per = (a.F + kCkBlock - 1) / kCkBlock;
+    p.all = a.gated ? 2 * p.per : p.per;
+    p.rowpart = static_cast<float *>(ws);
+    p.colpart = p.rowpart + (sh.wins * a.M + 3) / 4 * 4;
+    auto go = [&](auto act, auto gated, auto dy, auto dz) {
+        hipLaunchKernelGGL((act_bwd_kernel<decltype(act)::value, decltype(gated)::value, decltype(dy)::value,
+                                           decltype(dz)::value>),
+                           dim3((unsigned)sh.wins, (unsigned)sh.groups), dim3(kWaves * kWave), 0, st, p);
+    };
+    auto with_dz = [&](auto act, auto gated, auto dy) {
+        a.dz_bf16 ? go(act, gated, dy, std::true_type()) : go(act, gated, dy, std::false_type());
+    };
+    auto with_dy = [&](auto act, auto gated) {
+        a.dy_bf16 ? with_dz(act, gated, std::true_type()) : with_dz(act, gated, std::false_type());
+    };
+    auto with_act = [&](auto act) {
+        a.gated ? with_dy(act, std::true_type()) : with_dy(act, std::false_type());
+    };
+    if (a.M > 0) {
+        switch (a.act) {
+        case QLIN_ACT_NONE: with_act(std::integral_constant<int, QLIN_ACT_NONE>()); break;
+        case QLIN_ACT_RELU: with_act(std::integral_constant<int, QLIN_ACT_RELU>()); break;
+        case QLIN_ACT_SILU: with_act(std::integral_constant<int, QLIN_ACT_SILU>()); break;
+        case QLIN_ACT_GELU: with_act(std::integral_constant<int, QLIN_ACT_GELU>()); break;
+        default: with_act(std::integral_constant<int, QLIN_ACT_GELU_TANH>()); break;
+        }
+    }
+    // (s1 and its workgroups only where it is asked for.)
+    const unsigned blocks = (unsigned)((p.N + 63) / 64 + (a.s1 ? (a.M + 1023) / 1024 : 0));
+    if (a.s1 || a.s2 || a.db)
+        hipLaunchKernelGGL(act_bwd_scales_kernel, dim3(blocks), dim3(1024), 0, st, p.rowpart, (int)sh.wins,
+                           p.colpart, (int)sh.groups, a.M, p.N, a.s1, a.s2, a.db);
+}
+
+} // namespace qlin

@@ -15,32 +15,6 @@
 
 namespace {
 
-int64_t size_of(int dtype) { return dtype == QLIN_BF16 ? 2 : 4; }
-
-// A byte range; [p, p + n).
-struct Range {
-    const void *p;
-    int64_t n;
-};
-
-// Whether any of the written ranges meets another range of either list.
-template <size_t W, size_t R>
-bool clash(const Range (&written)[W], const Range (&read)[R])
-{
-    for (size_t i = 0; i < W; i++) {
-        for (size_t j = i + 1; j < W; j++)
-            if (overlap(written[i].p, written[i].n, written[j].p, written[j].n))
-                return true;
-        for (size_t j = 0; j < R; j++)
-            if (overlap(written[i].p, written[i].n, read[j].p, read[j].n))
-                return true;
-    }
-    return false;
-}
-
-// Like overlap, but the same array twice is allowed (an in-place call).
-bool partly(const void *a, const void *b, int64_t n) { return a != b && overlap(a, n, b, n); }
-
 size_t round256(size_t n) { return (n + 255) & ~(size_t)255; }
 
 bool adapter_shape_ok(int64_t M, int64_t N, int64_t K, int64_t L, int64_t R)

@@ -48,6 +48,32 @@ inline bool overlap(const void *a, int64_t na, const void *b, int64_t nb)
     return x < ye && y < xe;
 }
 
+inline int64_t size_of(int dtype) { return dtype == QLIN_BF16 ? 2 : 4; }
+
+// A byte range; [p, p + n).
+struct Range {
+    const void *p;
+    int64_t n;
+};
+
+// Whether any of the written ranges meets another range of either list.
+template <size_t W, size_t R>
+bool clash(const Range (&written)[W], const Range (&read)[R])
+{
+    for (size_t i = 0; i < W; i++) {
+        for (size_t j = i + 1; j < W; j++)
+            if (overlap(written[i].p, written[i].n, written[j].p, written[j].n))
+                return true;
+        for (size_t j = 0; j < R; j++)
+            if (overlap(written[i].p, written[i].n, read[j].p, read[j].n))
+                return true;
+    }
+    return false;
+}
+
+// Like overlap, but the same array twice is allowed (an in-place call).
+inline bool partly(const void *a, const void *b, int64_t n) { return a != b && overlap(a, n, b, n); }
+
 // Largest token count a call accepts (grid dimensions and int32 tile indices).
 constexpr int64_t kMaxRows = (int64_t)1 << 30;
 

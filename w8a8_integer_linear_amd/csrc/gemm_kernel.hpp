@@ -40,6 +40,7 @@
 
 #include <utility>
 
+#include "act.hpp"
 #include "adapter_frag.hpp"
 #include "common.hpp"
 #include "launch.hpp"
@@ -77,6 +78,8 @@ struct GemmParams {
     unsigned *count;
     // EPI_*_ADAPTER: the low-rank term added to the dequantized outputs.
     AdapterEpilogue ad;
+    // EPI_ACT and above.
+    ActEpilogue act;
 };
 
 // ------------------------------------------------------------------ staging
@@ -93,6 +96,8 @@ constexpr uint32_t kOob = 0x7FFFFFF0u;
 // Cache policy of buffer accesses that must be coherent across the XCDs'
 // L2s (sc1, the device-scope bit).
 constexpr int kCoherent = 16;
+// Cache policy of a store that nothing reads soon (nt).
+constexpr int kNonTemporal = 2;
 
 __device__ __forceinline__ __amdgpu_buffer_rsrc_t make_rsrc(const int8_t *base,
                                                           uint32_t records = kOob)
@@ -302,7 +307,10 @@ __device__ __forceinline__ void barrier_no_fence()
 // fp32, three bf16 terms).
 enum {
     EPI_RAW = 0, EPI_ROWSCALE = 1, EPI_FWD = 2, EPI_ROWSCALE_HAD = 3, EPI_FWD_ADAPTER_BF16 = 4,
-    EPI_FWD_ADAPTER_F32 = 5, EPI_HAD_ADAPTER_BF16 = 6, EPI_HAD_ADAPTER_TERMS = 7
+    EPI_FWD_ADAPTER_F32 = 5, EPI_HAD_ADAPTER_BF16 = 6, EPI_HAD_ADAPTER_TERMS = 7,
+    // The forward product with an activation (EPI_ACT + QLIN_ACT_*), and with a
+    // gate beside it (EPI_GATED + QLIN_ACT_*).
+    EPI_ACT = 16, EPI_GATED = 32
 };
 
 // Tile order: workgroups are dispatched round-robin over the 8 XCDs, so
@@ -778,6 +786,236 @@ template <int QT, int FM, int FN> struct AdapterTerm {
     }
 };
 
+// Lane offset of load q of a gated product's B tile (lane_offset of its output's row):
+// rows 64 g + r and 64 g + 32 + r of the tile, r < 32, are the two rows of output
+// 32 g + r.
+template <typename OpB>
+__device__ __forceinline__ uint32_t gated_offset(int q, int w, int64_t ld, int lim)
+{
+    int gi, gk;
+    OpB::lane_slot(q, w, gi, gk);
+    const int out = gi / 64 * 32 + gi % 32;
+    return out < lim ? (uint32_t)((int64_t)out * ld + gk) : kOob;
+}
+
+// Maximum of |v| over a lane's two blocks of four and over the four lanes that hold
+// the rest of the row's 32 outputs; NaN if any is.
+__device__ __forceinline__ float ck_max(const float (&x)[4], const float (&y)[4])
+{
+    float m = 0.0f;
+#pragma unroll
+    for (int e = 0; e < 4; e++)
+        m = max_nan(max_nan(m, __builtin_fabsf(x[e])), __builtin_fabsf(y[e]));
+    const uint32_t u = __float_as_uint(m);
+    const auto s16 = __builtin_amdgcn_permlane16_swap(u, u, false, false);
+    m = max_nan(__uint_as_float(s16[0]), __uint_as_float(s16[1]));
+    const uint32_t v = __float_as_uint(m);
+    const auto s32 = __builtin_amdgcn_permlane32_swap(v, v, false, false);
+    return max_nan(__uint_as_float(s32[0]), __uint_as_float(s32[1]));
+}
+
+// Epilogue of a forward product in a feed-forward block: z = dequantized sums plus
+// bias, exactly as the plain forward's; the checkpoint's codes rne(fl(z / s)), s =
+// fl(max / 127) per 32 outputs; y = act(z) + residual, or act(z) times the other
+// half's z.
+//
+// The wave's 128 rows go in passes through its 16 KiB of the idle stage buffers, so
+// that global accesses are runs of whole rows: y as fp32 in the first 8 KiB, the
+// codes in the next 4 (64 bytes per row: its outputs', with a gate 32 of each
+// half).  The residual is loaded in the order y is stored in, a pass ahead of its
+// use and before the previous pass's stores (a load's wait also waits for the stores
+// issued before it).
+template <bool GATED, int ACT, int FM, int FN>
+__device__ __forceinline__ void act_epilogue(const GemmParams &p, const i32x4 (&acc)[FM][FN],
+                                             lds_i8 *slice, int i, int j)
+{
+    typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
+    typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
+    typedef __attribute__((address_space(3))) u32x4 lds_u32x4;
+    typedef __attribute__((address_space(3))) uint32_t lds_u32;
+    static_assert(FN == 4, "64 columns of the product per wave");
+    constexpr int CW = GATED ? 32 : 64;             // outputs per wave and row
+    constexpr int kBlocks = GATED ? 4 : 1;          // row blocks per pass: 8 or 4 KiB of y
+    constexpr int kRows = 16 * kBlocks, kPasses = FM / kBlocks;
+    constexpr int kChunks = CW / 4;                 // 4 outputs each
+    constexpr int kRowsPer = kWave / kChunks, kStores = kRows / kRowsPer;
+    lds_i8 *codes = slice + 8192;
+    i = __builtin_amdgcn_readfirstlane(i);
+    j = __builtin_amdgcn_readfirstlane(j);
+    const ActEpilogue &e = p.act;
+    const int lane = __lane_id(), r = lane % 16, h = lane / 16;
+    const int F = p.S;
+    const int64_t N = GATED ? 2 * (int64_t)F : F;
+    // The lane's columns: output 16 (b % (FN / halves)) + 4 h + 0 .. 3 of the wave's.
+    f32x4 cs[FN], bj[FN];
+#pragma unroll
+    for (int b = 0; b < FN; b++) {
+        const int o = j + 16 * (GATED ? b & 1 : b) + 4 * h;
+        const int64_t n = o + (GATED && b >= 2 ? (int64_t)F : 0);
+        const bool ok = o < F;
+        cs[b] = ok ? *reinterpret_cast<const f32x4 *>(p.scol + n) : f32x4{0, 0, 0, 0};
+        bj[b] = ok && p.bias ? *reinterpret_cast<const f32x4 *>(p.bias + n) : f32x4{0, 0, 0, 0};
+    }
+    float rsv[FM];
+#pragma unroll
+    for (int a = 0; a < FM; a++)
+        rsv[a] = i + 16 * a + r < p.R ? p.srow[i + 16 * a + r] : 0.0f;
+    // Access k of a pass: row k kRowsPer + sr, outputs 4 sc .. + 3 of the wave's.  Each
+    // goes through a buffer resource from its first row, whose extent drops rows past
+    // the last; the lanes' offsets, kOob past the last column, stay below that by
+    // QLIN_MAX_BLOCK_ROWS.
+    const int sr = lane / kChunks, sc = lane % kChunks;
+    const uint32_t lane_at = (uint32_t)sr * (uint32_t)F + 4 * sc;
+    const uint32_t at2 = j + 4 * sc < F ? lane_at * 2 : kOob, at4 = j + 4 * sc < F ? lane_at * 4 : kOob;
+    // Rows from m of an array whose rows hold n elements of size bytes, from column j.
+    auto rows_from = [&](const void *base, int m, int64_t n, int size) {
+        // (A wave whose columns all lie past the last has j > n.)
+        const int64_t left = m < p.R && j < F ? ((p.R - m) * n - j) * size : 0;
+        return make_rsrc(static_cast<const int8_t *>(base) + (m * n + j) * size,
+                         left < (int64_t)kOob ? (uint32_t)left : kOob);
+    };
+    u32x4 res[2][kStores];
+    auto fetch = [&](int pass) {
+        if (GATED || !e.res)
+            return;
+#pragma unroll
+        for (int k = 0; k < kStores; k++) {
+            const int m = i + pass * kRows + k * kRowsPer;
+            if (e.res_bf16) {
+                const u32x2 t = __builtin_amdgcn_raw_buffer_load_b64(rows_from(e.res, m, F, 2), at2, 0, 0);
+                res[pass % 2][k][0] = t[0];
+                res[pass % 2][k][1] = t[1];
+            } else {
+                res[pass % 2][k] = __builtin_amdgcn_raw_buffer_load_b128(rows_from(e.res, m, F, 4), at4, 0, 0);
+            }
+        }
+    };
+    fetch(0);
+    static_for<kPasses>([&](auto P) {
+        constexpr int pass = decltype(P)::value;
+#pragma unroll
+        for (int q = 0; q < kBlocks; q++) {
+            const int a = pass * kBlocks + q, row = 16 * q + r;
+            float z[FN][4];
+#pragma unroll
+            for (int b = 0; b < FN; b++)
+#pragma unroll
+                for (int t = 0; t < 4; t++) {
+                    z[b][t] = (float)acc[a][b][t] * rsv[a] * cs[b][t];
+                    if (p.bias)
+                        z[b][t] = z[b][t] + bj[b][t];
+                }
+            if (e.ck) {
+                float s[2];
+#pragma unroll
+                for (int pair = 0; pair < 2; pair++) {
+                    s[pair] = ck_max(z[2 * pair], z[2 * pair + 1]) / 127.0f;
+                    const float g[8] = {z[2 * pair][0], z[2 * pair][1], z[2 * pair][2], z[2 * pair][3],
+                                        z[2 * pair + 1][0], z[2 * pair + 1][1], z[2 * pair + 1][2],
+                                        z[2 * pair + 1][3]};
+                    i32x2 c = {0, 0};
+                    if (s[pair] >= 0x1p-126f) {
+                        c = quant8(g, s[pair], recip_refined(s[pair]));
+                    } else if (s[pair] > 0.0f) {
+                        float x[8];
+#pragma unroll
+                        for (int t = 0; t < 8; t++)
+                            x[t] = quant_code_exact(g[t], s[pair]);
+                        c = i32x2{(int)pack4(x[0], x[1], x[2], x[3]), (int)pack4(x[4], x[5], x[6], x[7])};
+                    }
+                    // Chunk b of 16 codes sits at b ^ ((row >> 2) & 3): rows 4 apart
+                    // would share their banks.
+#pragma unroll
+                    for (int t = 0; t < 2; t++)
+                        *reinterpret_cast<lds_u32 *>(codes + row * 64 + 16 * ((2 * pair + t) ^ ((row >> 2) & 3)) +
+                                                     4 * h) = (uint32_t)c[t];
+                }
+                // Lanes h = 0 and 1 store the two blocks' scales.
+                const uint32_t first = GATED ? 0 : 32 * h;
+                const uint32_t per = (uint32_t)(F + kCkBlock - 1) / kCkBlock, all = GATED ? 2 * per : per;
+                const uint32_t lane_s = r * all + (GATED ? h * per : h);
+                if (h < 2 && j + (int)first < F && i + 16 * a + r < p.R)
+                    (e.ck_s + (int64_t)(i + 16 * a) * all + j / kCkBlock)[lane_s] = h ? s[1] : s[0];
+            }
+#pragma unroll
+            for (int b = 0; b < (GATED ? 2 : 4); b++) {
+                float y[4];
+#pragma unroll
+                for (int t = 0; t < 4; t++) {
+                    y[t] = act_value<ACT>(z[b][t]);
+                    if constexpr (GATED)
+                        y[t] = y[t] * z[b + 2][t];
+                }
+                stage_put<CW>(slice, row, 4 * b + h, __float_as_uint(y[0]), __float_as_uint(y[1]),
+                              __float_as_uint(y[2]), __float_as_uint(y[3]));
+            }
+        }
+        if (pass + 1 < kPasses)
+            fetch(pass + 1);
+        wait_lgkmcnt0();
+        __builtin_amdgcn_sched_barrier(0);
+        u32x4 t[kStores];
+#pragma unroll
+        for (int k = 0; k < kStores; k++)
+            t[k] = *reinterpret_cast<lds_u32x4 *>(slice + 4 * stage_slot<CW>(k * kRowsPer + sr, sc));
+        u32x4 c[kRows / 16];
+        if (e.ck) {
+#pragma unroll
+            for (int k = 0; k < kRows / 16; k++) {
+                const int row = 16 * k + lane / 4;
+                c[k] = *reinterpret_cast<lds_u32x4 *>(codes + row * 64 + 16 * ((lane % 4) ^ ((row >> 2) & 3)));
+            }
+        }
+#pragma unroll
+        for (int k = 0; k < kStores; k++)
+            asm volatile("" : "+v"(t[k]));
+#pragma unroll
+        for (int k = 0; k < kStores; k++) {
+            float v[4];
+#pragma unroll
+            for (int x = 0; x < 4; x++)
+                v[x] = __uint_as_float(t[k][x]);
+            if (!GATED && e.res) {
+                const u32x4 u = res[pass % 2][k];
+                if (e.res_bf16) {
+                    v[0] = v[0] + bf16_lo(u[0]);
+                    v[1] = v[1] + bf16_hi(u[0]);
+                    v[2] = v[2] + bf16_lo(u[1]);
+                    v[3] = v[3] + bf16_hi(u[1]);
+                } else {
+#pragma unroll
+                    for (int x = 0; x < 4; x++)
+                        v[x] = v[x] + __uint_as_float(u[x]);
+                }
+            }
+            const int m = i + pass * kRows + k * kRowsPer;
+            if (e.y_bf16) {
+                const u32x2 o = {pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3])};
+                __builtin_amdgcn_raw_buffer_store_b64(o, rows_from(p.out, m, F, 2), at2, 0, kNonTemporal);
+            } else {
+                const u32x4 o = {__float_as_uint(v[0]), __float_as_uint(v[1]), __float_as_uint(v[2]),
+                                 __float_as_uint(v[3])};
+                __builtin_amdgcn_raw_buffer_store_b128(o, rows_from(p.out, m, F, 4), at4, 0, kNonTemporal);
+            }
+        }
+        if (e.ck) {
+            // 16 rows per store; with a gate the row's second 32 codes are the other
+            // half's.
+            const int ch = lane % 4, o = GATED ? 16 * (ch & 1) : 16 * ch;
+            const uint32_t ck_at =
+                j + o < F ? (uint32_t)(lane / 4) * (uint32_t)N + o + (GATED && ch >= 2 ? F : 0) : kOob;
+#pragma unroll
+            for (int k = 0; k < kRows / 16; k++)
+                __builtin_amdgcn_raw_buffer_store_b128(c[k], rows_from(e.ck, i + pass * kRows + 16 * k, N, 1), ck_at,
+                                                       0, 0);
+        }
+        // The next pass overwrites the slice: every read of it is back.  (The scheduler
+        // would otherwise hoist every pass's residual to the top.)
+        wait_lgkmcnt0();
+        __builtin_amdgcn_sched_barrier(0);
+    });
+}
+
 // The product kernel: 256 x 256 tiles, 8 waves of RW x CW = 128 x 64 outputs
 // in FM x FN = 8 x 4 blocks of 16 x 16, 128 contraction bytes per stage in
 // two LDS stages (two MFMA steps of 64 bytes each).  Per lane the 128 int32
@@ -799,7 +1037,8 @@ __global__ __launch_bounds__(WM *WN * 64, 1) void gemm_kernel(GemmParams p)
 {
     constexpr bool kFwd =
         EPI == EPI_FWD || EPI == EPI_FWD_ADAPTER_BF16 || EPI == EPI_FWD_ADAPTER_F32;
-    constexpr bool kAdapter = EPI >= EPI_FWD_ADAPTER_BF16;
+    constexpr bool kAdapter = EPI >= EPI_FWD_ADAPTER_BF16 && EPI < EPI_ACT;
+    constexpr bool kGated = EPI >= EPI_GATED;
     constexpr bool kHad = EPI == EPI_ROWSCALE_HAD || (kAdapter && !kFwd);
     constexpr int kQ = EPI == EPI_FWD_ADAPTER_F32 ? 0 : EPI == EPI_HAD_ADAPTER_TERMS ? 3 : 1;
     constexpr int BM = 256, BN = 256, kBK = 128;
@@ -840,7 +1079,7 @@ __global__ __launch_bounds__(WM *WN * 64, 1) void gemm_kernel(GemmParams p)
 
     const WorkUnit u = work_unit<MODE>(p, kBK);
     const int kb = u.kb, KT = u.KT;
-    const int i0 = u.ti * BM, j0 = u.tj * BN;
+    const int i0 = u.ti * BM, j0 = u.tj * (kGated ? BN / 2 : BN);
     const int lane = __lane_id();
     const int w = threadIdx.x / kWave;
     const int wi = w / WN, wj = w % WN;
@@ -848,17 +1087,24 @@ __global__ __launch_bounds__(WM *WN * 64, 1) void gemm_kernel(GemmParams p)
     if constexpr (kAdapter)
         common = AdapterTerm<kQ, FM, FN>::common(p, i0 + wi * RW);
     const int8_t *abase = AKM ? p.a + i0 : p.a + (int64_t)i0 * p.lda;
-    const int8_t *bbase = BKM ? p.b + j0 : p.b + (int64_t)j0 * p.ldb;
     const int alim = p.R - i0, blim = p.S - j0;
     // The lanes' load offsets within a stage, the same for every stage.
     const int wu = __builtin_amdgcn_readfirstlane(w);
+    // With a gate the tile's 256 columns are 128 outputs, each wave's 64 the gate's
+    // 32 and the other half's 32 of the same outputs, so that a lane holds both
+    // factors of an output.  A wave's load instruction fills 8 rows of B's tile, and
+    // instructions of one wave are 64 rows apart: half the waves load gate rows only
+    // and half the others, each from its own base.
+    static_assert(!kGated || (!BKM && NT / kWave == 8 && CW == 64), "the gate's rows by wave");
+    const int8_t *bbase =
+        BKM ? p.b + j0 : p.b + (int64_t)(j0 + (kGated && wu >= 4 ? p.act.F : 0)) * p.ldb;
     uint32_t voffA[OpA::kLoads], voffB[OpB::kLoads];
 #pragma unroll
     for (int q = 0; q < OpA::kLoads; q++)
         voffA[q] = OpA::lane_offset(q, wu, p.lda, alim);
 #pragma unroll
     for (int q = 0; q < OpB::kLoads; q++)
-        voffB[q] = OpB::lane_offset(q, wu, p.ldb, blim);
+        voffB[q] = kGated ? gated_offset<OpB>(q, wu, p.ldb, blim) : OpB::lane_offset(q, wu, p.ldb, blim);
     // LDS holds the operands' stages operand by operand: A's two stages, then
     // B's, so that a stage's offset fits the LDS reads' immediate and the
     // unrolled loop below addresses either stage with constants.
@@ -1081,6 +1327,12 @@ __global__ __launch_bounds__(WM *WN * 64, 1) void gemm_kernel(GemmParams p)
             }
             return;
         }
+    }
+
+    if constexpr (EPI >= EPI_ACT) {
+        act_epilogue<kGated, EPI % EPI_ACT, FM, FN>(p, acc, (lds_i8 *)smem + w * 16384,
+                                                    i0 + wi * RW, j0 + wj * (kGated ? CW / 2 : CW));
+        return;
     }
 
     // Output values of row block a as 32-bit patterns, in the accumulator
@@ -1317,15 +1569,24 @@ __global__ __launch_bounds__(WM *WN * 64, 1) void gemm_kernel(GemmParams p)
 // matrix; -1: none): thread t has output (t / 16, t % 16), whose R products
 // need no matrix core.  Their first 16 column values are loaded before the
 // weight is, so that both reads are in flight together.
-template <bool RAW, int CHUNK, int AD = -1>
+//
+// EPI (EPI_ACT or EPI_GATED + QLIN_ACT_*) ends in y = act(z) + residual, or the gated
+// product of the workgroup's rows 0 .. 7, the gate's, and 8 .. 15, the other half's
+// of the same eight outputs; N is then the number of outputs.
+template <int EPI> struct SkinnyExtra {
+    using type = std::conditional_t<(EPI >= EPI_ACT), ActEpilogue, AdapterEpilogue>;
+};
+
+template <bool RAW, int CHUNK, int AD = -1, int EPI = EPI_FWD>
 __global__ __launch_bounds__(256) void skinny_fwd_kernel(const int8_t *__restrict__ qx,
                                                          const float *__restrict__ sx,
                                                          const int8_t *__restrict__ qw,
                                                          const float *__restrict__ sw,
                                                          const float *__restrict__ bias, int M,
                                                          int N, int K, void *__restrict__ out,
-                                                         AdapterEpilogue ad)
+                                                         typename SkinnyExtra<EPI>::type ad)
 {
+    constexpr bool kGated = EPI >= EPI_GATED;
     constexpr int kBuf = 16 * CHUNK;            // one chunk of the 16 rows
     constexpr int kSegs = CHUNK / 1024;         // 1 KiB segments per row
     constexpr int kPer = CHUNK / 256;           // loads (and MFMA steps) per wave
@@ -1334,11 +1595,15 @@ __global__ __launch_bounds__(256) void skinny_fwd_kernel(const int8_t *__restric
     __shared__ __attribute__((aligned(1024))) int8_t smem[2 * kBuf + 4 * kWave * 16];
     const int lane = __lane_id();
     const int w = threadIdx.x / kWave;
-    const int n0 = blockIdx.x * 16;
+    const int n0 = blockIdx.x * (kGated ? 8 : 16);
     const int col = lane % 16, g = lane / 16;
     const bool xok = col < M;
     const __amdgpu_buffer_rsrc_t xr = make_rsrc(qx);
-    const __amdgpu_buffer_rsrc_t wr = make_rsrc(qw + (int64_t)n0 * K);
+    // (A wave's instructions fill four rows: waves 2 and 3 the gated half's.)
+    int64_t row0 = n0;
+    if constexpr (kGated)
+        row0 += __builtin_amdgcn_readfirstlane(w) >= 2 ? ad.F : 0;
+    const __amdgpu_buffer_rsrc_t wr = make_rsrc(qw + row0 * K);
     const int chunks = (K + CHUNK - 1) / CHUNK;
 
     // Chunk kc into buffer b: wave w's instruction p fills 1 KiB of row
@@ -1350,14 +1615,15 @@ __global__ __launch_bounds__(256) void skinny_fwd_kernel(const int8_t *__restric
             const int idx = w * kPer + p;
             const int row = idx / kSegs, slot = (idx % kSegs) * 64 + lane;
             const int k = kc * CHUNK + (slot ^ (row & 15)) * 16;
-            const uint32_t off = kc < chunks && k < K ? (uint32_t)(row * K + k) : kOob;
+            const uint32_t off =
+                kc < chunks && k < K ? (uint32_t)((kGated ? row & 7 : row) * K + k) : kOob;
             lds_i8 *dst = (lds_i8 *)smem + b * kBuf + row * CHUNK + (idx % kSegs) * 1024;
             __builtin_amdgcn_raw_ptr_buffer_load_lds(
                 wr, (__attribute__((address_space(3))) void *)dst, 16, off, 0, 0, 0);
         }
     };
 
-    const int om = threadIdx.x / 16, on = n0 + threadIdx.x % 16;
+    const int om = threadIdx.x / 16, on = n0 + threadIdx.x % (kGated ? 8 : 16);
     constexpr bool kBf = AD == X_BF16;
     Raw8<kBf> early[2];
     int id = -1;
@@ -1412,6 +1678,31 @@ __global__ __launch_bounds__(256) void skinny_fwd_kernel(const int8_t *__restric
     i32x4 *red = reinterpret_cast<i32x4 *>(smem + 2 * kBuf);
     red[w * kWave + lane] = acc;
     __syncthreads();
+    if constexpr (EPI >= EPI_ACT) {
+        if (om >= M || (kGated && threadIdx.x % 16 >= 8))
+            return;
+        auto z = [&](int c, int64_t n) {        // column c of the 16, row n of the weight
+            int32_t sum = 0;
+#pragma unroll
+            for (int i = 0; i < 4; i++)
+                sum += reinterpret_cast<const int32_t *>(red)[(i * kWave + 16 * (om / 4) + c) * 4 + om % 4];
+            const float f = (float)sum * sx[om] * sw[n];
+            return bias ? f + bias[n] : f;
+        };
+        const int c = threadIdx.x % 16;
+        const int64_t at = (int64_t)om * N + on;
+        float y = act_value<EPI % EPI_ACT>(z(c, on));
+        if constexpr (kGated)
+            y = y * z(c + 8, on + ad.F);
+        if (ad.res)
+            y = y + (ad.res_bf16 ? bf16_lo(static_cast<const uint16_t *>(ad.res)[at])
+                                 : static_cast<const float *>(ad.res)[at]);
+        if (ad.y_bf16)
+            static_cast<uint16_t *>(out)[at] = (uint16_t)pack_bf16x2(y, y);
+        else
+            static_cast<float *>(out)[at] = y;
+        return;
+    }
     if constexpr (AD >= 0) {
         if (om >= M)
             return;

@@ -83,6 +83,46 @@ struct AdapterTermArgs {
 };
 void launch_adapter_expand(const AdapterTermArgs &e, hipStream_t st);
 
+// What a forward product's outputs z become in the kernel: y = act(z) + residual
+// [M, F], or with a gate act(z[:, :F]) z[:, F:]; and the checkpoint of z, INT8
+// codes [M, N] with a scale per kCkBlock outputs of a row (of each half, the last
+// one's block may be short).  N = F, or 2 F with a gate (ProductArgs::N).
+constexpr int kCkBlock = 32;
+struct ActEpilogue {
+    int act;
+    bool gated;
+    int64_t F;
+    bool y_bf16;
+    const void *res;        // may be null
+    bool res_bf16;
+    int8_t *ck;             // may be null
+    float *ck_s;
+};
+// ProductArgs::out is y.  M of 16 and less without a checkpoint streams the weight.
+void launch_product_act(const ProductArgs &p, const ActEpilogue &e, hipStream_t st);
+
+// Backward of act and gate from the checkpoint (act_bwd.hip).
+struct ActBackward {
+    const void *dy;
+    bool dy_bf16;
+    const int8_t *ck;
+    const float *ck_s;
+    int act;
+    bool gated;
+    const float *sw, *sx;   // of the two quantizations; null with s1, s2
+    int64_t M, F;
+    void *dz;
+    bool dz_bf16;
+    float *s1, *s2, *db;    // may be null
+};
+size_t act_bwd_bytes(int64_t M, int64_t F, bool gated);
+void launch_act_bwd(const ActBackward &a, void *ws, hipStream_t st);
+
+// The codes of both quantizations of a gradient whose scales are known.
+void launch_grad_codes(const void *x, bool bf16, int64_t rows, int64_t cols, const float *sw,
+                       const float *sx, const float *s1, const float *s2, int8_t *q1, int8_t *q2,
+                       hipStream_t st);
+
 // Whether the product kernels can address every operand byte of this shape
 // with their 32-bit buffer offsets (for contractions past the int32 bound,
 // those of one chunk's launch).

@@ -712,6 +712,16 @@ void launch_quantize_grad(const void *x, bool bf16, int64_t rows, int64_t cols, 
     const unsigned gs = (unsigned)((cols + 63) / 64 + (rows + 1023) / 1024);
     hipLaunchKernelGGL(grad_scales_kernel, dim3(gs), dim3(1024), 0, st, rowpart, (int)wins,
                        colpart, (int)groups, rows, cols, s1, s2, col_sum);
+    launch_grad_codes(x, bf16, rows, cols, sw, sx, s1, s2, q1, q2, st);
+}
+
+// Also of a gradient whose scales come from elsewhere.  A bf16 dY may exceed the fp32
+// values that its scales are from by half a step, so that a quotient reaches 127 (1 +
+// 2^-8) = 127.496, which still rounds to 127.
+void launch_grad_codes(const void *x, bool bf16, int64_t rows, int64_t cols, const float *sw,
+                       const float *sx, const float *s1, const float *s2, int8_t *q1, int8_t *q2,
+                       hipStream_t st)
+{
     const dim3 g2((unsigned)((cols / 8 + 255) / 256), (unsigned)((rows + kCodeRows - 1) / kCodeRows));
     if (bf16)
         hipLaunchKernelGGL(grad_codes_kernel<true>, g2, dim3(256), 0, st, x, rows, cols, sw, sx,
