@@ -15,8 +15,8 @@ namespace {
 
 constexpr int kCols = 512;      // outputs of a wave's window: eight per lane
 constexpr int kWaves = 4;       // of a workgroup, one window, other rows
-constexpr int kBatch = 4;       // rows a lane loads before it uses any of them
-constexpr int kGroups = 1024;   // workgroups aimed at: four per compute unit
+constexpr int kBatch = 2;       // rows a lane loads before it uses any of them
+constexpr int kGroups = 4096;   // workgroups aimed at
 
 struct Args {
     ActBackward a;
@@ -26,6 +26,19 @@ struct Args {
     float *colpart;             // [2 groups, N]: maxima, then sums, of a row group
 };
 
+// Eight INT8 codes times a scale, each product rounded once: a code is taken as the
+// unsigned byte c + 128, which one instruction converts, and 128 s is taken off in a
+// fused multiply-add.
+__device__ __forceinline__ void codes_times(i32x2 q, float s, float v[8])
+{
+    const float off = s * -128.0f;
+#pragma unroll
+    for (int e = 0; e < 8; e++) {
+        const uint32_t w = (uint32_t)q[e / 4] ^ 0x80808080u;
+        v[e] = __builtin_fmaf((float)((w >> (8 * (e % 4))) & 0xFFu), s, off);
+    }
+}
+
 // dz of one row's eight outputs, the gate's (and, with a gate, the other half's in
 // d[8 ..]).
 template <int ACT, bool GATED>
@@ -33,15 +46,15 @@ __device__ __forceinline__ void dz8(const float dy[8], i32x2 cg, float sg, i32x2
                                     float *d)
 {
     float g[8], u[8];
-    codes_to_float(cg, g);
+    codes_times(cg, sg, g);
     if constexpr (GATED)
-        codes_to_float(cu, u);
+        codes_times(cu, su, u);
 #pragma unroll
     for (int e = 0; e < 8; e++) {
         float value, slope;
-        act_slope<ACT>(g[e] * sg, value, slope);
+        act_slope<ACT>(g[e], value, slope);
         if constexpr (GATED) {
-            d[e] = dy[e] * (u[e] * su) * slope;
+            d[e] = dy[e] * u[e] * slope;
             d[8 + e] = dy[e] * value;
         } else {
             d[e] = dy[e] * slope;
@@ -71,57 +84,88 @@ __global__ __launch_bounds__(256) void act_bwd_kernel(Args p)
             w[e] = 0.0f;
         mx[e] = sm[e] = 0.0f;
     }
-    const int64_t step = (int64_t)gridDim.y * kWaves * kBatch;
-    for (int64_t rb = ((int64_t)blockIdx.y * kWaves + wave) * kBatch; rb < M; rb += step) {
+    struct Rows {
         Raw8<DY_BF16> dy[kBatch];
         i32x2 q[kBatch][H];
         float s[kBatch][H], px[kBatch];
+    };
+    // Rows past the last read it again, with a dy of zeros.
+    auto load = [&](Rows &x, int64_t rb) {
 #pragma unroll
         for (int u = 0; u < kBatch; u++) {
             const int64_t r = rb + u < M ? rb + u : M - 1;
-            dy[u] = load_raw8<DY_BF16>(static_cast<const char *>(p.a.dy) + (r * F + win * kCols) * (DY_BF16 ? 2 : 4), c);
+            x.dy[u] = load_raw8<DY_BF16>(static_cast<const char *>(p.a.dy) + (r * F + win * kCols) * (DY_BF16 ? 2 : 4), c);
 #pragma unroll
             for (int h = 0; h < H; h++) {
-                q[u][h] = *reinterpret_cast<const i32x2 *>(p.a.ck + r * N + h * F + win * kCols + c);
-                s[u][h] = (p.a.ck_s + r * p.all + h * p.per + win * (kCols / kCkBlock))[c / kCkBlock];
+                x.q[u][h] = __builtin_nontemporal_load(
+                    reinterpret_cast<const i32x2 *>(p.a.ck + r * N + h * F + win * kCols + c));
+                x.s[u][h] = (p.a.ck_s + r * p.all + h * p.per + win * (kCols / kCkBlock))[c / kCkBlock];
             }
-            px[u] = p.a.sx ? p.a.sx[r] : 0.0f;
+            x.px[u] = p.a.sx ? p.a.sx[r] : 0.0f;
         }
-        float rm[kBatch];
+    };
+    auto reduce = [&](const Rows &x, int64_t rb) {
+        float d[kBatch][E], rm[kBatch];
 #pragma unroll
         for (int u = 0; u < kBatch; u++) {
-            rm[u] = 0.0f;
-            if (rb + u >= M)
-                continue;
-            float v[8], d[E];
-            unpack8<DY_BF16>(dy[u], v);
-            dz8<ACT, GATED>(v, q[u][0], s[u][0], q[u][H - 1], s[u][H - 1], d);
+            float v[8];
+            unpack8<DY_BF16>(x.dy[u], v);
 #pragma unroll
-            for (int e = 0; e < E; e++) {
-                sm[e] = sm[e] + d[e];
-                mx[e] = max_nan(mx[e], __builtin_fabsf(d[e] * px[u]));
-                rm[u] = max_nan(rm[u], __builtin_fabsf(d[e] * w[e]));
-            }
-            if (ok) {
+            for (int e = 0; e < 8; e++)
+                v[e] = rb + u < M ? v[e] : 0.0f;
+            dz8<ACT, GATED>(v, x.q[u][0], x.s[u][0], x.q[u][H - 1], x.s[u][H - 1], d[u]);
+            rm[u] = 0.0f;
+#pragma unroll
+            for (int e = 0; e < E; e++)
+                rm[u] = max_nan(rm[u], __builtin_fabsf(d[u][e] * w[e]));
+            if (ok && rb + u < M) {
 #pragma unroll
                 for (int h = 0; h < H; h++) {
                     const int64_t at = (rb + u) * N + h * F + win * kCols;
                     if constexpr (DZ_BF16)
-                        *reinterpret_cast<i32x4 *>(static_cast<uint16_t *>(p.a.dz) + at + c) = pack_bf16x8(d + 8 * h);
+                        __builtin_nontemporal_store(
+                            pack_bf16x8(d[u] + 8 * h),
+                            reinterpret_cast<i32x4 *>(static_cast<uint16_t *>(p.a.dz) + at + c));
                     else
-                        store8(static_cast<float *>(p.a.dz) + at, c, d + 8 * h);
+                        store8(static_cast<float *>(p.a.dz) + at, c, d[u] + 8 * h);
                 }
             }
         }
+        // (Two rows' maxima at a time: the instruction takes three operands.)
+#pragma unroll
+        for (int e = 0; e < E; e++)
+#pragma unroll
+            for (int u = 0; u < kBatch; u++) {
+                sm[e] = sm[e] + d[u][e];
+                mx[e] = max_nan(mx[e], __builtin_fabsf(d[u][e] * x.px[u]));
+            }
         if (p.a.sw) {
             float m = 0.0f;
 #pragma unroll
             for (int u = 0; u < kBatch; u++) {
-                const float t = wave_all(ok ? rm[u] : 0.0f, [](float a, float b) { return max_nan(a, b); });
+                const float t = wave_all(rm[u], [](float a, float b) { return max_nan(a, b); });
                 m = lane == u ? t : m;
             }
             if (lane < kBatch && rb + lane < M)
                 p.rowpart[win * M + rb + lane] = m;
+        }
+    };
+    // The next rows' loads are in flight while a batch is reduced.
+    const int64_t step = (int64_t)gridDim.y * kWaves * kBatch;
+    int64_t rb = ((int64_t)blockIdx.y * kWaves + wave) * kBatch;
+    if (rb < M) {
+        Rows one, two;
+        load(one, rb);
+        while (true) {
+            load(two, rb + step);
+            reduce(one, rb);
+            if (rb + step >= M)
+                break;
+            load(one, rb + 2 * step);
+            reduce(two, rb + step);
+            rb += 2 * step;
+            if (rb >= M)
+                break;
         }
     }
     if (wave > 0) {
@@ -149,30 +193,27 @@ __global__ __launch_bounds__(256) void act_bwd_kernel(Args p)
     }
 }
 
-// Partials -> s1, s2 and db.  The first ceil(N / 64) workgroups own 64 columns each,
-// their 16 waves every 16th row group, combined through LDS in a fixed order; the
-// workgroups after them own 1024 rows each.
+// Partials -> s1, s2 and db.  A workgroup owns 64 columns, or, past the first
+// ceil(N / 64) workgroups, 64 rows: its 16 waves take every 16th row group (window) and
+// are combined through LDS in a fixed order.
 __global__ __launch_bounds__(1024) void act_bwd_scales_kernel(const float *__restrict__ rowpart, int wins,
                                                               const float *__restrict__ colpart, int groups,
                                                               int64_t M, int64_t N, float *__restrict__ s1,
                                                               float *__restrict__ s2, float *__restrict__ db)
 {
-    const int64_t cblocks = (N + 63) / 64;
-    if ((int64_t)blockIdx.x >= cblocks) {
-        const int64_t r = ((int64_t)blockIdx.x - cblocks) * 1024 + threadIdx.x;
-        if (r < M) {
-            float m = 0.0f;
-            for (int k = 0; k < wins; k++)
-                m = max_nan(m, rowpart[k * M + r]);
-            s1[r] = m / 127.0f;
-        }
-        return;
-    }
     __shared__ float red_max[16][64], red_sum[16][64];
+    const int64_t cblocks = (N + 63) / 64;
+    const bool rows = (int64_t)blockIdx.x >= cblocks;
     const int lc = threadIdx.x % 64, sl = threadIdx.x / 64;
-    const int64_t c = (int64_t)blockIdx.x * 64 + lc;
+    const int64_t c = ((int64_t)blockIdx.x - (rows ? cblocks : 0)) * 64 + lc;
     float m = 0.0f, sum = 0.0f;
-    if (c < N) {
+    if (rows) {
+        if (c < M) {
+#pragma unroll 4
+            for (int k = sl; k < wins; k += 16)
+                m = max_nan(m, rowpart[k * M + c]);
+        }
+    } else if (c < N) {
 #pragma unroll 4
         for (int g = sl; g < groups; g += 16) {
             m = max_nan(m, colpart[(2 * (int64_t)g) * N + c]);
@@ -182,12 +223,16 @@ __global__ __launch_bounds__(1024) void act_bwd_scales_kernel(const float *__res
     red_max[sl][lc] = m;
     red_sum[sl][lc] = sum;
     __syncthreads();
-    if (sl == 0 && c < N) {
+    if (sl != 0 || c >= (rows ? M : N))
+        return;
 #pragma unroll
-        for (int i = 1; i < 16; i++) {
-            m = max_nan(m, red_max[i][lc]);
-            sum = sum + red_sum[i][lc];
-        }
+    for (int i = 1; i < 16; i++) {
+        m = max_nan(m, red_max[i][lc]);
+        sum = sum + red_sum[i][lc];
+    }
+    if (rows) {
+        s1[c] = m / 127.0f;
+    } else {
         if (s2)
             s2[c] = m / 127.0f;
         if (db)
@@ -195,15 +240,18 @@ __global__ __launch_bounds__(1024) void act_bwd_scales_kernel(const float *__res
     }
 }
 
-// Windows of a row and row groups: about kGroups workgroups, at most one per
-// kWaves * kBatch rows.
+// Windows of a row and row groups: about kGroups workgroups, of at least 32 rows (the
+// partials of a group are 8 bytes per column, written and read), or if that leaves
+// fewer than two workgroups per compute unit, of at least one batch per wave.
 struct Shape {
     int64_t wins, groups;
 };
 Shape shape_of(int64_t M, int64_t F)
 {
     const int64_t wins = (F + kCols - 1) / kCols, most = (M + kWaves * kBatch - 1) / (kWaves * kBatch);
-    const int64_t groups = (kGroups + wins - 1) / wins;
+    const int64_t few = (512 + wins - 1) / wins, all = (kGroups + wins - 1) / wins;
+    int64_t groups = M / 32 > few ? M / 32 : few;
+    groups = groups < all ? groups : all;
     return {wins, groups < most ? groups : most};
 }
 
@@ -250,7 +298,7 @@ void launch_act_bwd(const ActBackward &a, void *ws, hipStream_t st)
         }
     }
     // (s1 and its workgroups only where it is asked for.)
-    const unsigned blocks = (unsigned)((p.N + 63) / 64 + (a.s1 ? (a.M + 1023) / 1024 : 0));
+    const unsigned blocks = (unsigned)((p.N + 63) / 64 + (a.s1 ? (a.M + 63) / 64 : 0));
     if (a.s1 || a.s2 || a.db)
         hipLaunchKernelGGL(act_bwd_scales_kernel, dim3(blocks), dim3(1024), 0, st, p.rowpart, (int)sh.wins,
                            p.colpart, (int)sh.groups, a.M, p.N, a.s1, a.s2, a.db);
