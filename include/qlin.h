@@ -615,7 +615,7 @@ enum {
     QLIN_ACT_GELU_TANH = 4
 };
 #define QLIN_CK_BLOCK 32                /* outputs that share a checkpoint's scale */
-#define QLIN_MAX_BLOCK_ROWS 67108864    /* weight rows of the calls below */
+#define QLIN_MAX_BLOCK_ROWS 2097152     /* weight rows of the calls below */
 
 /*
  * Forward product of a feed-forward block with its activation:

@@ -27,7 +27,7 @@ NOTHING = dict(qx=None, sx=None, sw=None, y=None, ck=None, ck_s=None, ws=None, w
     (dict(ck=A[6]), 1), (dict(y=A[4]), 1),
     (dict(residual=A[6], res_dtype=0), 1),          # y itself, but of another type
     (dict(residual=A[6] + 64), 1), (dict(ck=A[5]), 1),
-    (dict(K=131088), 2), (dict(N=67108880), 2), (dict(N=1 << 40), 2), (dict(M=(1 << 30) + 1), 2),
+    (dict(K=131088), 2), (dict(N=2097168), 2), (dict(N=1 << 40), 2), (dict(M=(1 << 30) + 1), 2),
     (dict(residual=None, res_dtype=9, **NOTHING), 0), (dict(bias=None, residual=None, **NOTHING), 0),
 ])
 def test_act_refusals(L, kw, expect):        # noqa: F811
@@ -47,7 +47,7 @@ def _gated(**kw):
     (dict(K=40), 1), (dict(M=-3), 1), (dict(y_dtype=-1), 1), (dict(y=A[1]), 1), (dict(ck=None), 1),
     (dict(y=A[2] + 64 * 64), 1),                    # over the second half's rows
     (dict(ck_s=A[7] + 20 * 64), 1),                 # over the second half's codes
-    (dict(F=33554448), 2), (dict(F=1 << 61), 2), (dict(F=(1 << 63) - 16), 2), (dict(K=131088), 2),
+    (dict(F=1048592), 2), (dict(F=1 << 61), 2), (dict(F=(1 << 63) - 16), 2), (dict(K=131088), 2),
     (NOTHING, 0),
 ])
 def test_gated_refusals(L, kw, expect):      # noqa: F811
@@ -83,7 +83,7 @@ def _bwd(**kw):
     (dict(dz_dtype=5), 1), (dict(ws=None), 1), (dict(ws_bytes=64), 1), (dict(ws=ODD), 1),
     (dict(dz=A[0]), 1), (dict(dz=A[1]), 1), (dict(s1=A[4]), 1), (dict(s2=A[8]), 1), (dict(ws=A[5] + 256), 1),
     (dict(db=A[2]), 1), (dict(dz=A[1] - 16 * 16), 1),
-    (dict(F=33554448), 2), (dict(F=67108880, gated=0), 2), (dict(M=(1 << 30) + 1), 2), (dict(F=1 << 62), 2),
+    (dict(F=1048592), 2), (dict(F=2097168, gated=0), 2), (dict(M=(1 << 30) + 1), 2), (dict(F=1 << 62), 2),
 ])
 def test_act_bwd_refusals(L, kw, expect):    # noqa: F811
     _cpu_only()
@@ -94,7 +94,7 @@ def test_act_bwd_workspace_sizes(L):         # noqa: F811
     assert L.qlin_act_bwd_ws_bytes(0, 64, 0) == 0
     # A row maximum per token and window, two values per column and row group.
     assert L.qlin_act_bwd_ws_bytes(20, 64, 1) >= 4 * (20 + 2 * 128)
-    for bad in ((-1, 64, 0), (4, 24, 0), (4, 33554448, 1), (1 << 40, 64, 0), (4, -16, 1)):
+    for bad in ((-1, 64, 0), (4, 24, 0), (4, 1048592, 1), (1 << 40, 64, 0), (4, -16, 1)):
         assert L.qlin_act_bwd_ws_bytes(*bad) == 0
 
 

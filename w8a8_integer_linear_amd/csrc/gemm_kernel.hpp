@@ -798,20 +798,38 @@ __device__ __forceinline__ uint32_t gated_offset(int q, int w, int64_t ld, int l
     return out < lim ? (uint32_t)((int64_t)out * ld + gk) : kOob;
 }
 
-// Maximum of |v| over a lane's two blocks of four and over the four lanes that hold
-// the rest of the row's 32 outputs; NaN if any is.
-__device__ __forceinline__ float ck_max(const float (&x)[4], const float (&y)[4])
+// fl(a / 127): with r = fl(1 / 127) and q = fl(a r), the remainder a - 127 q is exact
+// and fl(q + remainder r) is the correctly rounded quotient (Markstein); three
+// instructions against ten.
+__device__ __forceinline__ float over_127(float a)
+{
+    constexpr float r = 1.0f / 127.0f;
+    const float q = a * r;
+    return __builtin_fmaf(__builtin_fmaf(-127.0f, q, a), r, q);
+}
+
+// One row's eight outputs of a checkpoint block that four neighbouring lanes hold: the
+// block's scale and the lane's codes.  The maximum is NaN if any value is.
+__device__ __forceinline__ i32x2 ck_codes(const float z[8], float &s)
 {
     float m = 0.0f;
 #pragma unroll
-    for (int e = 0; e < 4; e++)
-        m = max_nan(max_nan(m, __builtin_fabsf(x[e])), __builtin_fabsf(y[e]));
-    const uint32_t u = __float_as_uint(m);
-    const auto s16 = __builtin_amdgcn_permlane16_swap(u, u, false, false);
-    m = max_nan(__uint_as_float(s16[0]), __uint_as_float(s16[1]));
-    const uint32_t v = __float_as_uint(m);
-    const auto s32 = __builtin_amdgcn_permlane32_swap(v, v, false, false);
-    return max_nan(__uint_as_float(s32[0]), __uint_as_float(s32[1]));
+    for (int e = 0; e < 8; e++)
+        m = max_nan(m, __builtin_fabsf(z[e]));
+    m = max_nan(m, dpp_mov<0xB1>(m));       // lane ^ 1
+    m = max_nan(m, dpp_mov<0x4E>(m));       // lane ^ 2
+    s = over_127(m);
+    if (s >= 0x1p-126f)
+        return quant8(z, s, recip_refined(s));
+    i32x2 c = {0, 0};
+    if (s > 0.0f) {
+        float x[8];
+#pragma unroll
+        for (int e = 0; e < 8; e++)
+            x[e] = quant_code_exact(z[e], s);
+        c = i32x2{(int)pack4(x[0], x[1], x[2], x[3]), (int)pack4(x[4], x[5], x[6], x[7])};
+    }
+    return c;
 }
 
 // Epilogue of a forward product in a feed-forward block: z = dequantized sums plus
@@ -819,198 +837,192 @@ __device__ __forceinline__ float ck_max(const float (&x)[4], const float (&y)[4]
 // fl(max / 127) per 32 outputs; y = act(z) + residual, or act(z) times the other
 // half's z.
 //
-// The wave's 128 rows go in passes through its 16 KiB of the idle stage buffers, so
-// that global accesses are runs of whole rows: y as fp32 in the first 8 KiB, the
-// codes in the next 4 (64 bytes per row: its outputs', with a gate 32 of each
-// half).  The residual is loaded in the order y is stored in, a pass ahead of its
-// use and before the previous pass's stores (a load's wait also waits for the stores
-// issued before it).
+// The wave's 128 x 64 sums pass through its 16 KiB of the idle stage buffers, 64 rows
+// at a time, and come back eight outputs of a row per lane: four lanes hold a
+// checkpoint's block, stores are 16 bytes per lane, and the arithmetic is a loop of a
+// few hundred instructions.  (In the accumulators' layout it has to be unrolled over
+// all 128 registers, more code than the instruction cache holds: 4000 x 4096 -> 14336
+// with GELU and checkpoint 286 us, this way 258.)  With a gate a row is 32 outputs:
+// a lane reads the gate's eight sums and the other half's.
 template <bool GATED, int ACT, int FM, int FN>
 __device__ __forceinline__ void act_epilogue(const GemmParams &p, const i32x4 (&acc)[FM][FN],
                                              lds_i8 *slice, int i, int j)
 {
-    typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
-    typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
-    typedef __attribute__((address_space(3))) u32x4 lds_u32x4;
-    typedef __attribute__((address_space(3))) uint32_t lds_u32;
-    static_assert(FN == 4, "64 columns of the product per wave");
+    typedef __attribute__((address_space(3))) i32x4 lds_i32x4;
+    static_assert(FN == 4 && FM == 8, "a wave's 128 x 64 sums");
     constexpr int CW = GATED ? 32 : 64;             // outputs per wave and row
-    constexpr int kBlocks = GATED ? 4 : 1;          // row blocks per pass: 8 or 4 KiB of y
-    constexpr int kRows = 16 * kBlocks, kPasses = FM / kBlocks;
-    constexpr int kChunks = CW / 4;                 // 4 outputs each
-    constexpr int kRowsPer = kWave / kChunks, kStores = kRows / kRowsPer;
-    lds_i8 *codes = slice + 8192;
+    constexpr int kLanes = CW / 8;                  // lanes per row
+    constexpr int kRows = kWave / kLanes;           // rows per step
+    constexpr int H = GATED ? 2 : 1;
     i = __builtin_amdgcn_readfirstlane(i);
     j = __builtin_amdgcn_readfirstlane(j);
     const ActEpilogue &e = p.act;
-    const int lane = __lane_id(), r = lane % 16, h = lane / 16;
-    const int F = p.S;
-    const int64_t N = GATED ? 2 * (int64_t)F : F;
-    // The lane's columns: output 16 (b % (FN / halves)) + 4 h + 0 .. 3 of the wave's.
-    f32x4 cs[FN], bj[FN];
+    const int lane = __lane_id(), F = p.S;
+    // The lane's row within a step and its first output within the wave's.  With a
+    // gate, 16 lanes read four rows' sums at a time, whose chunks (below) fall on
+    // distinct banks for rows a, a + 1, a + 8, a + 9.
+    const int sub = lane / kLanes;
+    const int row0 = GATED ? 2 * (sub / 4) + (sub & 1) + 8 * ((sub >> 1) & 1) : sub;
+    const int col = 8 * (lane % kLanes);
+    const bool ok = j + col < F;                    // then all eight are
+    f32x4 cs[2 * H], bj[2 * H];
 #pragma unroll
-    for (int b = 0; b < FN; b++) {
-        const int o = j + 16 * (GATED ? b & 1 : b) + 4 * h;
-        const int64_t n = o + (GATED && b >= 2 ? (int64_t)F : 0);
-        const bool ok = o < F;
-        cs[b] = ok ? *reinterpret_cast<const f32x4 *>(p.scol + n) : f32x4{0, 0, 0, 0};
-        bj[b] = ok && p.bias ? *reinterpret_cast<const f32x4 *>(p.bias + n) : f32x4{0, 0, 0, 0};
+    for (int t = 0; t < 2 * H; t++) {
+        const int64_t n = j + col + 4 * (t & 1) + (t >= 2 ? (int64_t)F : 0);
+        cs[t] = ok ? *reinterpret_cast<const f32x4 *>(p.scol + n) : f32x4{0, 0, 0, 0};
+        bj[t] = ok && p.bias ? *reinterpret_cast<const f32x4 *>(p.bias + n) : f32x4{0, 0, 0, 0};
     }
-    float rsv[FM];
-#pragma unroll
-    for (int a = 0; a < FM; a++)
-        rsv[a] = i + 16 * a + r < p.R ? p.srow[i + 16 * a + r] : 0.0f;
-    // Access k of a pass: row k kRowsPer + sr, outputs 4 sc .. + 3 of the wave's.  Each
-    // goes through a buffer resource from its first row, whose extent drops rows past
-    // the last; the lanes' offsets, kOob past the last column, stay below that by
-    // QLIN_MAX_BLOCK_ROWS.
-    const int sr = lane / kChunks, sc = lane % kChunks;
-    const uint32_t lane_at = (uint32_t)sr * (uint32_t)F + 4 * sc;
-    const uint32_t at2 = j + 4 * sc < F ? lane_at * 2 : kOob, at4 = j + 4 * sc < F ? lane_at * 4 : kOob;
-    // Rows from m of an array whose rows hold n elements of size bytes, from column j.
-    auto rows_from = [&](const void *base, int m, int64_t n, int size) {
-        // (A wave whose columns all lie past the last has j > n.)
-        const int64_t left = m < p.R && j < F ? ((p.R - m) * n - j) * size : 0;
-        return make_rsrc(static_cast<const int8_t *>(base) + (m * n + j) * size,
-                         left < (int64_t)kOob ? (uint32_t)left : kOob);
+    // Every array is accessed through a buffer resource over the wave's rows, whose
+    // extent (below 2^30 bytes by QLIN_MAX_BLOCK_ROWS) drops rows past the last; the
+    // lanes' offsets, kOob past the last column, move on by a constant per step, below
+    // 2^30 in all, and hold all of an access's offset.
+    const int rows = p.R - i < 128 ? p.R - i : 128;
+    // An array whose rows hold n elements of size bytes, from element c.  (A wave whose
+    // rows or columns all lie past the last has rows <= 0 or j >= F.)
+    auto rows_of = [&](const void *base, uint32_t n, uint32_t c, int size) {
+        return make_rsrc(static_cast<const int8_t *>(base) + ((int64_t)i * n + c) * size,
+                         rows > 0 && j < F ? ((uint32_t)rows * n - c) * size : 0);
     };
-    u32x4 res[2][kStores];
-    auto fetch = [&](int pass) {
+    const uint32_t n = H * (uint32_t)F, per = (uint32_t)(F + kCkBlock - 1) / kCkBlock, all = H * per;
+    const int y_size = e.y_bf16 ? 2 : 4, r_size = e.res_bf16 ? 2 : 4;
+    const __amdgpu_buffer_rsrc_t ry = rows_of(p.out, F, j, y_size);
+    const __amdgpu_buffer_rsrc_t rr = rows_of(e.res, F, j, r_size);
+    const __amdgpu_buffer_rsrc_t rc = rows_of(e.ck, n, j, 1), rs = rows_of(e.ck_s, all, j / kCkBlock, 4);
+    const uint32_t rowstep = kRows * (uint32_t)F;
+    uint32_t c_at = ok ? (uint32_t)row0 * n + col : kOob;
+    uint32_t s_at = ok && lane % 4 == 0 ? (row0 * all + col / kCkBlock) * 4 : kOob;
+    // y and the residual: a bf16 y's eight outputs together; of an fp32 y, outputs 4 l
+    // .. and 4 (l + kLanes) .. for lane l of the row, so that each store writes a
+    // contiguous run of the row (32 bytes per lane in two stores, half of every line
+    // each: 12000 x 5376 -> 7168 412 us, so 375); the eight values change lanes through
+    // the row's place in LDS, where its sums have been read.
+    const bool wide = !e.y_bf16;
+    const int o0 = wide ? 4 * (lane % kLanes) : col, o1 = wide ? o0 + 4 * kLanes : col + 4;
+    const uint32_t at0 = (uint32_t)row0 * (uint32_t)F + o0, at1 = (uint32_t)row0 * (uint32_t)F + o1;
+    const bool ok0 = j + o0 < F, ok1 = j + o1 < F;
+    uint32_t y_at0 = ok0 ? at0 * y_size : kOob, y_at1 = ok1 ? at1 * y_size : kOob;
+    uint32_t r_at0 = ok0 ? at0 * r_size : kOob, r_at1 = ok1 ? at1 * r_size : kOob;
+    // The residual of a step, loaded kAhead steps before its use (a load's wait also
+    // waits for the stores issued before it, which are as many steps old by then).
+    struct Res {
+        i32x4 lo, hi;           // of a bf16 residual, the first two words of each
+    };
+    auto fetch = [&](Res &r) {
         if (GATED || !e.res)
             return;
-#pragma unroll
-        for (int k = 0; k < kStores; k++) {
-            const int m = i + pass * kRows + k * kRowsPer;
-            if (e.res_bf16) {
-                const u32x2 t = __builtin_amdgcn_raw_buffer_load_b64(rows_from(e.res, m, F, 2), at2, 0, 0);
-                res[pass % 2][k][0] = t[0];
-                res[pass % 2][k][1] = t[1];
-            } else {
-                res[pass % 2][k] = __builtin_amdgcn_raw_buffer_load_b128(rows_from(e.res, m, F, 4), at4, 0, 0);
-            }
+        if (e.res_bf16) {
+            const i32x2 lo = __builtin_amdgcn_raw_buffer_load_b64(rr, r_at0, 0, kNonTemporal);
+            const i32x2 hi = __builtin_amdgcn_raw_buffer_load_b64(rr, r_at1, 0, kNonTemporal);
+            r.lo = i32x4{lo[0], lo[1], 0, 0};
+            r.hi = i32x4{hi[0], hi[1], 0, 0};
+        } else {
+            r.lo = __builtin_amdgcn_raw_buffer_load_b128(rr, r_at0, 0, kNonTemporal);
+            r.hi = __builtin_amdgcn_raw_buffer_load_b128(rr, r_at1, 0, kNonTemporal);
         }
+        r_at0 += rowstep * r_size;
+        r_at1 += rowstep * r_size;
     };
-    fetch(0);
-    static_for<kPasses>([&](auto P) {
-        constexpr int pass = decltype(P)::value;
+    float scale = 0.0f;         // of row `lane` of the 64
+    auto one_step = [&](int step, const Res &res) {
+        const int row = step * kRows + row0;
+        float z[8 * H];
+        const float row_scale = __shfl(scale, row);
 #pragma unroll
-        for (int q = 0; q < kBlocks; q++) {
-            const int a = pass * kBlocks + q, row = 16 * q + r;
-            float z[FN][4];
-#pragma unroll
-            for (int b = 0; b < FN; b++)
-#pragma unroll
-                for (int t = 0; t < 4; t++) {
-                    z[b][t] = (float)acc[a][b][t] * rsv[a] * cs[b][t];
-                    if (p.bias)
-                        z[b][t] = z[b][t] + bj[b][t];
-                }
-            if (e.ck) {
-                float s[2];
-#pragma unroll
-                for (int pair = 0; pair < 2; pair++) {
-                    s[pair] = ck_max(z[2 * pair], z[2 * pair + 1]) / 127.0f;
-                    const float g[8] = {z[2 * pair][0], z[2 * pair][1], z[2 * pair][2], z[2 * pair][3],
-                                        z[2 * pair + 1][0], z[2 * pair + 1][1], z[2 * pair + 1][2],
-                                        z[2 * pair + 1][3]};
-                    i32x2 c = {0, 0};
-                    if (s[pair] >= 0x1p-126f) {
-                        c = quant8(g, s[pair], recip_refined(s[pair]));
-                    } else if (s[pair] > 0.0f) {
-                        float x[8];
-#pragma unroll
-                        for (int t = 0; t < 8; t++)
-                            x[t] = quant_code_exact(g[t], s[pair]);
-                        c = i32x2{(int)pack4(x[0], x[1], x[2], x[3]), (int)pack4(x[4], x[5], x[6], x[7])};
-                    }
-                    // Chunk b of 16 codes sits at b ^ ((row >> 2) & 3): rows 4 apart
-                    // would share their banks.
-#pragma unroll
-                    for (int t = 0; t < 2; t++)
-                        *reinterpret_cast<lds_u32 *>(codes + row * 64 + 16 * ((2 * pair + t) ^ ((row >> 2) & 3)) +
-                                                     4 * h) = (uint32_t)c[t];
-                }
-                // Lanes h = 0 and 1 store the two blocks' scales.
-                const uint32_t first = GATED ? 0 : 32 * h;
-                const uint32_t per = (uint32_t)(F + kCkBlock - 1) / kCkBlock, all = GATED ? 2 * per : per;
-                const uint32_t lane_s = r * all + (GATED ? h * per : h);
-                if (h < 2 && j + (int)first < F && i + 16 * a + r < p.R)
-                    (e.ck_s + (int64_t)(i + 16 * a) * all + j / kCkBlock)[lane_s] = h ? s[1] : s[0];
-            }
-#pragma unroll
-            for (int b = 0; b < (GATED ? 2 : 4); b++) {
-                float y[4];
-#pragma unroll
-                for (int t = 0; t < 4; t++) {
-                    y[t] = act_value<ACT>(z[b][t]);
-                    if constexpr (GATED)
-                        y[t] = y[t] * z[b + 2][t];
-                }
-                stage_put<CW>(slice, row, 4 * b + h, __float_as_uint(y[0]), __float_as_uint(y[1]),
-                              __float_as_uint(y[2]), __float_as_uint(y[3]));
-            }
-        }
-        if (pass + 1 < kPasses)
-            fetch(pass + 1);
-        wait_lgkmcnt0();
-        __builtin_amdgcn_sched_barrier(0);
-        u32x4 t[kStores];
-#pragma unroll
-        for (int k = 0; k < kStores; k++)
-            t[k] = *reinterpret_cast<lds_u32x4 *>(slice + 4 * stage_slot<CW>(k * kRowsPer + sr, sc));
-        u32x4 c[kRows / 16];
-        if (e.ck) {
-#pragma unroll
-            for (int k = 0; k < kRows / 16; k++) {
-                const int row = 16 * k + lane / 4;
-                c[k] = *reinterpret_cast<lds_u32x4 *>(codes + row * 64 + 16 * ((lane % 4) ^ ((row >> 2) & 3)));
-            }
-        }
-#pragma unroll
-        for (int k = 0; k < kStores; k++)
-            asm volatile("" : "+v"(t[k]));
-#pragma unroll
-        for (int k = 0; k < kStores; k++) {
-            float v[4];
+        for (int t = 0; t < 2 * H; t++) {
+            const int chunk = col / 4 + (t & 1) + (t >= 2 ? 8 : 0);
+            const i32x4 v = *reinterpret_cast<lds_i32x4 *>(slice + row * 256 + 16 * (chunk ^ (row & 15)));
 #pragma unroll
             for (int x = 0; x < 4; x++)
-                v[x] = __uint_as_float(t[k][x]);
-            if (!GATED && e.res) {
-                const u32x4 u = res[pass % 2][k];
-                if (e.res_bf16) {
-                    v[0] = v[0] + bf16_lo(u[0]);
-                    v[1] = v[1] + bf16_hi(u[0]);
-                    v[2] = v[2] + bf16_lo(u[1]);
-                    v[3] = v[3] + bf16_hi(u[1]);
-                } else {
+                z[4 * t + x] = (float)v[x] * row_scale * cs[t][x];
+        }
+        if (p.bias) {
 #pragma unroll
-                    for (int x = 0; x < 4; x++)
-                        v[x] = v[x] + __uint_as_float(u[x]);
-                }
-            }
-            const int m = i + pass * kRows + k * kRowsPer;
-            if (e.y_bf16) {
-                const u32x2 o = {pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3])};
-                __builtin_amdgcn_raw_buffer_store_b64(o, rows_from(p.out, m, F, 2), at2, 0, kNonTemporal);
-            } else {
-                const u32x4 o = {__float_as_uint(v[0]), __float_as_uint(v[1]), __float_as_uint(v[2]),
-                                 __float_as_uint(v[3])};
-                __builtin_amdgcn_raw_buffer_store_b128(o, rows_from(p.out, m, F, 4), at4, 0, kNonTemporal);
-            }
+            for (int t = 0; t < 8 * H; t++)
+                z[t] = z[t] + bj[t / 4][t % 4];
         }
         if (e.ck) {
-            // 16 rows per store; with a gate the row's second 32 codes are the other
-            // half's.
-            const int ch = lane % 4, o = GATED ? 16 * (ch & 1) : 16 * ch;
-            const uint32_t ck_at =
-                j + o < F ? (uint32_t)(lane / 4) * (uint32_t)N + o + (GATED && ch >= 2 ? F : 0) : kOob;
 #pragma unroll
-            for (int k = 0; k < kRows / 16; k++)
-                __builtin_amdgcn_raw_buffer_store_b128(c[k], rows_from(e.ck, i + pass * kRows + 16 * k, N, 1), ck_at,
-                                                       0, 0);
+            for (int h = 0; h < H; h++) {
+                float s;
+                const i32x2 c = ck_codes(z + 8 * h, s);
+                __builtin_amdgcn_raw_buffer_store_b64(c, rc, c_at + h * F, 0, 0);
+                __builtin_amdgcn_raw_buffer_store_b32(__float_as_int(s), rs, s_at + h * per * 4, 0, 0);
+            }
+            c_at += kRows * n;
+            s_at += kRows * all * 4;
         }
-        // The next pass overwrites the slice: every read of it is back.  (The scheduler
-        // would otherwise hoist every pass's residual to the top.)
+        float y[8];
+#pragma unroll
+        for (int t = 0; t < 8; t++) {
+            y[t] = act_value<ACT>(z[t]);
+            if constexpr (GATED)
+                y[t] = y[t] * z[8 + t];
+        }
+        if (wide) {
+#pragma unroll
+            for (int t = 0; t < 2; t++) {
+                const f32x4 v = {y[4 * t], y[4 * t + 1], y[4 * t + 2], y[4 * t + 3]};
+                *reinterpret_cast<lds_i32x4 *>(slice + row * 256 + 16 * ((col / 4 + t) ^ (row & 15))) =
+                    __builtin_bit_cast(i32x4, v);
+            }
+            wait_lgkmcnt0();
+#pragma unroll
+            for (int t = 0; t < 2; t++) {
+                const f32x4 v = __builtin_bit_cast(
+                    f32x4, *reinterpret_cast<lds_i32x4 *>(
+                               slice + row * 256 + 16 * ((lane % kLanes + t * kLanes) ^ (row & 15))));
+#pragma unroll
+                for (int x = 0; x < 4; x++)
+                    y[4 * t + x] = v[x];
+            }
+        }
+        if (!GATED && e.res) {
+#pragma unroll
+            for (int t = 0; t < 8; t++) {
+                const i32x4 &r = t < 4 ? res.lo : res.hi;
+                const uint32_t half = (uint32_t)r[t % 4 / 2];
+                y[t] = y[t] + (e.res_bf16 ? (t & 1 ? bf16_hi(half) : bf16_lo(half)) : __int_as_float(r[t % 4]));
+            }
+        }
+        if (wide) {
+            const f32x4 lo = {y[0], y[1], y[2], y[3]}, hi = {y[4], y[5], y[6], y[7]};
+            __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(i32x4, lo), ry, y_at0, 0, kNonTemporal);
+            __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(i32x4, hi), ry, y_at1, 0, kNonTemporal);
+        } else {
+            __builtin_amdgcn_raw_buffer_store_b128(pack_bf16x8(y), ry, y_at0, 0, kNonTemporal);
+        }
+        y_at0 += rowstep * y_size;
+        y_at1 += rowstep * y_size;
+    };
+    constexpr int kAhead = 3;
+    static_assert((64 / kRows) % (kAhead + 1) == 0, "ring of residuals");
+    Res ring[kAhead + 1] = {};
+#pragma unroll
+    for (int k = 0; k < kAhead; k++)
+        fetch(ring[k]);
+    static_for<2>([&](auto Half) {
+        constexpr int half = decltype(Half)::value;
+        // Row r, 16-byte chunk c (four columns of the product) at chunk c ^ (r & 15):
+        // the 16 rows that a store writes together fall on distinct banks.
+#pragma unroll
+        for (int a = 0; a < 4; a++)
+#pragma unroll
+            for (int b = 0; b < FN; b++) {
+                const int row = 16 * a + lane % 16, chunk = 4 * b + lane / 16;
+                *reinterpret_cast<lds_i32x4 *>(slice + row * 256 + 16 * (chunk ^ (row & 15))) =
+                    acc[4 * half + a][b];
+            }
+        const int mine = i + 64 * half + lane;
+        scale = mine < p.R ? p.srow[mine] : 0.0f;
+        wait_lgkmcnt0();
+#pragma unroll 1
+        for (int step = 0; step < 64 / kRows; step += kAhead + 1)
+            static_for<kAhead + 1>([&](auto K) {
+                constexpr int k = decltype(K)::value;
+                fetch(ring[(k + kAhead) % (kAhead + 1)]);   // (past the wave's rows: zeros)
+                one_step(step + k, ring[k]);
+            });
+        // (The second half's sums go over the first's: every read of them is back.)
         wait_lgkmcnt0();
         __builtin_amdgcn_sched_barrier(0);
     });
