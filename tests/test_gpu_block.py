@@ -50,7 +50,8 @@ def _guarded(torch, shape, dtype):
     return out, whole
 
 
-SHAPES = [(1, 16, 16), (1, 4096, 256), (3, 48, 80), (16, 272, 4096), (16, 32, 1040), (17, 16, 16),
+SHAPES = [(1, 16, 16), (1, 4096, 256), (3, 48, 80), (16, 272, 4096), (16, 32, 1040), (5, 48, 2064), (9, 6416, 528),
+          (12, 6432, 1040), (4, 4096, 3088), (8, 4112, 1008), (17, 16, 16),
           (33, 144, 1168), (255, 528, 64), (257, 1040, 192), (300, 2064, 400), (1000, 784, 256)]
 
 

@@ -1581,24 +1581,15 @@ __global__ __launch_bounds__(WM *WN * 64, 1) void gemm_kernel(GemmParams p)
 // matrix; -1: none): thread t has output (t / 16, t % 16), whose R products
 // need no matrix core.  Their first 16 column values are loaded before the
 // weight is, so that both reads are in flight together.
-//
-// EPI (EPI_ACT or EPI_GATED + QLIN_ACT_*) ends in y = act(z) + residual, or the gated
-// product of the workgroup's rows 0 .. 7, the gate's, and 8 .. 15, the other half's
-// of the same eight outputs; N is then the number of outputs.
-template <int EPI> struct SkinnyExtra {
-    using type = std::conditional_t<(EPI >= EPI_ACT), ActEpilogue, AdapterEpilogue>;
-};
-
-template <bool RAW, int CHUNK, int AD = -1, int EPI = EPI_FWD>
+template <bool RAW, int CHUNK, int AD = -1>
 __global__ __launch_bounds__(256) void skinny_fwd_kernel(const int8_t *__restrict__ qx,
                                                          const float *__restrict__ sx,
                                                          const int8_t *__restrict__ qw,
                                                          const float *__restrict__ sw,
                                                          const float *__restrict__ bias, int M,
                                                          int N, int K, void *__restrict__ out,
-                                                         typename SkinnyExtra<EPI>::type ad)
+                                                         AdapterEpilogue ad)
 {
-    constexpr bool kGated = EPI >= EPI_GATED;
     constexpr int kBuf = 16 * CHUNK;            // one chunk of the 16 rows
     constexpr int kSegs = CHUNK / 1024;         // 1 KiB segments per row
     constexpr int kPer = CHUNK / 256;           // loads (and MFMA steps) per wave
@@ -1607,15 +1598,11 @@ __global__ __launch_bounds__(256) void skinny_fwd_kernel(const int8_t *__restric
     __shared__ __attribute__((aligned(1024))) int8_t smem[2 * kBuf + 4 * kWave * 16];
     const int lane = __lane_id();
     const int w = threadIdx.x / kWave;
-    const int n0 = blockIdx.x * (kGated ? 8 : 16);
+    const int n0 = blockIdx.x * 16;
     const int col = lane % 16, g = lane / 16;
     const bool xok = col < M;
     const __amdgpu_buffer_rsrc_t xr = make_rsrc(qx);
-    // (A wave's instructions fill four rows: waves 2 and 3 the gated half's.)
-    int64_t row0 = n0;
-    if constexpr (kGated)
-        row0 += __builtin_amdgcn_readfirstlane(w) >= 2 ? ad.F : 0;
-    const __amdgpu_buffer_rsrc_t wr = make_rsrc(qw + row0 * K);
+    const __amdgpu_buffer_rsrc_t wr = make_rsrc(qw + (int64_t)n0 * K);
     const int chunks = (K + CHUNK - 1) / CHUNK;
 
     // Chunk kc into buffer b: wave w's instruction p fills 1 KiB of row
@@ -1627,15 +1614,14 @@ __global__ __launch_bounds__(256) void skinny_fwd_kernel(const int8_t *__restric
             const int idx = w * kPer + p;
             const int row = idx / kSegs, slot = (idx % kSegs) * 64 + lane;
             const int k = kc * CHUNK + (slot ^ (row & 15)) * 16;
-            const uint32_t off =
-                kc < chunks && k < K ? (uint32_t)((kGated ? row & 7 : row) * K + k) : kOob;
+            const uint32_t off = kc < chunks && k < K ? (uint32_t)(row * K + k) : kOob;
             lds_i8 *dst = (lds_i8 *)smem + b * kBuf + row * CHUNK + (idx % kSegs) * 1024;
             __builtin_amdgcn_raw_ptr_buffer_load_lds(
                 wr, (__attribute__((address_space(3))) void *)dst, 16, off, 0, 0, 0);
         }
     };
 
-    const int om = threadIdx.x / 16, on = n0 + threadIdx.x % (kGated ? 8 : 16);
+    const int om = threadIdx.x / 16, on = n0 + threadIdx.x % 16;
     constexpr bool kBf = AD == X_BF16;
     Raw8<kBf> early[2];
     int id = -1;
@@ -1690,31 +1676,6 @@ __global__ __launch_bounds__(256) void skinny_fwd_kernel(const int8_t *__restric
     i32x4 *red = reinterpret_cast<i32x4 *>(smem + 2 * kBuf);
     red[w * kWave + lane] = acc;
     __syncthreads();
-    if constexpr (EPI >= EPI_ACT) {
-        if (om >= M || (kGated && threadIdx.x % 16 >= 8))
-            return;
-        auto z = [&](int c, int64_t n) {        // column c of the 16, row n of the weight
-            int32_t sum = 0;
-#pragma unroll
-            for (int i = 0; i < 4; i++)
-                sum += reinterpret_cast<const int32_t *>(red)[(i * kWave + 16 * (om / 4) + c) * 4 + om % 4];
-            const float f = (float)sum * sx[om] * sw[n];
-            return bias ? f + bias[n] : f;
-        };
-        const int c = threadIdx.x % 16;
-        const int64_t at = (int64_t)om * N + on;
-        float y = act_value<EPI % EPI_ACT>(z(c, on));
-        if constexpr (kGated)
-            y = y * z(c + 8, on + ad.F);
-        if (ad.res)
-            y = y + (ad.res_bf16 ? bf16_lo(static_cast<const uint16_t *>(ad.res)[at])
-                                 : static_cast<const float *>(ad.res)[at]);
-        if (ad.y_bf16)
-            static_cast<uint16_t *>(out)[at] = (uint16_t)pack_bf16x2(y, y);
-        else
-            static_cast<float *>(out)[at] = y;
-        return;
-    }
     if constexpr (AD >= 0) {
         if (om >= M)
             return;
