@@ -53,6 +53,10 @@ def _guarded(torch, shape, dtype):
 SHAPES = [(1, 16, 16), (1, 4096, 256), (3, 48, 80), (16, 272, 4096), (16, 32, 1040), (5, 48, 2064), (9, 6416, 528),
           (12, 6432, 1040), (4, 4096, 3088), (8, 4112, 1008), (17, 16, 16),
           (33, 144, 1168), (255, 528, 64), (257, 1040, 192), (300, 2064, 400), (1000, 784, 256)]
+# The tiles of few tokens, each size: 32, 64 and 128 tokens per workgroup, four and eight
+# waves; and calls just past them, of 256 x 256 tiles.
+SHAPES += [(32, 80, 528), (64, 6416, 272), (50, 8240, 80), (65, 48, 1040), (100, 6416, 528), (129, 6416, 48),
+           (161, 10944, 64), (513, 4112, 144)]
 
 
 @pytest.mark.parametrize("M,N,K", SHAPES)

@@ -20,7 +20,7 @@ MARSHAL = os.path.join(HERE, "_marshal.so")
 BUILD_DIR = os.path.join(ROOT, "_build")
 SOURCES = ["api.hip", "api_around.hip", "quant.hip", "gemm.hip", "gemm_adapter.hip", "sgd.hip",
            "norm.hip", "adapter.hip", "adamw.hip", "stream.hip", "mfma_ceiling.hip", "gemm_act.hip",
-           "act_bwd.hip", "api_block.hip"]
+           "gemm_act_few.hip", "act_bwd.hip", "api_block.hip"]
 
 ARCH = "gfx950"
 FLAGS = [

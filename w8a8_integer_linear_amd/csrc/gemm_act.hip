@@ -174,9 +174,11 @@ template <int EPI> void run_stream(const ProductArgs &a, const ActEpilogue &e, h
 
 template <int ACT> void run(const ProductArgs &a, const ActEpilogue &e, hipStream_t st)
 {
-    // (A workgroup of the streaming kernel has 16 of the weight's rows, less than a
+    // (A workgroup of the streaming kernel may have 16 of the weight's rows, less than a
     // block of the checkpoint.)
     const bool stream = a.M <= 16 && !e.ck;
+    if (!stream && product_act_few(a))
+        return launch_product_act_few(a, e, st);
     if (e.gated)
         stream ? run_stream<EPI_GATED + ACT>(a, e, st) : run_tiles<EPI_GATED + ACT>(a, e, st);
     else

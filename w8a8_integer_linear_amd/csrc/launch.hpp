@@ -98,8 +98,12 @@ struct ActEpilogue {
     int8_t *ck;             // may be null
     float *ck_s;
 };
-// ProductArgs::out is y.  M of 16 and less without a checkpoint streams the weight.
+// ProductArgs::out is y.
 void launch_product_act(const ProductArgs &p, const ActEpilogue &e, hipStream_t st);
+// The same in tiles of few tokens, and whether they serve a call better
+// (gemm_act_few.hip).
+bool product_act_few(const ProductArgs &p);
+void launch_product_act_few(const ProductArgs &p, const ActEpilogue &e, hipStream_t st);
 
 // Backward of act and gate from the checkpoint (act_bwd.hip).
 struct ActBackward {
