@@ -5,6 +5,7 @@ and contiguity, their device pointers and the current HIP stream are passed to
 the C ABI, and a nonzero status raises QlinError.  Every step of the layer runs
 in the library's HIP kernels; there is no fallback.
 """
+import contextlib
 import ctypes
 import functools
 import os
@@ -694,19 +695,35 @@ def qlin_adamw_tensors(plan, lr, beta1, beta2, eps, seed, step, stream=None):
 
 # ---------------------------------------------- inside a feed-forward block
 
-def _on_device(f):
-    """Runs f on its first tensor's device, which all its tensors have to be on."""
-    @functools.wraps(f)
-    def call(first, *args, **kw):
-        device = first.get_device() if isinstance(first, torch.Tensor) else -1
-        for t in (*args, *kw.values()):
-            if isinstance(t, torch.Tensor) and t.get_device() != device:
-                raise ValueError(f"the tensors are on different devices ({t.device} and {first.device})")
-        if device < 0 or device == torch._C._cuda_getDevice():
-            return f(first, *args, **kw)
-        with torch.cuda.device(device):
-            return f(first, *args, **kw)
-    return call
+def _elsewhere(first, stream):
+    """Whether a call has to move to a stream or to its first tensor's device."""
+    return stream is not None or (isinstance(first, torch.Tensor) and first.is_cuda
+                                  and first.get_device() != torch._C._cuda_getDevice())
+
+
+def _handle(first):
+    """The current stream's, for a call on GPU tensors (others are about to be refused)."""
+    return _stream(None) if isinstance(first, torch.Tensor) and first.is_cuda else 0
+
+
+@contextlib.contextmanager
+def _there(first, stream):
+    """The device of the first tensor, and the stream, as the current ones."""
+    with contextlib.ExitStack() as s:
+        if isinstance(first, torch.Tensor) and first.is_cuda:
+            s.enter_context(torch.cuda.device(first.device))
+        if stream is not None:
+            s.enter_context(torch.cuda.stream(stream))
+        yield
+
+
+@functools.lru_cache(maxsize=None)
+def _compiled(name):
+    """(the compiled binding, the address of a library function)"""
+    _load_compiled()
+    from . import _marshal
+    _marshal.set_failed(_check)
+    return _marshal, ctypes.cast(getattr(lib(), name), _vp).value
 
 
 def _act_code(act):
@@ -716,37 +733,14 @@ def _act_code(act):
     return code
 
 
-def _forward(name, gated, qx, sx, qw, sw, bias, act, residual, y, dtype, ck, ck_s, save, workspace, stream):
-    code = _act_code(act)
-    M, K = qx.shape
-    N = qw.shape[0]
-    if gated and N % 2:
-        raise ValueError(f"qw has the gate's rows and as many others, got {N}")
-    F = N // 2 if gated else N
-    px, pw = _addr(qx, "qx", torch.int8), _addr(qw, "qw", torch.int8, N, K)
-    psx, psw = _addr(sx, "sx", torch.float32, M), _addr(sw, "sw", torch.float32, N)
-    pb = None if bias is None else _addr(bias, "bias", torch.float32, N)
-    y = _new(qx, dtype, M, F) if y is None else y
-    py, y_code = _addr(y, "y", y.dtype, M, F), _dtype_code(y)
-    pck = pcs = None
-    if save or ck is not None or ck_s is not None:
-        per = (N // F) * -(-F // CK_BLOCK) if F else 0
-        ck = _new(qx, torch.int8, M, N) if ck is None else ck
-        ck_s = _new(qx, torch.float32, M, per) if ck_s is None else ck_s
-        pck, pcs = _addr(ck, "ck", torch.int8, M, N), _addr(ck_s, "ck_s", torch.float32, M, per)
-    need = qlin_fwd_gated_ws_bytes if gated else qlin_fwd_act_ws_bytes
-    workspace, pws, size = _workspace(workspace, lambda: need(M, F, K), qx, zero=True)
-    if gated:
-        status = lib().qlin_fwd_gated(px, psx, pw, psw, pb, code, M, F, K, py, y_code, pck, pcs, pws, size,
-                                      _stream(stream))
-    else:
-        pr, r_code = None, 0
-        if residual is not None:
-            pr, r_code = _addr(residual, "residual", residual.dtype, M, N), _dtype_code(residual)
-        status = lib().qlin_fwd_act(px, psx, pw, psw, pb, code, pr, r_code, M, N, K, py, y_code, pck, pcs,
-                                    pws, size, _stream(stream))
-    _check(name, status)
-    return y, ck, ck_s
+def _scratch(workspace, need, like, zero):
+    """The workspace: the caller's, a fresh one, or None where none is needed."""
+    if workspace is not None or not isinstance(like, torch.Tensor) or not like.is_cuda:
+        return workspace
+    n = need()
+    if not n:
+        return None
+    return (torch.zeros if zero else torch.empty)(n, dtype=torch.uint8, device=like.device)
 
 
 @functools.lru_cache(maxsize=1024)
@@ -754,15 +748,20 @@ def qlin_fwd_act_ws_bytes(M, N, K):
     return int(lib().qlin_fwd_act_ws_bytes(int(M), int(N), int(K)))
 
 
-@_on_device
-@_on_stream
 def qlin_fwd_act(qx, sx, qw, sw, bias=None, act="none", residual=None, y=None, dtype=torch.bfloat16, ck=None,
                  ck_s=None, save=False, workspace=None, stream=None):
     """act(z) + residual with z = qlin_fwd(...), rounded once to y's type (dtype where
     y is not given).  save, or ck and ck_s: keeps the 8-bit checkpoint of z for
     qlin_act_bwd.  Returns (y, ck, ck_s); ck and ck_s are None without a checkpoint."""
-    return _forward("qlin_fwd_act", False, qx, sx, qw, sw, bias, act, residual, y, dtype, ck, ck_s, save,
-                    workspace, stream)
+    if _elsewhere(qx, stream):
+        with _there(qx, stream):
+            return qlin_fwd_act(qx, sx, qw, sw, bias, act, residual, y, dtype, ck, ck_s, save, workspace)
+    compiled, f = _compiled("qlin_fwd_act")
+    code = _act_code(act)
+    if workspace is None:
+        workspace = _scratch(None, lambda: qlin_fwd_act_ws_bytes(qx.shape[0], qw.shape[0], qx.shape[1]), qx, True)
+    return compiled.forward(f, False, qx, sx, qw, sw, bias, code, residual, y, dtype, ck, ck_s, save, workspace,
+                            _handle(qx))
 
 
 @functools.lru_cache(maxsize=1024)
@@ -770,14 +769,20 @@ def qlin_fwd_gated_ws_bytes(M, F, K):
     return int(lib().qlin_fwd_gated_ws_bytes(int(M), int(F), int(K)))
 
 
-@_on_device
-@_on_stream
 def qlin_fwd_gated(qx, sx, qw, sw, bias=None, act="silu", y=None, dtype=torch.bfloat16, ck=None, ck_s=None,
                    save=False, workspace=None, stream=None):
     """act(g) u with [g | u] = qlin_fwd(...); qw [2 F, K] has the gate's rows first.
     Everything else as in qlin_fwd_act."""
-    return _forward("qlin_fwd_gated", True, qx, sx, qw, sw, bias, act, None, y, dtype, ck, ck_s, save,
-                    workspace, stream)
+    if _elsewhere(qx, stream):
+        with _there(qx, stream):
+            return qlin_fwd_gated(qx, sx, qw, sw, bias, act, y, dtype, ck, ck_s, save, workspace)
+    compiled, f = _compiled("qlin_fwd_gated")
+    code = _act_code(act)
+    if workspace is None:
+        workspace = _scratch(None, lambda: qlin_fwd_gated_ws_bytes(qx.shape[0], qw.shape[0] // 2, qx.shape[1]), qx,
+                             True)
+    return compiled.forward(f, True, qx, sx, qw, sw, bias, code, None, y, dtype, ck, ck_s, save, workspace,
+                            _handle(qx))
 
 
 @functools.lru_cache(maxsize=1024)
@@ -785,55 +790,37 @@ def qlin_act_bwd_ws_bytes(M, F, gated=False):
     return int(lib().qlin_act_bwd_ws_bytes(int(M), int(F), int(gated)))
 
 
-@_on_device
-@_on_stream
 def qlin_act_bwd(dy, ck, ck_s, act, gated=False, sw=None, sx=None, dz=None, dtype=torch.bfloat16, s1=None,
                  s2=None, db=None, want_db=False, workspace=None, stream=None):
     """Backward of qlin_fwd_act or qlin_fwd_gated from their checkpoint.  Returns (dz,
     s1, s2, db): dz of the given tensor's type or of dtype, the scales of its two
     quantizations (s1 where sw is given, s2 where sx is, for
     qlin_quantize_grad_scaled), db where it is given or wanted."""
+    if _elsewhere(dy, stream):
+        with _there(dy, stream):
+            return qlin_act_bwd(dy, ck, ck_s, act, gated, sw, sx, dz, dtype, s1, s2, db, want_db, workspace)
+    compiled, f = _compiled("qlin_act_bwd")
     code = _act_code(act)
-    M, F = dy.shape
-    N = 2 * F if gated else F
-    per = (2 if gated else 1) * -(-F // CK_BLOCK)
-    pdy, dy_code = _addr(dy, "dy", dy.dtype), _dtype_code(dy)
-    pck, pcs = _addr(ck, "ck", torch.int8, M, N), _addr(ck_s, "ck_s", torch.float32, M, per)
-    dz = _new(dy, dtype, M, N) if dz is None else dz
-    pdz, dz_code = _addr(dz, "dz", dz.dtype, M, N), _dtype_code(dz)
-    psw = psx = p1 = p2 = pdb = None
-    if sw is not None:
-        s1 = _new(dy, torch.float32, M) if s1 is None else s1
-        psw, p1 = _addr(sw, "sw", torch.float32, N), _addr(s1, "s1", torch.float32, M)
-    elif s1 is not None:
-        raise ValueError("s1 needs sw")
-    if sx is not None:
-        s2 = _new(dy, torch.float32, N) if s2 is None else s2
-        psx, p2 = _addr(sx, "sx", torch.float32, M), _addr(s2, "s2", torch.float32, N)
-    elif s2 is not None:
-        raise ValueError("s2 needs sx")
-    if db is None and want_db:
-        db = _new(dy, torch.float32, N)
-    if db is not None:
-        pdb = _addr(db, "db", torch.float32, N)
-    workspace, pws, size = _workspace(workspace, lambda: qlin_act_bwd_ws_bytes(M, F, bool(gated)), dy,
-                                      zero=False)
-    _check("qlin_act_bwd", lib().qlin_act_bwd(
-        pdy, dy_code, pck, pcs, code, int(bool(gated)), psw, psx, M, F, pdz, dz_code, p1, p2, pdb, pws, size,
-        _stream(stream)))
-    return dz, s1, s2, db
+    if workspace is None:
+        workspace = _scratch(None, lambda: qlin_act_bwd_ws_bytes(dy.shape[0], dy.shape[1], bool(gated)), dy, False)
+    return compiled.backward(f, dy, ck, ck_s, code, gated, sw, sx, dz, dtype, s1, s2, db, want_db, workspace,
+                             _handle(dy))
 
 
-@_on_device
-@_on_stream
 def qlin_quantize_grad_scaled(dy, sw, sx, s1, s2, q1=None, q2=None, stream=None):
     """qlin_quantize_grad's codes for known scales.  Returns (q1, q2)."""
+    if _elsewhere(dy, stream):
+        with _there(dy, stream):
+            return qlin_quantize_grad_scaled(dy, sw, sx, s1, s2, q1, q2)
     M, N = dy.shape
     pdy, code = _addr(dy, "dy", dy.dtype), _dtype_code(dy)
+    for t in (sw, sx, s1, s2, q1, q2):
+        if t is not None and t.device != dy.device:
+            raise ValueError(f"the tensors are on different devices ({t.device} and {dy.device})")
     q1 = _new(dy, torch.int8, M, N) if q1 is None else q1
     q2 = _new(dy, torch.int8, M, N) if q2 is None else q2
     _check("qlin_quantize_grad_scaled", lib().qlin_quantize_grad_scaled(
         pdy, code, M, N, _addr(sw, "sw", torch.float32, N), _addr(sx, "sx", torch.float32, M),
         _addr(s1, "s1", torch.float32, M), _addr(s2, "s2", torch.float32, N),
-        _addr(q1, "q1", torch.int8, M, N), _addr(q2, "q2", torch.int8, M, N), _stream(stream)))
+        _addr(q1, "q1", torch.int8, M, N), _addr(q2, "q2", torch.int8, M, N), _stream(None)))
     return q1, q2

@@ -56,7 +56,7 @@ def _build_marshal(verbose):
     tmp = MARSHAL + ".tmp"
     cmd = [shutil.which("g++") or "c++", "-O2", "-std=c++17", "-fPIC", "-shared", "-Wall",
            f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}",
-           f"-I{sysconfig.get_paths()['include']}",
+           f"-I{sysconfig.get_paths()['include']}", f"-I{os.path.join(ROOT, 'include')}",
            *[f"-isystem{p}" for p in cpp_extension.include_paths()],
            os.path.join(CSRC, "marshal.cpp"), f"-L{libs}", "-ltorch_python", "-ltorch_cpu", "-lc10",
            "-o", tmp]

@@ -7,8 +7,14 @@
 
 #include <ATen/ops/empty.h>
 #include <torch/csrc/Dtype.h>
+#include <torch/csrc/DynamicTypes.h>
 #include <torch/csrc/Exceptions.h>
 #include <torch/csrc/autograd/python_variable.h>
+
+#include <optional>
+#include <utility>
+
+#include "qlin.h"
 
 namespace {
 
@@ -96,6 +102,256 @@ PyObject *empty(PyObject *, PyObject *const *args, Py_ssize_t n)
     END_HANDLE_TH_ERRORS
 }
 
+// ------------------------------------------------ inside a feed-forward block
+//
+// Whole calls: a dozen tensors' checks, their addresses and the library's call with
+// twenty arguments take longer through the interpreter and ctypes than a few tokens
+// take the GPU (host time per call 7.6 -> 4.4 us forward, 10.4 -> 6.6 backward).
+
+PyObject *failed = nullptr;     // failed(name, status): raises for a nonzero status
+
+// A Python error is set.
+struct Raised {
+};
+
+// Checks tensors against one another's device.
+struct Args {
+    at::Device device = at::kCPU;
+    bool first = true;
+
+    // The address of a contiguous GPU tensor of this type and shape; raises the
+    // binding's own error for another one.
+    void *operator()(PyObject *o, const char *name, at::ScalarType type, std::initializer_list<int64_t> shape)
+    {
+        if (THPVariable_Check(o)) {
+            const at::Tensor &t = THPVariable_Unpack(o);
+            if (t.is_cuda() && t.layout() == at::kStrided && t.scalar_type() == type && t.is_contiguous() &&
+                t.sizes() == at::IntArrayRef(shape)) {
+                if (!first && t.device() != device) {
+                    PyErr_Format(PyExc_ValueError, "the tensors are on different devices (%s: %s, not %s)", name,
+                                 t.device().str().c_str(), device.str().c_str());
+                    throw Raised();
+                }
+                device = t.device();
+                first = false;
+                return const_cast<void *>(t.const_data_ptr());
+            }
+        }
+        PyObject *dims = PyTuple_New((Py_ssize_t)shape.size());
+        Py_ssize_t i = 0;
+        for (const int64_t d : shape)
+            PyTuple_SET_ITEM(dims, i++, PyLong_FromLongLong(d));
+        PyObject *dtype = reinterpret_cast<PyObject *>(torch::getTHPDtype(type));
+        PyObject *r = PyObject_CallFunction(refuse, "OsOO", o, name, dtype, dims);
+        Py_DECREF(dims);
+        if (r) {
+            Py_DECREF(r);
+            PyErr_Format(PyExc_ValueError, "%s: unsupported tensor", name);
+        }
+        throw Raised();
+    }
+
+    // Of a float tensor: its type as the library names it.
+    void *operator()(PyObject *o, const char *name, int &code, std::initializer_list<int64_t> shape)
+    {
+        at::ScalarType type = at::kFloat;
+        if (THPVariable_Check(o))
+            type = THPVariable_Unpack(o).scalar_type();
+        if (type != at::kFloat && type != at::kBFloat16) {
+            PyErr_Format(PyExc_TypeError, "%s must be float32 or bfloat16, got %s", name, c10::toString(type));
+            throw Raised();
+        }
+        code = type == at::kFloat ? QLIN_F32 : QLIN_BF16;
+        return (*this)(o, name, type, shape);
+    }
+};
+
+// The two sizes of a tensor whose other checks follow.
+std::pair<int64_t, int64_t> two(PyObject *o, const char *name)
+{
+    if (!THPVariable_Check(o) || THPVariable_Unpack(o).dim() != 2) {
+        PyErr_Format(PyExc_ValueError, "%s must be a tensor of two dimensions", name);
+        throw Raised();
+    }
+    const at::Tensor &t = THPVariable_Unpack(o);
+    return {t.size(0), t.size(1)};
+}
+
+// An owned reference: o, or if that is None a new tensor beside like.
+struct Out {
+    PyObject *o;
+    Out(PyObject *given, PyObject *like, at::ScalarType type, std::initializer_list<int64_t> shape)
+    {
+        if (given != Py_None)
+            Py_INCREF(o = given);
+        else
+            o = THPVariable_Wrap(at::empty(at::IntArrayRef(shape), THPVariable_Unpack(like).options().dtype(type)));
+        if (!o)
+            throw Raised();
+    }
+    explicit Out(PyObject *none) : o(none) { Py_INCREF(o); }
+    Out(const Out &) = delete;
+    ~Out() { Py_XDECREF(o); }
+};
+
+at::ScalarType type_of(PyObject *dtype)
+{
+    if (!THPDtype_Check(dtype)) {
+        PyErr_SetString(PyExc_TypeError, "dtype must be a torch dtype");
+        throw Raised();
+    }
+    return reinterpret_cast<THPDtype *>(dtype)->scalar_type;
+}
+
+// The address and size of a workspace (None: none is needed).
+void *workspace_of(Args &arg, PyObject *o, size_t &bytes)
+{
+    bytes = 0;
+    if (o == Py_None)
+        return nullptr;
+    bytes = THPVariable_Check(o) ? (size_t)THPVariable_Unpack(o).numel() : 0;
+    return arg(o, "workspace", at::kByte, {(int64_t)bytes});
+}
+
+void check(const char *name, int status)
+{
+    if (status == QLIN_OK)
+        return;
+    PyObject *r = PyObject_CallFunction(failed, "si", name, status);
+    Py_XDECREF(r);
+    if (r)
+        PyErr_SetString(PyExc_RuntimeError, name);
+    throw Raised();
+}
+
+template <typename F> F function_at(PyObject *address) { return reinterpret_cast<F>(PyLong_AsVoidPtr(address)); }
+
+// forward(function, gated, qx, sx, qw, sw, bias, act, residual, y, dtype, ck, ck_s, save,
+// workspace, stream) -> (y, ck, ck_s)
+PyObject *forward(PyObject *, PyObject *const *a, Py_ssize_t n)
+{
+    if (n != 16) {
+        PyErr_SetString(PyExc_TypeError, "forward takes 16 arguments");
+        return nullptr;
+    }
+    HANDLE_TH_ERRORS
+    try {
+        const bool gated = PyObject_IsTrue(a[1]);
+        const char *name = gated ? "qlin_fwd_gated" : "qlin_fwd_act";
+        PyObject *qx = a[2];
+        const auto [M, K] = two(qx, "qx");
+        const int64_t N = two(a[4], "qw").first;
+        if (gated && N % 2) {
+            PyErr_Format(PyExc_ValueError, "qw has the gate's rows and as many others, got %lld", (long long)N);
+            throw Raised();
+        }
+        const int64_t F = gated ? N / 2 : N;
+        Args arg;
+        const auto *px = static_cast<const int8_t *>(arg(qx, "qx", at::kChar, {M, K}));
+        const auto *psx = static_cast<const float *>(arg(a[3], "sx", at::kFloat, {M}));
+        const auto *pw = static_cast<const int8_t *>(arg(a[4], "qw", at::kChar, {N, K}));
+        const auto *psw = static_cast<const float *>(arg(a[5], "sw", at::kFloat, {N}));
+        const float *pb =
+            a[6] == Py_None ? nullptr : static_cast<const float *>(arg(a[6], "bias", at::kFloat, {N}));
+        const int act = (int)PyLong_AsLong(a[7]);
+        int y_code = 0, r_code = 0;
+        const void *pr = a[8] == Py_None ? nullptr : arg(a[8], "residual", r_code, {M, F});
+        const Out y(a[9], qx, type_of(a[10]), {M, F});
+        void *py = arg(y.o, "y", y_code, {M, F});
+        const bool keep = PyObject_IsTrue(a[13]) || a[11] != Py_None || a[12] != Py_None;
+        const int64_t per = (F + QLIN_CK_BLOCK - 1) / QLIN_CK_BLOCK * (gated ? 2 : 1);
+        // (Named, so that both are given back where the second cannot be made.)
+        std::optional<Out> ck, ck_s;
+        int8_t *pc = nullptr;
+        float *pcs = nullptr;
+        if (keep) {
+            ck.emplace(a[11], qx, at::kChar, std::initializer_list<int64_t>{M, N});
+            ck_s.emplace(a[12], qx, at::kFloat, std::initializer_list<int64_t>{M, per});
+            pc = static_cast<int8_t *>(arg(ck->o, "ck", at::kChar, {M, N}));
+            pcs = static_cast<float *>(arg(ck_s->o, "ck_s", at::kFloat, {M, per}));
+        } else {
+            ck.emplace(Py_None);
+            ck_s.emplace(Py_None);
+        }
+        size_t bytes;
+        void *ws = workspace_of(arg, a[14], bytes);
+        void *stream = PyLong_AsVoidPtr(a[15]);
+        if (PyErr_Occurred())
+            throw Raised();
+        check(name, gated ? function_at<decltype(&qlin_fwd_gated)>(a[0])(px, psx, pw, psw, pb, act, M, F, K, py,
+                                                                         y_code, pc, pcs, ws, bytes, stream)
+                          : function_at<decltype(&qlin_fwd_act)>(a[0])(px, psx, pw, psw, pb, act, pr, r_code, M, N,
+                                                                       K, py, y_code, pc, pcs, ws, bytes, stream));
+        return PyTuple_Pack(3, y.o, ck->o, ck_s->o);
+    } catch (const Raised &) {
+        return nullptr;
+    }
+    END_HANDLE_TH_ERRORS
+}
+
+// backward(function, dy, ck, ck_s, act, gated, sw, sx, dz, dtype, s1, s2, db, want_db,
+// workspace, stream) -> (dz, s1, s2, db)
+PyObject *backward(PyObject *, PyObject *const *a, Py_ssize_t n)
+{
+    if (n != 16) {
+        PyErr_SetString(PyExc_TypeError, "backward takes 16 arguments");
+        return nullptr;
+    }
+    HANDLE_TH_ERRORS
+    try {
+        PyObject *dy = a[1];
+        const auto [M, F] = two(dy, "dy");
+        const bool gated = PyObject_IsTrue(a[5]);
+        const int64_t N = gated ? 2 * F : F, per = (F + QLIN_CK_BLOCK - 1) / QLIN_CK_BLOCK * (gated ? 2 : 1);
+        Args arg;
+        int dy_code = 0, dz_code = 0;
+        const void *pdy = arg(dy, "dy", dy_code, {M, F});
+        const auto *pc = static_cast<const int8_t *>(arg(a[2], "ck", at::kChar, {M, N}));
+        const auto *pcs = static_cast<const float *>(arg(a[3], "ck_s", at::kFloat, {M, per}));
+        const int act = (int)PyLong_AsLong(a[4]);
+        const Out dz(a[8], dy, type_of(a[9]), {M, N});
+        void *pz = arg(dz.o, "dz", dz_code, {M, N});
+        // A scale and what it is the scale of: both or neither.
+        std::optional<Out> s[3];
+        const float *p[2] = {nullptr, nullptr};
+        float *out[3] = {nullptr, nullptr, nullptr};
+        const char *names[3] = {"s1", "s2", "db"}, *of[2] = {"sw", "sx"};
+        for (int k = 0; k < 3; k++) {
+            const int64_t size = k == 0 ? M : N;
+            if (k < 2 ? a[6 + k] != Py_None : PyObject_IsTrue(a[13]) || a[12] != Py_None) {
+                if (k < 2)
+                    p[k] = static_cast<const float *>(arg(a[6 + k], of[k], at::kFloat, {k == 0 ? N : M}));
+                s[k].emplace(a[10 + k], dy, at::kFloat, std::initializer_list<int64_t>{size});
+                out[k] = static_cast<float *>(arg(s[k]->o, names[k], at::kFloat, {size}));
+            } else if (a[10 + k] != Py_None) {
+                PyErr_Format(PyExc_ValueError, "%s needs %s", names[k], of[k]);
+                throw Raised();
+            } else {
+                s[k].emplace(Py_None);
+            }
+        }
+        size_t bytes;
+        void *ws = workspace_of(arg, a[14], bytes);
+        void *stream = PyLong_AsVoidPtr(a[15]);
+        if (PyErr_Occurred())
+            throw Raised();
+        check("qlin_act_bwd", function_at<decltype(&qlin_act_bwd)>(a[0])(pdy, dy_code, pc, pcs, act, gated, p[0], p[1],
+                                                                         M, F, pz, dz_code, out[0], out[1], out[2],
+                                                                         ws, bytes, stream));
+        return PyTuple_Pack(4, dz.o, s[0]->o, s[1]->o, s[2]->o);
+    } catch (const Raised &) {
+        return nullptr;
+    }
+    END_HANDLE_TH_ERRORS
+}
+
+PyObject *set_failed(PyObject *, PyObject *f)
+{
+    Py_INCREF(f);
+    Py_XSETREF(failed, f);
+    Py_RETURN_NONE;
+}
+
 PyObject *set_refuse(PyObject *, PyObject *f)
 {
     Py_INCREF(f);
@@ -109,6 +365,11 @@ PyMethodDef methods[] = {
     {"empty", reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(empty)), METH_FASTCALL,
      "empty(like, dtype, *sizes)"},
     {"set_refuse", set_refuse, METH_O, "set_refuse(function)"},
+    {"set_failed", set_failed, METH_O, "set_failed(function)"},
+    {"forward", reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(forward)), METH_FASTCALL,
+     "a forward call inside a feed-forward block"},
+    {"backward", reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(backward)), METH_FASTCALL,
+     "qlin_act_bwd"},
     {nullptr, nullptr, 0, nullptr},
 };
 PyModuleDef module = {PyModuleDef_HEAD_INIT, "_marshal", nullptr, -1, methods,
