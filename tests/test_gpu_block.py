@@ -110,10 +110,11 @@ def test_gated_forward(M, F, K, act):
         assert torch.equal(s.cpu(), scales) and torch.equal(c.cpu(), codes)
 
 
-@pytest.mark.parametrize("M,N,K", [(1000, 8480, 1040), (611, 14336, 1024), (2100, 5408, 528)])
-def test_more_tiles_than_compute_units(M, N, K):
-    """A last round of tiles that is split along the contraction, and one workspace
-    that both calls and the plain product use in turn."""
+@pytest.mark.parametrize("M,N,K", [(1000, 8480, 1040), (611, 14336, 1024), (600, 8160, 4112), (700, 2816, 1552),
+                                   (1300, 11744, 1552)])
+def test_many_tiles(M, N, K):
+    """Whole tiles, and last rounds of tiles that are split along the contraction in two
+    and three; one workspace that both calls and the plain product use in turn."""
     torch = torch_cuda()
     import w8a8_integer_linear_amd as qlin
     qx, sx, qw, sw, b = _operands(torch, M, N, K, 3)

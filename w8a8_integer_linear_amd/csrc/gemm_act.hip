@@ -17,7 +17,16 @@ template <int EPI> void run_tiles(const ProductArgs &a, const ActEpilogue &e, hi
     p.tiles_j = (int)((a.N + 255) / 256);       // (with a gate, 128 outputs per tile)
     const int tiles = p.tiles_i * p.tiles_j;
     const dim3 block(8 * kWave);
-    if (p.split >= 2)
+    // The last round's tiles are split along the contraction where that saves more than
+    // their partial sums cost, which grows with the tiles (all of them write theirs at
+    // once).  us split / whole, bf16 with GELU, by tiles and contraction:
+    //               2048          4096          8192
+    //     32     63.2 / 65.3   92.6 / 106
+    //     64     32.1 / 31.2   41.1 / 48.3   58.8 / 82.4
+    //    112     39.9 / 33.0   48.4 / 49.2   70.5 / 83.4
+    //    128     41.9 / 34.2   53.0 / 50.7   76.8 / 85.3
+    const bool split = p.split >= 2 && 10 * ((p.T + 127) / 128) > 3 * (tiles - p.full);
+    if (split)
         hipLaunchKernelGGL((gemm_kernel<2, 4, false, false, EPI, MODE_SPLIT>),
                            dim3((unsigned)(p.full + (tiles - p.full) * p.split)), block, 0, st, p);
     else
