@@ -550,14 +550,20 @@ __device__ __forceinline__ void store_pass(const GemmParams &p, const lds_i8 *st
 // for the same number of loads.  plan() is computed once per stage; issue()
 // enqueues loads G0 .. G1 - 1 of the stage's OpA::kLoads + OpB::kLoads per
 // lane (A's first).
-template <typename OpA, typename OpB, bool AKM, bool BKM, int kBK>
+//
+// BFREE: a contiguous B operand's loads are not masked in a partial stage (A's zeros
+// meet whatever B holds there): they run on into the operand's next rows, and past its
+// last one into the resource's end; bleft is the bytes from bbase to that.
+template <typename OpA, typename OpB, bool AKM, bool BKM, int kBK, bool BFREE = false>
 struct StageLoads {
+    static_assert(!BFREE || (!AKM && !BKM), "contiguous operands");
     __amdgpu_buffer_rsrc_t ra, rb;
     int trel;
     bool live, full;
 
     __device__ static __forceinline__ StageLoads plan(const GemmParams &p, const int8_t *abase,
-                                                      const int8_t *bbase, int kb, int KT, int s)
+                                                      const int8_t *bbase, int kb, int KT, int s,
+                                                      uint32_t bleft = 0)
     {
         StageLoads L;
         L.live = s < KT;
@@ -567,7 +573,12 @@ struct StageLoads {
         const int8_t *ak = AKM ? abase + (int64_t)k0 * p.lda : abase + k0;
         const int8_t *bk = BKM ? bbase + (int64_t)k0 * p.ldb : bbase + k0;
         L.ra = make_rsrc(ak, AKM ? km_records(L.live, L.full, L.trel, p.lda) : kOob);
-        L.rb = make_rsrc(bk, BKM ? km_records(L.live, L.full, L.trel, p.ldb) : kOob);
+        if constexpr (BFREE) {
+            const uint32_t left = bleft - (uint32_t)k0;
+            L.rb = make_rsrc(bk, left < kOob ? left : kOob);
+        } else {
+            L.rb = make_rsrc(bk, BKM ? km_records(L.live, L.full, L.trel, p.ldb) : kOob);
+        }
         return L;
     }
 
@@ -580,8 +591,8 @@ struct StageLoads {
         if constexpr (G0 < nA)
             OpA::template issue<G0, (G1 < nA ? G1 : nA)>(ra, voffA, trel, live, full, w, dstA);
         if constexpr (G1 > nA)
-            OpB::template issue<(G0 > nA ? G0 - nA : 0), G1 - nA>(rb, voffB, trel, live, full, w,
-                                                                  dstB);
+            OpB::template issue<(G0 > nA ? G0 - nA : 0), G1 - nA>(rb, voffB, trel, live,
+                                                                  BFREE || full, w, dstB);
     }
 };
 
@@ -1066,9 +1077,13 @@ __global__ __launch_bounds__(WM *WN * 64, 1) void gemm_kernel(GemmParams p)
     // the stage after next, behind the last row block's pairs, into the
     // buffers whose reads have just passed the stage barrier: a whole stage
     // to land (dW 4-5% and dX 3% faster; lead 2 for contiguous operands made
-    // the forward 2% slower).
+    // the forward 2% slower).  In a feed-forward block, whose batches are of any
+    // size, the weight has lead 2: fewer tiles share it and more of it comes from
+    // HBM (us, lead 1 / 2: 611 x 4096 -> 2 x 14336 96.5 / 93.2, 2048 x 5376 -> 2 x 7168
+    // 156 / 145, 8192 x 14336 -> 4096 376 / 351, 8192 x 4096 -> 2 x 14336 777 / 736; but
+    // 12000 x 5376 -> 7168 376 / 380).
     constexpr int kSpread = 8;
-    constexpr int kLeadA = AKM ? 2 : 1, kLeadB = BKM ? 2 : 1;
+    constexpr int kLeadA = AKM ? 2 : 1, kLeadB = BKM || EPI >= EPI_ACT ? 2 : 1;
     static_assert(NK == 2 && FM % 2 == 0 && kSpread <= FN * (FM - 1) && kSpread % FN == 0,
                   "fragment schedule shape");
     using OpA = Operand<BM, AKM, NT, kBK>;
@@ -1122,7 +1137,15 @@ __global__ __launch_bounds__(WM *WN * 64, 1) void gemm_kernel(GemmParams p)
     // unrolled loop below addresses either stage with constants.
     // Part G of stage s's buffer-to-LDS loads (planned in L), into buffers
     // s % 2.
-    using Loads = StageLoads<OpA, OpB, AKM, BKM, kBK>;
+    constexpr bool kFree = EPI >= EPI_ACT;
+    using Loads = StageLoads<OpA, OpB, AKM, BKM, kBK, kFree>;
+    // (Bytes to B's end, as far as 32-bit offsets and the longest row matter.)
+    uint32_t bleft = 0;
+    if constexpr (kFree) {
+        const int64_t rows = (kGated ? 2 : 1) * (int64_t)p.S - j0 - (kGated && wu >= 4 ? p.act.F : 0);
+        const int64_t left = rows * p.ldb;
+        bleft = left < (int64_t)kOob + (1 << 18) ? (uint32_t)left : kOob + (1 << 18);
+    }
     auto issue = [&](const Loads &L, int s, auto G) {
         constexpr int g = decltype(G)::value, per = kLoads / kSpread;
         L.template issue<g * per, (g + 1) * per>(voffA, voffB, wu, smem + (s & 1) * OpA::kBytes,
@@ -1206,8 +1229,8 @@ __global__ __launch_bounds__(WM *WN * 64, 1) void gemm_kernel(GemmParams p)
     // out by their operand's lead (kLeadA, kLeadB).
     auto stage = [&](int kt, auto P) {
         constexpr int par = decltype(P)::value;
-        const Loads L1 = Loads::plan(p, abase, bbase, kb, KT, kt + 1);
-        const Loads L2 = Loads::plan(p, abase, bbase, kb, KT, kt + 2);
+        const Loads L1 = Loads::plan(p, abase, bbase, kb, KT, kt + 1, bleft);
+        const Loads L2 = Loads::plan(p, abase, bbase, kb, KT, kt + 2, bleft);
         static_for<FM - 1>([&](auto F) {
             constexpr int f = decltype(F)::value;
             read_a(P, std::integral_constant<int, f + 1>{});
@@ -1267,9 +1290,9 @@ __global__ __launch_bounds__(WM *WN * 64, 1) void gemm_kernel(GemmParams p)
         });
     };
     {
-        const Loads L0 = Loads::plan(p, abase, bbase, kb, KT, 0);
+        const Loads L0 = Loads::plan(p, abase, bbase, kb, KT, 0, bleft);
         static_for<kSpread>([&](auto G) { issue(L0, 0, G); });
-        const Loads L1 = Loads::plan(p, abase, bbase, kb, KT, 1);
+        const Loads L1 = Loads::plan(p, abase, bbase, kb, KT, 1, bleft);
         static_for<n2>([&](auto G) {
             issue(L1, 1, std::integral_constant<int, part_of(2, decltype(G)::value)>{});
         });
