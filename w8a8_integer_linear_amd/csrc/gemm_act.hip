@@ -105,8 +105,9 @@ __global__ __launch_bounds__(256) void stream_act_kernel(GemmParams p)
             }
     };
     // Per chunk: the next one's loads (of nothing past the last), a wait until only they
-    // are outstanding, the products; the second barrier holds the buffer until every
-    // wave has read it.  (No fences, so that the loads stay in flight.)
+    // are outstanding, the products; the second barrier, behind a wait for the wave's
+    // own LDS reads, holds the buffer until every wave has read it.  (No fences, so that
+    // the loads stay in flight.)
     i32x4 x0[kSteps], x1[kSteps];
     issue(0, 0, x0);
     for (int kc = 0; kc < chunks; kc += 2) {
@@ -114,11 +115,13 @@ __global__ __launch_bounds__(256) void stream_act_kernel(GemmParams p)
         wait_vmcnt<kLoads + kSteps>();
         barrier_no_fence();
         multiply(0, x0);
+        wait_lgkmcnt0();
         barrier_no_fence();
         issue(kc + 2, 0, x0);
         wait_vmcnt<kLoads + kSteps>();
         barrier_no_fence();
         multiply(1, x1);
+        wait_lgkmcnt0();
         barrier_no_fence();
     }
     // (The loads of nothing past the end still write zeros to LDS.)

@@ -80,9 +80,11 @@ __global__ __launch_bounds__(WAVES * kWave) void few_act_kernel(GemmParams p)
         issue(c, c);                                // (past the last chunk: zeros)
     int cur = 0, fill = NB - 1;
     for (int kc = 0; kc < chunks; kc++) {
-        // Chunk kc has landed, and every wave has read chunk kc - 1, whose buffer is
-        // filled next.  (No fence, so that the loads stay in flight.)
+        // Chunk kc has landed, and every wave has read chunk kc - 1 (its own LDS reads are
+        // back), whose buffer is filled next.  (No fence, so that the loads stay in
+        // flight.)
         wait_vmcnt<(NB - 2) * kLoads>();
+        wait_lgkmcnt0();
         barrier_no_fence();
         issue(kc + NB - 1, fill);
         const int8_t *buf = smem + cur * kBuf;
