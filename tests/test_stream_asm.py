@@ -37,7 +37,8 @@ def test_the_check_itself():
 
 
 @pytest.mark.parametrize("source,kernel,count", [
-    ("gemm_act.hip", "stream_act_kernel", 30), ("gemm_act_few.hip", "few_act_kernel", 9)])
+    ("gemm_act.hip", "stream_act_kernel", 30), ("gemm_act_few.hip", "few_act_kernel", 9),
+    ("gemm.hip", "skinny_fwd_kernel", 4), ("gemm_adapter.hip", "skinny_fwd_kernel", 4)])
 def test_no_read_is_outstanding_at_a_barrier(tmp_path, source, kernel, count):
     cc = shutil.which("hipcc") or "/opt/rocm/bin/hipcc"
     if not os.path.exists(cc):

@@ -1691,9 +1691,11 @@ __global__ __launch_bounds__(256) void skinny_fwd_kernel(const int8_t *__restric
                 buf + col * CHUNK + (piece ^ col) * 16);
             acc = __builtin_amdgcn_mfma_i32_16x16x64_i8(av[t], bv, acc, 0, 0, 0);
         }
-        // Every wave has read this buffer (its MFMAs consumed the reads)
-        // before the loads of chunk kc + 2 refill it; no fence, so the loads
-        // of chunk kc + 1 stay in flight.
+        // Every wave has read this buffer (the wait: the compiler moves MFMAs
+        // and their reads' waits past the barrier) before the loads of chunk
+        // kc + 2 refill it; no fence, so the loads of chunk kc + 1 stay in
+        // flight.
+        wait_lgkmcnt0();
         barrier_no_fence();
     }
     i32x4 *red = reinterpret_cast<i32x4 *>(smem + 2 * kBuf);
