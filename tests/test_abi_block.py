@@ -68,6 +68,15 @@ def test_forward_needs_its_workspace(L):     # noqa: F811
         assert L.qlin_fwd_gated_ws_bytes(600, bad, 64) == 0
 
 
+def test_calls_that_split_nothing_need_no_workspace(L):      # noqa: F811
+    for M, N, K in ((1, 28672, 4096), (16, 4096, 14336), (64, 28672, 4096), (128, 4096, 14336), (512, 2048, 5376),
+                    (0, 64, 64)):
+        assert L.qlin_fwd_act_ws_bytes(M, N, K) == 0 and L.qlin_fwd_gated_ws_bytes(M, N // 2, K) == 0
+    _cpu_only()
+    none = dict(ws=None, ws_bytes=0)
+    assert L.qlin_fwd_act(*_act(M=600, N=7168, K=5376, **none)) == 1
+
+
 def _bwd(**kw):
     a = dict(dy=A[0], dy_dtype=0, ck=A[1], ck_s=A[2], act=2, gated=1, sw=A[3], sx=A[4], M=20, F=64, dz=A[5],
              dz_dtype=1, s1=A[6], s2=A[7], db=A[8], ws=A[9], ws_bytes=1 << 31)

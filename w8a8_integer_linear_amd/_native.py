@@ -733,14 +733,20 @@ def _act_code(act):
     return code
 
 
-def _scratch(workspace, need, like, zero):
-    """The workspace: the caller's, a fresh one, or None where none is needed."""
-    if workspace is not None or not isinstance(like, torch.Tensor) or not like.is_cuda:
-        return workspace
+COUNTER_BYTES = 4096        # arrival counters at the start of a product's workspace
+
+
+def _scratch(need, like, counters):
+    """A fresh workspace, its counters zero, or None where none is needed."""
+    if not isinstance(like, torch.Tensor) or not like.is_cuda:
+        return None
     n = need()
     if not n:
         return None
-    return (torch.zeros if zero else torch.empty)(n, dtype=torch.uint8, device=like.device)
+    workspace = torch.empty(n, dtype=torch.uint8, device=like.device)
+    if counters:
+        workspace[:COUNTER_BYTES].zero_()
+    return workspace
 
 
 @functools.lru_cache(maxsize=1024)
@@ -759,7 +765,7 @@ def qlin_fwd_act(qx, sx, qw, sw, bias=None, act="none", residual=None, y=None, d
     compiled, f = _compiled("qlin_fwd_act")
     code = _act_code(act)
     if workspace is None:
-        workspace = _scratch(None, lambda: qlin_fwd_act_ws_bytes(qx.shape[0], qw.shape[0], qx.shape[1]), qx, True)
+        workspace = _scratch(lambda: qlin_fwd_act_ws_bytes(qx.shape[0], qw.shape[0], qx.shape[1]), qx, True)
     return compiled.forward(f, False, qx, sx, qw, sw, bias, code, residual, y, dtype, ck, ck_s, save, workspace,
                             _handle(qx))
 
@@ -779,7 +785,7 @@ def qlin_fwd_gated(qx, sx, qw, sw, bias=None, act="silu", y=None, dtype=torch.bf
     compiled, f = _compiled("qlin_fwd_gated")
     code = _act_code(act)
     if workspace is None:
-        workspace = _scratch(None, lambda: qlin_fwd_gated_ws_bytes(qx.shape[0], qw.shape[0] // 2, qx.shape[1]), qx,
+        workspace = _scratch(lambda: qlin_fwd_gated_ws_bytes(qx.shape[0], qw.shape[0] // 2, qx.shape[1]), qx,
                              True)
     return compiled.forward(f, True, qx, sx, qw, sw, bias, code, None, y, dtype, ck, ck_s, save, workspace,
                             _handle(qx))
@@ -802,7 +808,7 @@ def qlin_act_bwd(dy, ck, ck_s, act, gated=False, sw=None, sx=None, dz=None, dtyp
     compiled, f = _compiled("qlin_act_bwd")
     code = _act_code(act)
     if workspace is None:
-        workspace = _scratch(None, lambda: qlin_act_bwd_ws_bytes(dy.shape[0], dy.shape[1], bool(gated)), dy, False)
+        workspace = _scratch(lambda: qlin_act_bwd_ws_bytes(dy.shape[0], dy.shape[1], bool(gated)), dy, False)
     return compiled.backward(f, dy, ck, ck_s, code, gated, sw, sx, dz, dtype, s1, s2, db, want_db, workspace,
                              _handle(dy))
 

@@ -30,8 +30,6 @@
 
 namespace qlin {
 
-constexpr int kActs = 5;        // QLIN_ACT_NONE .. QLIN_ACT_GELU_TANH
-
 constexpr float kLog2e = 1.44269504f;
 
 __device__ __forceinline__ float exp2_hw(float x) { return __builtin_amdgcn_exp2f(x); }

@@ -18,7 +18,9 @@ int64_t ck_scales(int64_t F, bool gated)
 
 size_t fwd_ws_bytes(int64_t M, int64_t N, int64_t K)
 {
-    return K > QLIN_MAX_CONTRACTION ? 0 : qlin_product_ws_bytes(QLIN_OP_FWD, M, N, K);
+    if (M < 0 || N < 0 || K < 0 || M > kMaxRows || N > kMaxRows || K > QLIN_MAX_CONTRACTION)
+        return 0;
+    return qlin::split_ws_bytes(qlin::act_split_plan(M, N, K));
 }
 
 // Both forward calls; N = 2 F with a gate.

@@ -17,16 +17,7 @@ template <int EPI> void run_tiles(const ProductArgs &a, const ActEpilogue &e, hi
     p.tiles_j = (int)((a.N + 255) / 256);       // (with a gate, 128 outputs per tile)
     const int tiles = p.tiles_i * p.tiles_j;
     const dim3 block(8 * kWave);
-    // The last round's tiles are split along the contraction where that saves more than
-    // their partial sums cost, which grows with the tiles (all of them write theirs at
-    // once).  us split / whole, bf16 with GELU, by tiles and contraction:
-    //               2048          4096          8192
-    //     32     63.2 / 65.3   92.6 / 106
-    //     64     32.1 / 31.2   41.1 / 48.3   58.8 / 82.4
-    //    112     39.9 / 33.0   48.4 / 49.2   70.5 / 83.4
-    //    128     41.9 / 34.2   53.0 / 50.7   76.8 / 85.3
-    const bool split = p.split >= 2 && 10 * ((p.T + 127) / 128) > 3 * (tiles - p.full);
-    if (split)
+    if (p.split >= 2 && act_split_plan(a.M, a.N, a.K).split >= 2)
         hipLaunchKernelGGL((gemm_kernel<2, 4, false, false, EPI, MODE_SPLIT>),
                            dim3((unsigned)(p.full + (tiles - p.full) * p.split)), block, 0, st, p);
     else
@@ -198,6 +189,26 @@ template <int ACT> void run(const ProductArgs &a, const ActEpilogue &e, hipStrea
 }
 
 } // namespace
+
+// The last round's tiles are split along the contraction where that saves more than
+// their partial sums cost, which grows with the tiles (all of them write theirs at
+// once).  us split / whole, bf16 with GELU, by tiles and contraction:
+//               2048          4096          8192
+//     32     63.2 / 65.3   92.6 / 106
+//     64     32.1 / 31.2   41.1 / 48.3   58.8 / 82.4
+//    112     39.9 / 33.0   48.4 / 49.2   70.5 / 83.4
+//    128     41.9 / 34.2   53.0 / 50.7   76.8 / 85.3
+SplitPlan act_split_plan(int64_t M, int64_t N, int64_t K)
+{
+    const SplitPlan none{0, 0, 1};
+    ProductArgs a{};
+    a.M = M;
+    a.N = N;
+    if (M <= 16 || product_act_few(a))
+        return none;
+    const SplitPlan sp = split_plan(0, M, N, K);
+    return 10 * ((K + 127) / 128) > 3 * (int64_t)sp.tail ? sp : none;
+}
 
 void launch_product_act(const ProductArgs &a, const ActEpilogue &e, hipStream_t st)
 {

@@ -140,6 +140,8 @@ struct SplitPlan {
 };
 constexpr size_t kSplitCountBytes = 4096;
 SplitPlan split_plan(int op, int64_t M, int64_t N, int64_t K);
+// Of launch_product_act's calls (gemm_act.hip).
+SplitPlan act_split_plan(int64_t M, int64_t N, int64_t K);
 // Workspace bytes the plan needs (0 when it splits nothing).
 size_t split_ws_bytes(const SplitPlan &sp);
 // Zero n 32-bit words at p on the stream (a kernel, so graph capture holds
