@@ -353,6 +353,35 @@ def test_other_stream_and_replayed_graph(gated):
         assert all(torch.equal(a, b) for a, b in zip(eager, held)), k
 
 
+def test_two_graphs_share_a_workspace():
+    """Replays in turn on one stream, eager calls with it between them."""
+    torch = torch_cuda()
+    import w8a8_integer_linear_amd as qlin
+    M, N, K = 600, 8160, 4112
+    ops = _operands(torch, M, N, K, 5)
+    need = max(qlin.qlin_fwd_act_ws_bytes(M, N, K), qlin.qlin_fwd_gated_ws_bytes(M, N // 2, K))
+    assert need
+    ws = torch.zeros(need, dtype=torch.uint8, device="cuda")
+    calls = [lambda: qlin.qlin_fwd_act(*ops[:4], bias=ops[4], act="gelu", workspace=ws)[0],
+             lambda: qlin.qlin_fwd_gated(*ops[:4], bias=ops[4], act="silu", workspace=ws)[0]]
+    want = [f() for f in calls]
+    torch.cuda.synchronize()
+    announce("two graphs, one workspace")
+    graphs, held = [], []
+    for f in calls:
+        graphs.append(torch.cuda.CUDAGraph())
+        with torch.cuda.graph(graphs[-1]):
+            held.append(f())
+    for k in range(4):
+        for h in held:
+            h.zero_()
+        for g in graphs if k % 2 else graphs[::-1]:
+            g.replay()
+        again = calls[k % 2]()
+        torch.cuda.synchronize()
+        assert torch.equal(again, want[k % 2]) and all(torch.equal(h, w) for h, w in zip(held, want)), k
+
+
 def test_two_streams_at_once():
     """Calls with workspaces of their own do not share anything."""
     torch = torch_cuda()

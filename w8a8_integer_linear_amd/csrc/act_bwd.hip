@@ -194,11 +194,12 @@ __global__ __launch_bounds__(256) void act_bwd_kernel(Args p)
 }
 
 // Partials -> s1, s2 and db.  A workgroup owns 64 columns, or, past the first
-// ceil(N / 64) workgroups, 64 rows: its 16 waves take every 16th row group (window) and
+// ceil(N / 64) workgroups, 64 of the launch's rows: its 16 waves take every 16th row group (window) and
 // are combined through LDS in a fixed order.
 __global__ __launch_bounds__(1024) void act_bwd_scales_kernel(const float *__restrict__ rowpart, int wins,
                                                               const float *__restrict__ colpart, int groups,
-                                                              int64_t M, int64_t N, float *__restrict__ s1,
+                                                              int64_t M, int64_t nrows, int64_t N,
+                                                              float *__restrict__ s1,
                                                               float *__restrict__ s2, float *__restrict__ db)
 {
     __shared__ float red_max[16][64], red_sum[16][64];
@@ -208,7 +209,7 @@ __global__ __launch_bounds__(1024) void act_bwd_scales_kernel(const float *__res
     const int64_t c = ((int64_t)blockIdx.x - (rows ? cblocks : 0)) * 64 + lc;
     float m = 0.0f, sum = 0.0f;
     if (rows) {
-        if (c < M) {
+        if (c < nrows) {
 #pragma unroll 4
             for (int k = sl; k < wins; k += 16)
                 m = max_nan(m, rowpart[k * M + c]);
@@ -223,7 +224,7 @@ __global__ __launch_bounds__(1024) void act_bwd_scales_kernel(const float *__res
     red_max[sl][lc] = m;
     red_sum[sl][lc] = sum;
     __syncthreads();
-    if (sl != 0 || c >= (rows ? M : N))
+    if (sl != 0 || c >= (rows ? nrows : N))
         return;
 #pragma unroll
     for (int i = 1; i < 16; i++) {
@@ -297,11 +298,19 @@ void launch_act_bwd(const ActBackward &a, void *ws, hipStream_t st)
         default: with_act(std::integral_constant<int, QLIN_ACT_GELU_TANH>()); break;
         }
     }
-    // (s1 and its workgroups only where it is asked for.)
-    const unsigned blocks = (unsigned)((p.N + 63) / 64 + (a.s1 ? (a.M + 63) / 64 : 0));
-    if (a.s1 || a.s2 || a.db)
-        hipLaunchKernelGGL(act_bwd_scales_kernel, dim3(blocks), dim3(1024), 0, st, p.rowpart, (int)sh.wins,
-                           p.colpart, (int)sh.groups, a.M, p.N, a.s1, a.s2, a.db);
+    // (s1 and its workgroups only where it is asked for.  A launch holds fewer than 2^32
+    // threads: more rows than 2^27 take another, without columns.)
+    if (!a.s1 && !a.s2 && !a.db)
+        return;
+    constexpr int64_t kRows = (int64_t)1 << 27;
+    int64_t row = 0;
+    do {
+        const int64_t left = a.s1 ? a.M - row : 0, n = left < kRows ? left : kRows, cols = row ? 0 : p.N;
+        hipLaunchKernelGGL(act_bwd_scales_kernel, dim3((unsigned)((cols + 63) / 64 + (n + 63) / 64)), dim3(1024), 0,
+                           st, p.rowpart + row, (int)sh.wins, p.colpart, (int)sh.groups, a.M, n, cols,
+                           a.s1 ? a.s1 + row : nullptr, a.s2, a.db);
+        row += kRows;
+    } while (a.s1 && row < a.M);
 }
 
 } // namespace qlin
