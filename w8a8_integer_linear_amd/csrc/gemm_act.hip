@@ -194,10 +194,10 @@ template <int ACT> void run(const ProductArgs &a, const ActEpilogue &e, hipStrea
 // their partial sums cost, which grows with the tiles (all of them write theirs at
 // once).  us split / whole, bf16 with GELU, by tiles and contraction:
 //               2048          4096          8192
-//     32     63.2 / 65.3   92.6 / 106
-//     64     32.1 / 31.2   41.1 / 48.3   58.8 / 82.4
-//    112     39.9 / 33.0   48.4 / 49.2   70.5 / 83.4
-//    128     41.9 / 34.2   53.0 / 50.7   76.8 / 85.3
+//     32     59.6 / 61.2  85.4 / 97.2
+//     64     31.3 / 30.0  39.6 / 45.3   57.4 / 75.8
+//    112     38.1 / 31.0  46.7 / 45.8   65.6 / 75.9
+//    128     41.4 / 32.7  51.0 / 48.3   71.5 / 77.1
 SplitPlan act_split_plan(int64_t M, int64_t N, int64_t K)
 {
     const SplitPlan none{0, 0, 1};

@@ -888,11 +888,13 @@ __device__ __forceinline__ void act_epilogue(const GemmParams &p, const i32x4 (&
     // lanes' offsets, kOob past the last column, move on by a constant per step, below
     // 2^30 in all, and hold all of an access's offset.
     const int rows = p.R - i < 128 ? p.R - i : 128;
+    if (rows <= 0)
+        return;
     // An array whose rows hold n elements of size bytes, from element c.  (A wave whose
-    // rows or columns all lie past the last has rows <= 0 or j >= F.)
+    // columns all lie past the last has j >= F.)
     auto rows_of = [&](const void *base, uint32_t n, uint32_t c, int size) {
         return make_rsrc(static_cast<const int8_t *>(base) + ((int64_t)i * n + c) * size,
-                         rows > 0 && j < F ? ((uint32_t)rows * n - c) * size : 0);
+                         j < F ? ((uint32_t)rows * n - c) * size : 0);
     };
     const uint32_t n = H * (uint32_t)F, per = (uint32_t)(F + kCkBlock - 1) / kCkBlock, all = H * per;
     const int y_size = e.y_bf16 ? 2 : 4, r_size = e.res_bf16 ? 2 : 4;
@@ -1077,13 +1079,19 @@ __global__ __launch_bounds__(WM *WN * 64, 1) void gemm_kernel(GemmParams p)
     // the stage after next, behind the last row block's pairs, into the
     // buffers whose reads have just passed the stage barrier: a whole stage
     // to land (dW 4-5% and dX 3% faster; lead 2 for contiguous operands made
-    // the forward 2% slower).  In a feed-forward block, whose batches are of any
-    // size, the weight has lead 2: fewer tiles share it and more of it comes from
-    // HBM (us, lead 1 / 2: 611 x 4096 -> 2 x 14336 96.5 / 93.2, 2048 x 5376 -> 2 x 7168
-    // 156 / 145, 8192 x 14336 -> 4096 376 / 351, 8192 x 4096 -> 2 x 14336 777 / 736; but
-    // 12000 x 5376 -> 7168 376 / 380).
+    // the forward 2% slower).  In a feed-forward block (kDeep),
+    // where fewer tiles may share the weight and more of it comes from HBM, its
+    // loads are also for the stage after next, behind the pairs of row blocks 2-3,
+    // and into a third buffer, whose reads passed the barrier before: they have
+    // more than a stage and a half to land (us, two buffers
+    // with lead 2 behind the last row block / three: 8192 x 4096 -> 2 x 14336 735 /
+    // 700, 2048 x 5376 -> 2 x 7168 151 / 141, 3700 x 5376 -> 7168 138 / 132, 8192 x
+    // 14336 -> 4096 355 / 345, 611 x 4096 -> 2 x 14336 94 / 90; with lead 1 777, 156,
+    // -, 376, 97.  Activations with lead 2 too: 749, 144, 137, 360, 90).
     constexpr int kSpread = 8;
-    constexpr int kLeadA = AKM ? 2 : 1, kLeadB = BKM || EPI >= EPI_ACT ? 2 : 1;
+    constexpr bool kDeep = EPI >= EPI_ACT;
+    constexpr int kLeadA = AKM ? 2 : 1, kLeadB = BKM || kDeep ? 2 : 1;
+    constexpr int kBufsB = kDeep ? 3 : 2;
     static_assert(NK == 2 && FM % 2 == 0 && kSpread <= FN * (FM - 1) && kSpread % FN == 0,
                   "fragment schedule shape");
     using OpA = Operand<BM, AKM, NT, kBK>;
@@ -1102,7 +1110,7 @@ __global__ __launch_bounds__(WM *WN * 64, 1) void gemm_kernel(GemmParams p)
         return i < a ? i : OpA::kLoads + (i - a);
     };
     constexpr int cA = OpA::kReads, cB = OpB::kReads;
-    __shared__ __attribute__((aligned(1024))) int8_t smem[2 * kStage];
+    __shared__ __attribute__((aligned(1024))) int8_t smem[2 * OpA::kBytes + kBufsB * OpB::kBytes];
 
     const WorkUnit u = work_unit<MODE>(p, kBK);
     const int kb = u.kb, KT = u.KT;
@@ -1133,23 +1141,22 @@ __global__ __launch_bounds__(WM *WN * 64, 1) void gemm_kernel(GemmParams p)
     for (int q = 0; q < OpB::kLoads; q++)
         voffB[q] = kGated ? gated_offset<OpB>(q, wu, p.ldb, blim) : OpB::lane_offset(q, wu, p.ldb, blim);
     // LDS holds the operands' stages operand by operand: A's two stages, then
-    // B's, so that a stage's offset fits the LDS reads' immediate and the
+    // B's two or three, so that a stage's offset fits the LDS reads' immediate and the
     // unrolled loop below addresses either stage with constants.
-    // Part G of stage s's buffer-to-LDS loads (planned in L), into buffers
-    // s % 2.
-    constexpr bool kFree = EPI >= EPI_ACT;
-    using Loads = StageLoads<OpA, OpB, AKM, BKM, kBK, kFree>;
+    // Part G of a stage's buffer-to-LDS loads (planned in L), into the operands'
+    // buffers bufA and bufB: those of stage s are s % 2 and s % kBufsB.
+    using Loads = StageLoads<OpA, OpB, AKM, BKM, kBK, kDeep>;
     // (Bytes to B's end, as far as 32-bit offsets and the longest row matter.)
     uint32_t bleft = 0;
-    if constexpr (kFree) {
+    if constexpr (kDeep) {
         const int64_t rows = (kGated ? 2 : 1) * (int64_t)p.S - j0 - (kGated && wu >= 4 ? p.act.F : 0);
         const int64_t left = rows * p.ldb;
         bleft = left < (int64_t)kOob + (1 << 18) ? (uint32_t)left : kOob + (1 << 18);
     }
-    auto issue = [&](const Loads &L, int s, auto G) {
+    auto issue = [&](const Loads &L, int bufA, int bufB, auto G) {
         constexpr int g = decltype(G)::value, per = kLoads / kSpread;
-        L.template issue<g * per, (g + 1) * per>(voffA, voffB, wu, smem + (s & 1) * OpA::kBytes,
-                                                 smem + 2 * OpA::kBytes + (s & 1) * OpB::kBytes);
+        L.template issue<g * per, (g + 1) * per>(voffA, voffB, wu, smem + bufA * OpA::kBytes,
+                                                 smem + 2 * OpA::kBytes + bufB * OpB::kBytes);
     };
 
     // Lane offsets of this wave's fragments inside a stage: per step for a
@@ -1188,11 +1195,13 @@ __global__ __launch_bounds__(WM *WN * 64, 1) void gemm_kernel(GemmParams p)
     };
     auto read_b = [&](auto P, auto KK, auto Bi) {
         constexpr int kk = decltype(KK)::value, b = decltype(Bi)::value;
-        constexpr int st = decltype(P)::value * OpB::kBytes;
+        constexpr int st = decltype(P)::value % 2 * OpB::kBytes;
+        // (A third buffer is past the immediate's reach.)
+        const uint32_t base = lds0 + decltype(P)::value / 2 * 2 * OpB::kBytes;
         if constexpr (BKM)
-            OpB::template frag<st + kk * OpB::kStep>(lds0 + offB[b], fb[kk][b]);
+            OpB::template frag<st + kk * OpB::kStep>(base + offB[b], fb[kk][b]);
         else
-            OpB::template frag<st + b * OpB::kBlock>(lds0 + offB[kk], fb[kk][b]);
+            OpB::template frag<st + b * OpB::kBlock>(base + offB[kk], fb[kk][b]);
     };
     auto read_b_pair = [&](auto P, auto Bi) {
         static_for<NK>([&](auto KK) { read_b(P, KK, Bi); });
@@ -1207,7 +1216,6 @@ __global__ __launch_bounds__(WM *WN * 64, 1) void gemm_kernel(GemmParams p)
                 OpB::value(fb[kk][b]), OpA::value(fa[sl][kk]), acc[f][b], 0, 0, 0);
     };
     using Zero = std::integral_constant<int, 0>;
-    using One = std::integral_constant<int, 1>;
     // Reads of a stage's head: row block 0, then the column blocks' pairs.
     auto head = [&](auto P) {
         read_a(P, Zero{});
@@ -1226,9 +1234,12 @@ __global__ __launch_bounds__(WM *WN * 64, 1) void gemm_kernel(GemmParams p)
     // MFMA pair on that block has just used (an MFMA reads its A and B
     // operands when it issues, and only its sums, C, are read later; the LDS
     // read writes its registers when it returns).  Buffer-to-LDS loads go
-    // out by their operand's lead (kLeadA, kLeadB).
-    auto stage = [&](int kt, auto P) {
-        constexpr int par = decltype(P)::value;
+    // out by their operand's lead (kLeadA, kLeadB).  S is kt's remainder: the
+    // stage's buffers are S % 2 and S % kBufsB.
+    auto stage = [&](int kt, auto S) {
+        constexpr int par = decltype(S)::value % 2, bufB = decltype(S)::value % kBufsB;
+        constexpr std::integral_constant<int, par> P;
+        constexpr std::integral_constant<int, (bufB + 1) % kBufsB> NextB;
         const Loads L1 = Loads::plan(p, abase, bbase, kb, KT, kt + 1, bleft);
         const Loads L2 = Loads::plan(p, abase, bbase, kb, KT, kt + 2, bleft);
         static_for<FM - 1>([&](auto F) {
@@ -1256,7 +1267,13 @@ __global__ __launch_bounds__(WM *WN * 64, 1) void gemm_kernel(GemmParams p)
                 }
                 constexpr int slot = FN * f + b, every = 2 * FN / (n1 ? n1 : 2 * FN);
                 if constexpr (n1 > 0 && slot < 2 * FN && slot % every == 0) {
-                    issue(L1, kt + 1, std::integral_constant<int, part_of(1, slot / every)>{});
+                    issue(L1, 1 - par, 1 - par, std::integral_constant<int, part_of(1, slot / every)>{});
+                    mfma_pair(F, Bi);
+                    __builtin_amdgcn_sched_group_barrier(0x008, NK, 0);
+                    __builtin_amdgcn_sched_group_barrier(0x020, kLoads / kSpread, 0);
+                } else if constexpr (kDeep && slot >= 2 * FN && slot < 4 * FN && slot % 2 == 0) {
+                    issue(L2, par, (bufB + 2) % kBufsB,
+                          std::integral_constant<int, part_of(2, slot / 2 - FN)>{});
                     mfma_pair(F, Bi);
                     __builtin_amdgcn_sched_group_barrier(0x008, NK, 0);
                     __builtin_amdgcn_sched_group_barrier(0x020, kLoads / kSpread, 0);
@@ -1266,8 +1283,9 @@ __global__ __launch_bounds__(WM *WN * 64, 1) void gemm_kernel(GemmParams p)
                 __builtin_amdgcn_sched_barrier(0);
             });
         });
-        // Stage kt + 1 has landed (its loads were the only ones in flight).
-        wait_vmcnt<0>();
+        // Stage kt + 1 has landed (its loads were the only ones in flight, or the
+        // weight's of stage kt + 2 were issued behind them).
+        wait_vmcnt<kDeep ? n2 : 0>();
         wait_lgkmcnt<0>();
 #pragma unroll
         for (int kk = 0; kk < NK; kk++)
@@ -1281,29 +1299,52 @@ __global__ __launch_bounds__(WM *WN * 64, 1) void gemm_kernel(GemmParams p)
             constexpr int b = decltype(Bi)::value;
             mfma_pair(std::integral_constant<int, FM - 1>{}, Bi);
             __builtin_amdgcn_sched_barrier(0);
-            read_b_pair(std::integral_constant<int, 1 - par>{}, Bi);
-            static_for<n2 / FN>([&](auto G) {
-                issue(L2, kt + 2,
-                      std::integral_constant<int, part_of(2, b * (n2 / FN) + decltype(G)::value)>{});
-            });
+            read_b_pair(NextB, Bi);
+            if constexpr (!kDeep)
+                static_for<n2 / FN>([&](auto G) {
+                    issue(L2, par, bufB,
+                          std::integral_constant<int, part_of(2, b * (n2 / FN) + decltype(G)::value)>{});
+                });
             __builtin_amdgcn_sched_barrier(0);
         });
     };
     {
         const Loads L0 = Loads::plan(p, abase, bbase, kb, KT, 0, bleft);
-        static_for<kSpread>([&](auto G) { issue(L0, 0, G); });
+        static_for<kSpread>([&](auto G) { issue(L0, 0, 0, G); });
         const Loads L1 = Loads::plan(p, abase, bbase, kb, KT, 1, bleft);
         static_for<n2>([&](auto G) {
-            issue(L1, 1, std::integral_constant<int, part_of(2, decltype(G)::value)>{});
+            issue(L1, 1, 1, std::integral_constant<int, part_of(2, decltype(G)::value)>{});
         });
     }
     wait_vmcnt<n2>();       // stage 0 landed
     barrier_no_fence();
-    head(Zero{});
-    for (int kt = 0; kt < KT; kt += 2) {
-        stage(kt, Zero{});
-        if (kt + 1 < KT)
-            stage(kt + 1, One{});
+    // Of a tile whose last rows are past the output, the waves whose rows all are only
+    // load, and leave their SIMD to those it also has of the others (us, without / with,
+    // 4096 -> 2 x 14336: 100 rows 47.6 / 42.8, 611 91.1 / 88.7, 1100 134.8 / 132.8).
+    if (kDeep && i0 + __builtin_amdgcn_readfirstlane(wi) * RW >= p.R) {
+        int bufB = 2;               // of stage kt + 2
+        for (int kt = 0; kt < KT; kt++) {
+            const Loads L1 = Loads::plan(p, abase, bbase, kb, KT, kt + 1, bleft);
+            const Loads L2 = Loads::plan(p, abase, bbase, kb, KT, kt + 2, bleft);
+            static_for<n1>([&](auto G) {
+                issue(L1, 1 - kt % 2, 0, std::integral_constant<int, part_of(1, decltype(G)::value)>{});
+            });
+            static_for<n2>([&](auto G) {
+                issue(L2, 0, bufB, std::integral_constant<int, part_of(2, decltype(G)::value)>{});
+            });
+            wait_vmcnt<kDeep ? n2 : 0>();
+            barrier_no_fence();
+            bufB = bufB == 2 ? 0 : bufB + 1;
+        }
+    } else {
+        head(Zero{});
+        // (Unrolled over the buffers of both operands.)
+        constexpr int kUnroll = kBufsB == 3 ? 6 : 2;
+        for (int kt = 0; kt < KT; kt += kUnroll)
+            static_for<kUnroll>([&](auto S) {
+                if (decltype(S)::value == 0 || kt + decltype(S)::value < KT)
+                    stage(kt + decltype(S)::value, S);
+            });
     }
     // The last stage has issued the next stage's fragment reads (never used)
     // and zero-fill loads into the stage buffers.  Wait for the reads and keep
