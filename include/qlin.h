@@ -55,6 +55,10 @@
  *    projection" are deterministic too, but use fused multiply-adds and bf16
  *    matrix instructions with fp32 sums (fp32 operands as three bf16 terms);
  *    each states its own precision.
+ *    Those inside a feed-forward block are deterministic, and exact where they
+ *    say so: the sums before an activation, checkpoints and codes; activations
+ *    and derivatives use fused multiply-adds and the hardware's exponential
+ *    and reciprocal (csrc/act.hpp states their errors).
  */
 #ifndef QLIN_H
 #define QLIN_H
