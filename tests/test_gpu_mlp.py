@@ -112,6 +112,53 @@ def test_passes_kept_apart_and_updates():
     assert block.backward(dy[:1].contiguous()).shape == (1, 256)
 
 
+def test_no_tokens():
+    torch = torch_cuda()
+    announce("mlp: no tokens")
+    block, x, res, dy = _block(torch, 5, 128, 256, 128, True, "silu", torch.bfloat16)
+    block.forward(x), block.backward(dy)
+    y = block.forward(x[:0], residual=res[:0])
+    dx = block.backward(dy[:0])
+    assert y.shape == (0, 128) and y.dtype == torch.bfloat16 and dx.shape == (0, 128)
+    for fc in (block.fc1, block.fc2):
+        assert (fc.dw == 0).all() and (fc.db == 0).all()
+
+
+def test_without_biases():
+    """The same as with biases of zeros."""
+    torch = torch_cuda()
+    import w8a8_integer_linear_amd as qlin
+    announce("mlp: no biases")
+    g = torch.Generator().manual_seed(8)
+    w1, w2, x, dy = (torch.randn(s, generator=g).cuda() for s in ((512, 128), (128, 256), (70, 128), (70, 128)))
+    kw = dict(act="gelu", gated=True, dtype=torch.float32)
+    plain = qlin.MLPW8A8Training(w1, w2, **kw)
+    zeros = qlin.MLPW8A8Training(w1, w2, torch.zeros(512, device="cuda"), torch.zeros(128, device="cuda"), **kw)
+    assert torch.equal(plain.forward(x), zeros.forward(x))
+    assert torch.equal(plain.backward(dy), zeros.backward(dy))
+    assert torch.equal(plain.fc1.dw, zeros.fc1.dw) and torch.equal(plain.fc2.dw, zeros.fc2.dw)
+    plain.sgd_step(0.1, 3, 1), zeros.sgd_step(0.1, 3, 1)
+    assert torch.equal(plain.fc1.qw, zeros.fc1.qw) and torch.equal(plain.fc2.qw, zeros.fc2.qw)
+
+
+def test_two_streams_at_once():
+    """Passes of one block on streams of their own: each has its workspace."""
+    torch = torch_cuda()
+    announce("mlp: two streams")
+    block, x, res, _ = _block(torch, 600, 4096, 4096, 256, True, "silu", torch.bfloat16)
+    inputs = [x, torch.flip(x, (0,)).contiguous()]
+    want = [block.forward(v, save=False) for v in inputs]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in inputs]
+    for _ in range(4):
+        got = []
+        for s, v in zip(streams, inputs):
+            with torch.cuda.stream(s):
+                got.append(block.forward(v, save=False))
+        torch.cuda.synchronize()
+        assert all(torch.equal(a, b) for a, b in zip(got, want))
+
+
 def test_block_in_a_graph():
     torch = torch_cuda()
     announce("mlp in a graph")
