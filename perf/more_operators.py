@@ -161,7 +161,6 @@ def prepare(case, seed):
         z = _randn((M, N), g, 1.5)
         z[:, torch.randperm(N, generator=g, device=dev)[:N // 100]] *= 4.0
         s["ck"], s["ck_s"] = _checkpoint(z, F)
-        s["ck"] = s["ck"].contiguous()      # (a view where F ends inside a block)
     s["sx"][M - pad:] = 0
     if c["op"] in ("act_bwd", "train"):
         s["dy"] = _randn((M, F), g, 0.01)
