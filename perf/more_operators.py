@@ -286,9 +286,10 @@ def run(s):
                                             **given)
         out = [y]
     if op in ("act_bwd", "train"):
-        out += qlin.qlin_act_bwd(s["dy"], ck, ck_s, s["act"], gated=gated, sw=s["sw"], sx=s["sx"],
-                                 dz=s["out_dz"], s1=s["out_s1"], s2=s["out_s2"], db=s["out_db"],
-                                 workspace=s["bwd_ws"])
+        # (The prepared codes are a view where an ungated width ends inside a block.)
+        out += qlin.qlin_act_bwd(s["dy"], ck.contiguous(), ck_s, s["act"], gated=gated, sw=s["sw"],
+                                 sx=s["sx"], dz=s["out_dz"], s1=s["out_s1"], s2=s["out_s2"],
+                                 db=s["out_db"], workspace=s["bwd_ws"])
     return out
 
 
