@@ -109,7 +109,9 @@ __global__ __launch_bounds__(WAVES * kWave) void few_act_kernel(GemmParams p)
         cur = cur + 1 < NB ? cur + 1 : 0;
         fill = fill + 1 < NB ? fill + 1 : 0;
     }
+    // (No load still writes to LDS, and no wave still reads the last chunk from it.)
     wait_vmcnt<0>();
+    wait_lgkmcnt0();
     barrier_no_fence();
     int32_t *sums = reinterpret_cast<int32_t *>(smem);
     for (int k = threadIdx.x; k < kSums / 4; k += kThreads)
