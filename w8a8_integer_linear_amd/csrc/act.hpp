@@ -10,18 +10,19 @@
 // reciprocal (1 ulp each): a relative error of about 2^-22 plus 2^-24 |z| from
 // the rounded exponent, the latter where s(z) is small.
 //
-// Phi in two forms, both without a branch (the library's erf has two, of which a wave
-// takes both):
-//   normal_cdf, for the derivative, which needs e^(-z^2/2) beside it: Phi(-x), x >= 0,
-//   is that times a polynomial of degree 8 without a constant term in t = 1 / (1 +
-//   0.3 x); erfc's scaled form is smooth in t and falls like t for large x.  Relative
-//   error at most 1.3e-7 over 0 <= x <= 14, past which the exponential is below 2^-126.
-//   gelu_value, for the value alone: z Phi(z) = max(z, 0) - x Phi(-x), x = |z|, with
-//   Phi(-x) = 2^P(x), P of degree 7 (log2 of Phi is nearly a parabola).  x 2^P(x) is
-//   within 4.7e-8 for x <= 6, and taken at 6, where it is 5.9e-9, past that.  One
-//   transcendental instruction instead of two: 14 issue slots against 25, and the
-//   product's epilogue is bound by those (4000 x 4096 -> 14336 with it: 229 -> 219 us).
-// The coefficients are minimax fits (linear programming) of these errors.
+// Phi without a branch (the library's erf has two, of which a wave takes both): for x =
+// |z|, Phi(-x) is e^(-x^2/2) times a polynomial of degree 9 without a constant term in t =
+// 1 / (1 + 0.34 x); erfc's scaled form is smooth in t and falls like t for large x.  The
+// coefficients are a minimax fit (linear programming) of the relative error, each rounded
+// to fp32 before the next is fitted: 4.1e-8 over 0 <= x <= 13.2, past which the
+// exponential is below 2^-126 and may be flushed.  As computed in fp32, Phi(-x) is within
+// 4.5e-7 of itself for x <= 2, and within 2^-21 + 2^-24 x^2 further out, where the rounded
+// exponent is what counts (2.1e-6 at 6).
+//   z Phi(z) = max(z, 0) - x Phi(-x), with x = min(|z|, 20), where the exponential is 0.
+// Forward and backward take this one form.  (A polynomial P of degree 7 with Phi(-x) =
+// 2^P(x) has one transcendental instruction instead of two, 14 issue slots against 24, but
+// only an absolute error: 5% of the value at -6, a constant below.  us, that / this: 4000 x
+// 4096 -> 14336 with checkpoint and backward 326 / 337, 777 x 4096 -> 14336 59.7 / 61.3.)
 #pragma once
 
 #include <hip/hip_runtime.h>
@@ -38,36 +39,29 @@ __device__ __forceinline__ float rcp_hw(float x) { return __builtin_amdgcn_rcpf(
 // s(z); 0 where the exponential overflows.
 __device__ __forceinline__ float logistic(float z) { return rcp_hw(1.0f + exp2_hw(z * -kLog2e)); }
 
-// Phi(z), and e^(-z^2/2).
-__device__ __forceinline__ float normal_cdf(float z, float &gauss)
+// Phi(-x) and e^(-x^2/2), x >= 0.
+__device__ __forceinline__ float normal_tail(float x, float &gauss)
 {
-    const float x = __builtin_fabsf(z);
-    const float t = rcp_hw(__builtin_fmaf(x, 0.3f, 1.0f));
-    gauss = exp2_hw(z * z * (-0.5f * kLog2e));
-    float q = 0.03556719721f;
-    q = __builtin_fmaf(q, t, -0.156760921f);
-    q = __builtin_fmaf(q, t, 0.2056028133f);
-    q = __builtin_fmaf(q, t, -0.05300297223f);
-    q = __builtin_fmaf(q, t, 0.1282069439f);
-    q = __builtin_fmaf(q, t, 0.1000190791f);
-    q = __builtin_fmaf(q, t, 0.1207374586f);
-    q = __builtin_fmaf(q, t, 0.1196303368f);
-    q = q * t * gauss;
-    return z < 0.0f ? q : 1.0f - q;
+    const float t = rcp_hw(__builtin_fmaf(x, 0.34f, 1.0f));
+    gauss = exp2_hw(x * x * (-0.5f * kLog2e));
+    float q = -0.02649738826f;
+    q = __builtin_fmaf(q, t, 0.141270116f);
+    q = __builtin_fmaf(q, t, -0.2766533494f);
+    q = __builtin_fmaf(q, t, 0.2060405612f);
+    q = __builtin_fmaf(q, t, -0.04725845158f);
+    q = __builtin_fmaf(q, t, 0.1163846999f);
+    q = __builtin_fmaf(q, t, 0.1149504483f);
+    q = __builtin_fmaf(q, t, 0.1361446381f);
+    q = __builtin_fmaf(q, t, 0.1356187314f);
+    return q * t * gauss;
 }
 
-__device__ __forceinline__ float gelu_value(float z)
+// z Phi(z), and what its derivative needs: Phi(-x) and e^(-x^2/2).
+__device__ __forceinline__ float gelu(float z, float &tail, float &gauss)
 {
-    const float x = __builtin_elementwise_minimum(__builtin_fabsf(z), 6.0f);
-    float q = 3.304236914e-06f;
-    q = __builtin_fmaf(q, x, -4.404308744e-06f);
-    q = __builtin_fmaf(q, x, -0.0006028252271f);
-    q = __builtin_fmaf(q, x, 0.007711402484f);
-    q = __builtin_fmaf(q, x, -0.05297750938f);
-    q = __builtin_fmaf(q, x, -0.459034572f);
-    q = __builtin_fmaf(q, x, -1.151128862f);
-    q = __builtin_fmaf(q, x, -0.9999994886f);
-    return __builtin_fmaf(-x, exp2_hw(q), fmaxf(z, 0.0f));
+    const float x = __builtin_elementwise_minimum(__builtin_fabsf(z), 20.0f);
+    tail = normal_tail(x, gauss);
+    return __builtin_fmaf(-x, tail, fmaxf(z, 0.0f));
 }
 
 constexpr float kTanhRate = 1.5957691216f;      // 2 sqrt(2 / pi)
@@ -85,7 +79,8 @@ template <int ACT> __device__ __forceinline__ float act_value(float z)
     } else if constexpr (ACT == QLIN_ACT_SILU) {
         return z * logistic(z);
     } else if constexpr (ACT == QLIN_ACT_GELU) {
-        return gelu_value(z);
+        float tail, gauss;
+        return gelu(z, tail, gauss);
     } else if constexpr (ACT == QLIN_ACT_GELU_TANH) {
         return z * logistic(tanh_inner(z));
     } else {
@@ -104,10 +99,9 @@ template <int ACT> __device__ __forceinline__ void act_slope(float z, float &val
         value = z * s;
         slope = __builtin_fmaf(value, 1.0f - s, s);
     } else if constexpr (ACT == QLIN_ACT_GELU) {
-        float gauss;
-        const float cdf = normal_cdf(z, gauss);
-        value = z * cdf;
-        slope = __builtin_fmaf(z * 0.3989422804f, gauss, cdf);
+        float tail, gauss;
+        value = gelu(z, tail, gauss);
+        slope = __builtin_fmaf(z * 0.3989422804f, gauss, z < 0.0f ? tail : 1.0f - tail);
     } else if constexpr (ACT == QLIN_ACT_GELU_TANH) {
         const float s = logistic(tanh_inner(z));
         value = z * s;
