@@ -74,3 +74,29 @@ def test_gelu_values_of_the_backward_pass():
     want, err = _gelu(torch, z)
     off = (dz[:, F].double().cpu() - want).abs()
     assert (off <= err).all(), float((off / err).max())
+
+
+@pytest.mark.parametrize("act", ["none", "relu", "silu", "gelu", "gelu_tanh"])
+@pytest.mark.parametrize("gated", [False, True])
+def test_far_from_zero(act, gated):
+    """Where an activation has become z or 0, so has its derivative 1 or 0, up to the
+    largest z: also where z^2 is past fp32."""
+    torch = torch_cuda()
+    import w8a8_integer_linear_amd as qlin
+    announce("far from zero", act, gated)
+    z = torch.cat([s * 2.0 ** torch.arange(7.0, 127.0) for s in (-1.0, 1.0)])
+    M, F = len(z), 32
+    N = 2 * F if gated else F
+    ck = torch.ones((M, N), dtype=torch.int8)
+    ck[:, :F][z < 0] = -1
+    ck_s = torch.ones((M, N // 32))
+    ck_s[:, 0] = z.abs()
+    dz, s1, s2, db = qlin.qlin_act_bwd(torch.ones((M, F), device="cuda"), ck.cuda(), ck_s.cuda(), act, gated=gated,
+                                       sw=torch.ones(N, device="cuda"), sx=torch.ones(M, device="cuda"),
+                                       dtype=torch.float32, want_db=True)
+    on = torch.ones(M, dtype=torch.double) if act == "none" else (z > 0).double()
+    dz = dz.double().cpu()
+    assert ((dz[:, :F] - on[:, None]).abs() <= TINY).all()
+    if gated:
+        assert ((dz[:, F:] - (z.double() * on)[:, None]).abs() <= TINY).all()
+    assert s1.isfinite().all() and s2.isfinite().all() and db.isfinite().all()

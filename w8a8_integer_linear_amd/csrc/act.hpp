@@ -105,7 +105,8 @@ template <int ACT> __device__ __forceinline__ void act_slope(float z, float &val
     } else if constexpr (ACT == QLIN_ACT_GELU_TANH) {
         const float s = logistic(tanh_inner(z));
         value = z * s;
-        const float rate = __builtin_fmaf(z * z, 3.0f * kTanhRate * kTanhCube, kTanhRate);
+        // (A finite rate: z^2 passes fp32 at 2^64, where 1 - s or the value is 0.)
+        const float rate = __builtin_fmaf(fminf(z * z, 0x1p64f), 3.0f * kTanhRate * kTanhCube, kTanhRate);
         slope = __builtin_fmaf(value * (1.0f - s), rate, s);
     } else {
         value = z;
