@@ -100,3 +100,21 @@ def test_far_from_zero(act, gated):
     if gated:
         assert ((dz[:, F:] - (z.double() * on)[:, None]).abs() <= TINY).all()
     assert s1.isfinite().all() and s2.isfinite().all() and db.isfinite().all()
+
+
+def test_the_largest_checkpoint():
+    """z next to fp32's largest: its block's scale times 128 is past fp32."""
+    torch = torch_cuda()
+    import w8a8_integer_linear_amd as qlin
+    announce("largest checkpoint")
+    M, N, K = 3, 64, 64
+    b = torch.linspace(-1.0, 1.0, N)
+    b[:32] = 0.999 * torch.finfo(torch.float32).max
+    b[7] *= -1
+    zeros = torch.zeros((M, K), dtype=torch.int8, device="cuda"), torch.zeros(M, device="cuda")
+    w = torch.zeros((N, K), dtype=torch.int8, device="cuda"), torch.ones(N, device="cuda")
+    y, ck, ck_s = qlin.qlin_fwd_act(*zeros, *w, bias=b.cuda(), act="relu", dtype=torch.float32, save=True)
+    assert bool((ck_s[:, 0] >= 2.0 ** 121).all()) and torch.equal(y.cpu(), b.clamp(min=0).expand(M, N))
+    dy = torch.ones((M, N), device="cuda")
+    dz = qlin.qlin_act_bwd(dy, ck, ck_s, "relu", dtype=torch.float32)[0]
+    assert torch.equal(dz.cpu(), (b > 0).float().expand(M, N))
