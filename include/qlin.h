@@ -696,8 +696,9 @@ size_t qlin_act_bwd_ws_bytes(int64_t M, int64_t F, int gated);
  * The codes of qlin_quantize_grad for scales that are known (s1 and s2 of
  * qlin_act_bwd, or of another call on the same gradient):
  *   q1 = rne(fl(fl(dy sw[n]) / s1[m])),  q2 = rne(fl(fl(dy sx[m]) / s2[n])),
- * [M, N] int8 each.  The scales have to be at least |dy sw| / 127.499 and |dy sx| /
- * 127.499, which those of the fp32 values of a dy rounded to bf16 are.
+ * [M, N] int8 each, +-127 at most: a dy rounded to bf16 may exceed the fp32 values that
+ * its scales are from (by 2^-8 of itself; where it is subnormal by half).  A zero scale
+ * gives zero codes.
  */
 int qlin_quantize_grad_scaled(const void *dy, int dtype, int64_t M, int64_t N, const float *sw,
                               const float *sx, const float *s1, const float *s2, int8_t *q1,

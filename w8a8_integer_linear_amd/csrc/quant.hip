@@ -621,9 +621,11 @@ __device__ __forceinline__ i32x2 quant8_each(const float g[8], const float s[8],
 // reciprocals stay in registers) and walks kCodeRows rows, writing the row
 // codes rne(fl(fl(dY * sw) / s1[r])) to q1 and the column codes
 // rne(fl(fl(dY * sx[r]) / s2[c])) to q2.  A zero scale gives zero codes; a
-// subnormal one (its reciprocal loses precision) the exact quotient.
-template <bool BF16>
-__global__ __launch_bounds__(256) void grad_codes_kernel(
+// subnormal one (its reciprocal loses precision) the exact quotient, +-127 at
+// most.  SATURATE does that for the other scales too, where they are not this
+// gradient's maxima: +-127.25 s has the code of everything past it.
+template <bool BF16, bool SATURATE>
+__device__ __forceinline__ void grad_codes(
     const void *__restrict__ x, int64_t rows, int64_t cols, const float *__restrict__ sw,
     const float *__restrict__ sx, const float *__restrict__ s1, const float *__restrict__ s2,
     int8_t *__restrict__ q1, int8_t *__restrict__ q2)
@@ -662,6 +664,11 @@ __global__ __launch_bounds__(256) void grad_codes_kernel(
             o[0] = (int)pack4(c[0], c[1], c[2], c[3]);
             o[1] = (int)pack4(c[4], c[5], c[6], c[7]);
         } else {
+            if constexpr (SATURATE) {
+#pragma unroll
+                for (int e = 0; e < 8; e++)
+                    g[e] = __builtin_amdgcn_fmed3f(g[e], -127.25f * sr, 127.25f * sr);
+            }
             o = quant8(g, sr, recip_refined(sr));
         }
         *reinterpret_cast<i32x2 *>(q1 + r * cols + c0) = o;
@@ -670,6 +677,11 @@ __global__ __launch_bounds__(256) void grad_codes_kernel(
         for (int e = 0; e < 8; e++)
             g[e] = v[e] * p;
         if (!cexact) {
+            if constexpr (SATURATE) {
+#pragma unroll
+                for (int e = 0; e < 8; e++)
+                    g[e] = __builtin_amdgcn_fmed3f(g[e], -127.25f * sc[e], 127.25f * sc[e]);
+            }
             o = quant8_each(g, sc, inv);
         } else {
             float c[8];
@@ -681,6 +693,29 @@ __global__ __launch_bounds__(256) void grad_codes_kernel(
         }
         *reinterpret_cast<i32x2 *>(q2 + r * cols + c0) = o;
     }
+}
+
+template <bool BF16>
+__global__ __launch_bounds__(256) void grad_codes_kernel(
+    const void *__restrict__ x, int64_t rows, int64_t cols, const float *__restrict__ sw,
+    const float *__restrict__ sx, const float *__restrict__ s1, const float *__restrict__ s2,
+    int8_t *__restrict__ q1, int8_t *__restrict__ q2)
+{
+    grad_codes<BF16, false>(x, rows, cols, sw, sx, s1, s2, q1, q2);
+}
+
+template <bool BF16>
+__global__ __launch_bounds__(256) void grad_codes_scaled_kernel(
+    const void *__restrict__ x, int64_t rows, int64_t cols, const float *__restrict__ sw,
+    const float *__restrict__ sx, const float *__restrict__ s1, const float *__restrict__ s2,
+    int8_t *__restrict__ q1, int8_t *__restrict__ q2)
+{
+    grad_codes<BF16, true>(x, rows, cols, sw, sx, s1, s2, q1, q2);
+}
+
+static dim3 codes_grid(int64_t rows, int64_t cols)
+{
+    return dim3((unsigned)((cols / 8 + 255) / 256), (unsigned)((rows + kCodeRows - 1) / kCodeRows));
 }
 
 void launch_quantize_grad(const void *x, bool bf16, int64_t rows, int64_t cols, const float *sw,
@@ -712,23 +747,29 @@ void launch_quantize_grad(const void *x, bool bf16, int64_t rows, int64_t cols, 
     const unsigned gs = (unsigned)((cols + 63) / 64 + (rows + 1023) / 1024);
     hipLaunchKernelGGL(grad_scales_kernel, dim3(gs), dim3(1024), 0, st, rowpart, (int)wins,
                        colpart, (int)groups, rows, cols, s1, s2, col_sum);
-    launch_grad_codes(x, bf16, rows, cols, sw, sx, s1, s2, q1, q2, st);
-}
-
-// Also of a gradient whose scales come from elsewhere.  A bf16 dY may exceed the fp32
-// values that its scales are from by half a step, so that a quotient reaches 127 (1 +
-// 2^-8) = 127.496, which still rounds to 127.
-void launch_grad_codes(const void *x, bool bf16, int64_t rows, int64_t cols, const float *sw,
-                       const float *sx, const float *s1, const float *s2, int8_t *q1, int8_t *q2,
-                       hipStream_t st)
-{
-    const dim3 g2((unsigned)((cols / 8 + 255) / 256), (unsigned)((rows + kCodeRows - 1) / kCodeRows));
+    const dim3 g2 = codes_grid(rows, cols);
     if (bf16)
         hipLaunchKernelGGL(grad_codes_kernel<true>, g2, dim3(256), 0, st, x, rows, cols, sw, sx,
                            s1, s2, q1, q2);
     else
         hipLaunchKernelGGL(grad_codes_kernel<false>, g2, dim3(256), 0, st, x, rows, cols, sw, sx,
                            s1, s2, q1, q2);
+}
+
+// Of a gradient whose scales come from elsewhere.  A bf16 dY may exceed the fp32 values
+// that its scales are from by half a step: a quotient of 127 (1 + 2^-8) = 127.496, which
+// still rounds to 127, and where dY is subnormal in bf16 up to twice that.
+void launch_grad_codes(const void *x, bool bf16, int64_t rows, int64_t cols, const float *sw,
+                       const float *sx, const float *s1, const float *s2, int8_t *q1, int8_t *q2,
+                       hipStream_t st)
+{
+    const dim3 g = codes_grid(rows, cols);
+    if (bf16)
+        hipLaunchKernelGGL(grad_codes_scaled_kernel<true>, g, dim3(256), 0, st, x, rows, cols, sw,
+                           sx, s1, s2, q1, q2);
+    else
+        hipLaunchKernelGGL(grad_codes_scaled_kernel<false>, g, dim3(256), 0, st, x, rows, cols, sw,
+                           sx, s1, s2, q1, q2);
 }
 
 // --------------------------------------------------------------- rotation
