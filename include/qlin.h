@@ -699,6 +699,8 @@ size_t qlin_act_bwd_ws_bytes(int64_t M, int64_t F, int gated);
  * [M, N] int8 each, +-127 at most: a dy rounded to bf16 may exceed the fp32 values that
  * its scales are from (by 2^-8 of itself; where it is subnormal by half).  A zero scale
  * gives zero codes.
+ * M in [0, 1,048,560]; N in [16, QLIN_MAX_ROW], a multiple of 16: the limits of
+ * qlin_quantize_grad, below those of qlin_act_bwd.
  */
 int qlin_quantize_grad_scaled(const void *dy, int dtype, int64_t M, int64_t N, const float *sw,
                               const float *sx, const float *s1, const float *s2, int8_t *q1,

@@ -20,6 +20,7 @@ QLIN_OK, QLIN_EINVAL, QLIN_EUNSUPPORTED, QLIN_EDEVICE = 0, 1, 2, 3
 QLIN_F32, QLIN_BF16 = 0, 1
 QLIN_OP_FWD, QLIN_OP_DX, QLIN_OP_DW = 0, 1, 2
 MAX_CONTRACTION = 131071
+MAX_ROW = 131072
 MAX_RANK, MAX_ADAPTERS = 128, 1023
 ACTIVATIONS = {"none": 0, "relu": 1, "silu": 2, "gelu": 3, "gelu_tanh": 4}
 CK_BLOCK = 32

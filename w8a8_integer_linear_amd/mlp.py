@@ -32,7 +32,8 @@ class MLPW8A8Training:
         """w1: [F, K], with a gate [2 F, K] (the gate's rows first); w2: [N, F]; float GPU
         tensors in the original basis.  b1, b2: biases or None.  act: a name of
         ACTIVATIONS.  dtype: of h and of its gradient dz between the products (float32
-        or bfloat16)."""
+        or bfloat16).  A w1 of more than MAX_ROW rows serves only: its gradient's rows
+        are longer than quantization takes."""
         nat._act_code(act)
         rows, self.K = w1.shape
         self.N, self.F = w2.shape
@@ -87,6 +88,8 @@ class MLPW8A8Training:
         c = self.saved if saved is None else saved
         if c is None:
             raise RuntimeError("backward needs a forward pass before it (save=True)")
+        if self.fc1.N > nat.MAX_ROW:        # (before the first gradient is overwritten)
+            raise ValueError(f"backward: w1 has {self.fc1.N} rows, at most {nat.MAX_ROW} are trained")
         fc1, fc2 = self.fc1, self.fc2
         M, ws = c["qx"].shape[0], self._workspace(c["qx"].shape[0])
         q1, s1, q2, s2, _ = nat.qlin_quantize_grad(dy, fc2.sw, c["sh"], col_sum=fc2.db)
