@@ -67,6 +67,9 @@ class MLPW8A8Training:
         """x: [M, K], fp32 or bf16; residual: [M, N], fp32 or bf16, or None.  Returns y
         [M, N], the residual's type or x's.  What backward needs of this pass is left in
         self.saved, or self.saved is left alone (save=False: evaluation, serving)."""
+        if nat._elsewhere(x, None):         # another device than the current one
+            with nat._there(x, None):
+                return self.forward(x, residual, save)
         M = x.shape[0]
         fc1, fc2, ws = self.fc1, self.fc2, self._workspace(M)
         qx, sx = nat.qlin_quantize_rows(x, had_block=self.had)
@@ -90,6 +93,9 @@ class MLPW8A8Training:
             raise RuntimeError("backward needs a forward pass before it (save=True)")
         if self.fc1.N > nat.MAX_ROW:        # (before the first gradient is overwritten)
             raise ValueError(f"backward: w1 has {self.fc1.N} rows, at most {nat.MAX_ROW} are trained")
+        if nat._elsewhere(dy, None):
+            with nat._there(dy, None):
+                return self.backward(dy, c)
         fc1, fc2 = self.fc1, self.fc2
         M, ws = c["qx"].shape[0], self._workspace(c["qx"].shape[0])
         q1, s1, q2, s2, _ = nat.qlin_quantize_grad(dy, fc2.sw, c["sh"], col_sum=fc2.db)
