@@ -123,6 +123,13 @@ __device__ __forceinline__ uint32_t km_records(bool live, bool full, int trel, i
     return n < kOob ? n : kOob;
 }
 
+// The same of an operand whose loads are not masked (StageLoads' BFREE), left bytes
+// before its end.
+__host__ __device__ constexpr uint32_t free_records(bool live, uint32_t left)
+{
+    return !live ? 0 : left < kOob ? left : kOob;
+}
+
 typedef __attribute__((address_space(3))) int8_t lds_i8;
 
 // One operand tile of ROWS output rows (or columns) by kBK = 128 contraction
@@ -553,7 +560,8 @@ __device__ __forceinline__ void store_pass(const GemmParams &p, const lds_i8 *st
 //
 // BFREE: a contiguous B operand's loads are not masked in a partial stage (A's zeros
 // meet whatever B holds there): they run on into the operand's next rows, and past its
-// last one into the resource's end; bleft is the bytes from bbase to that.
+// last one into the resource's end; bleft is the bytes from bbase to that.  Those of a
+// stage past the unit's end meet an empty resource.
 template <typename OpA, typename OpB, bool AKM, bool BKM, int kBK, bool BFREE = false>
 struct StageLoads {
     static_assert(!BFREE || (!AKM && !BKM), "contiguous operands");
@@ -574,8 +582,7 @@ struct StageLoads {
         const int8_t *bk = BKM ? bbase + (int64_t)k0 * p.ldb : bbase + k0;
         L.ra = make_rsrc(ak, AKM ? km_records(L.live, L.full, L.trel, p.lda) : kOob);
         if constexpr (BFREE) {
-            const uint32_t left = bleft - (uint32_t)k0;
-            L.rb = make_rsrc(bk, left < kOob ? left : kOob);
+            L.rb = make_rsrc(bk, free_records(L.live, bleft - (uint32_t)k0));
         } else {
             L.rb = make_rsrc(bk, BKM ? km_records(L.live, L.full, L.trel, p.ldb) : kOob);
         }
