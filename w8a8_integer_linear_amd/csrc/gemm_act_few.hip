@@ -146,7 +146,9 @@ __global__ __launch_bounds__(WAVES * kWave) void few_act_kernel(GemmParams p)
         float z[8 * H];
 #pragma unroll
         for (int t = 0; t < 8 * H; t++) {
-            z[t] = (float)sums[row * kRow + col + t % 8 + (t >= 8 ? 32 : 0)] * rs * cs[t];
+            // (Past the last column: 0, whatever the weight's next rows gave.)
+            const int32_t sum = col_ok ? sums[row * kRow + col + t % 8 + (t >= 8 ? 32 : 0)] : 0;
+            z[t] = (float)sum * rs * cs[t];
             if (p.bias)
                 z[t] = z[t] + bj[t];
         }
