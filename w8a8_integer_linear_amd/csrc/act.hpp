@@ -7,8 +7,8 @@
 //              z/2 (1 + tanh(sqrt(2/pi) (z + 0.044715 z^3)))
 //
 // The logistic function is 1 / (1 + 2^(-z log2 e)) by the hardware's exp2 and
-// reciprocal (1 ulp each): a relative error of about 2^-22 plus 2^-24 |z| from
-// the rounded exponent, the latter where s(z) is small.
+// reciprocal (1 ulp each): a relative error of about 2^-22 plus 1.3 2^-24 |z| from
+// the rounded exponent and its constant, the latter where s(z) is small.
 //
 // Phi without a branch (the library's erf has two, of which a wave takes both): for x =
 // |z|, Phi(-x) is e^(-x^2/2) times a polynomial of degree 9 without a constant term in t =

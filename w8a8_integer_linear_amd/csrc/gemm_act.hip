@@ -26,7 +26,8 @@ template <int EPI> void run_tiles(const ProductArgs &a, const ActEpilogue &e, hi
 }
 
 // The product for M <= 16 tokens: the weight is streamed once, which bounds it (a bare
-// read of the same bytes: 117 MB 20.5 us, 59 MB 10.7; here 23.1 and 13.4).  A workgroup
+// read of 117 MB from memory takes 18.8 us, of 59 MB 10.2; this 23.0 for 3 tokens, 13.9
+// for 5; with the weight in the infinity cache 15.9, 9.0; 18.6, 11.6).  A workgroup
 // owns ROWS of its rows, with a gate ROWS / 2 of each half, and copies them CHUNK bytes
 // of each at a time into LDS by buffer-to-LDS loads, two chunks in flight, and with
 // them the tokens' values of the chunk into registers.  Inside a row, 16-byte piece c

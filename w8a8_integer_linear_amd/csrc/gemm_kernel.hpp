@@ -1090,11 +1090,9 @@ __global__ __launch_bounds__(WM *WN * 64, 1) void gemm_kernel(GemmParams p)
     // where fewer tiles may share the weight and more of it comes from HBM, its
     // loads are also for the stage after next, behind the pairs of row blocks 2-3,
     // and into a third buffer, whose reads passed the barrier before: they have
-    // more than a stage and a half to land (us, two buffers
-    // with lead 2 behind the last row block / three: 8192 x 4096 -> 2 x 14336 735 /
-    // 700, 2048 x 5376 -> 2 x 7168 151 / 141, 3700 x 5376 -> 7168 138 / 132, 8192 x
-    // 14336 -> 4096 355 / 345, 611 x 4096 -> 2 x 14336 94 / 90; with lead 1 777, 156,
-    // -, 376, 97.  Activations with lead 2 too: 749, 144, 137, 360, 90).
+    // more than a stage and a half to land (us in turn on one board, lead 1 / two buffers
+    // with lead 2 behind the last row block / three: 8192 x 4096 -> 2 x 14336 794 / 765 /
+    // 748, 2048 x 5376 -> 2 x 7168 132 / 130 / 122, 8192 x 14336 -> 4096 372 / 353 / 353).
     constexpr int kSpread = 8;
     constexpr bool kDeep = EPI >= EPI_ACT;
     constexpr int kLeadA = AKM ? 2 : 1, kLeadB = BKM || kDeep ? 2 : 1;
