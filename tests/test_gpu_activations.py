@@ -118,3 +118,45 @@ def test_the_largest_checkpoint():
     dy = torch.ones((M, N), device="cuda")
     dz = qlin.qlin_act_bwd(dy, ck, ck_s, "relu", dtype=torch.float32)[0]
     assert torch.equal(dz.cpu(), (b > 0).float().expand(M, N))
+
+
+@pytest.mark.parametrize("act", ["relu", "silu", "gelu", "gelu_tanh"])
+def test_a_block_with_an_infinity(act):
+    """Its scale is not finite and its codes say nothing of the other 31 values: none of
+    their gradients is a number, and the next block's are as without it."""
+    torch = torch_cuda()
+    import w8a8_integer_linear_amd as qlin
+    announce("infinite block", act)
+    M, N, K = 5, 64, 64
+    zeros = torch.zeros((M, K), dtype=torch.int8, device="cuda"), torch.zeros(M, device="cuda")
+    w = torch.zeros((N, K), dtype=torch.int8, device="cuda"), torch.ones(N, device="cuda")
+    b = torch.linspace(-2.0, 2.0, N, device="cuda")
+    clean = qlin.qlin_fwd_act(*zeros, *w, bias=b, act=act, save=True)
+    dy = torch.ones((M, N), device="cuda")
+    want = qlin.qlin_act_bwd(dy, *clean[1:], act, dtype=torch.float32)[0]
+    for bad in (float("inf"), -float("inf"), float("nan")):
+        b[9] = bad
+        y, ck, ck_s = qlin.qlin_fwd_act(*zeros, *w, bias=b, act=act, dtype=torch.float32, save=True)
+        assert not ck_s[:, 0].isfinite().any()
+        if bad != bad:
+            assert y[:, 9].isnan().all()
+        elif bad > 0:
+            assert (y[:, 9] == bad).all()
+        sw, sx = torch.ones(N, device="cuda"), torch.ones(M, device="cuda")
+        dz, s1, s2, db = qlin.qlin_act_bwd(dy, ck, ck_s, act, sw=sw, sx=sx, dtype=torch.float32, want_db=True)
+        assert dz[:, :32].isnan().all() and torch.equal(dz[:, 32:], want[:, 32:])
+        assert not s1.isfinite().any() and not s2[:32].isfinite().any() and not db[:32].isfinite().any()
+        assert s2[32:].isfinite().all() and db[32:].isfinite().all()
+
+
+@pytest.mark.parametrize("act", ["relu", "silu", "gelu", "gelu_tanh"])
+def test_an_infinite_scale(act):
+    """Of a checkpoint from elsewhere: the same, whatever its codes."""
+    torch = torch_cuda()
+    import w8a8_integer_linear_amd as qlin
+    announce("infinite scale", act)
+    ck = torch.arange(-64, 64, dtype=torch.int8, device="cuda").view(2, 64)
+    ck_s = torch.ones((2, 2), device="cuda")
+    ck_s[:, 0] = float("inf")
+    dz = qlin.qlin_act_bwd(torch.ones((2, 64), device="cuda"), ck, ck_s, act, dtype=torch.float32)[0]
+    assert dz[:, :32].isnan().all() and dz[:, 32:].isfinite().all()

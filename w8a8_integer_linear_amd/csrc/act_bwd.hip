@@ -29,13 +29,14 @@ struct Args {
 // Eight INT8 codes times a scale, each product rounded once: a code is taken as the
 // unsigned byte c + 128, which one instruction converts, and 128 s is taken off in a
 // fused multiply-add.  (A wave that meets a scale of 2^121 or more, where 128 s is past
-// fp32, takes the codes themselves: z from 3.37e38 on have such a scale, and infinite z.)
+// fp32, takes the codes themselves: z from 3.37e38 on have such a scale.  An infinite
+// scale's codes say nothing of its block, which is NaN: s - s.)
 __device__ __forceinline__ void codes_times(i32x2 q, float s, float v[8])
 {
     if (__ballot(!(s < 0x1p121f))) {
 #pragma unroll
         for (int e = 0; e < 8; e++)
-            v[e] = (float)(int8_t)((uint32_t)q[e / 4] >> (8 * (e % 4))) * s;
+            v[e] = (float)(int8_t)((uint32_t)q[e / 4] >> (8 * (e % 4))) * s + (s - s);
         return;
     }
     const float off = s * -128.0f;
