@@ -48,3 +48,21 @@ def test_scales_that_are_too_small(dtype, M, N):
         v = (dy.double() * by.double() / s.double()).clamp(-127, 127)
         assert ((q.cpu().double() - v).abs() <= 0.5 + 3 * 2.0 ** -24 * 127.5).all()
         assert int((v.abs() == 127).sum()) > 0
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+def test_values_that_are_not_finite(dtype):
+    """The same codes as qlin_quantize_grad's, for the scales that it gives such a gradient."""
+    torch = torch_cuda()
+    import w8a8_integer_linear_amd as qlin
+    M, N = 64, 272
+    g = torch.Generator().manual_seed(5)
+    sw, sx = (torch.rand(N, generator=g) + 0.5).cuda(), (torch.rand(M, generator=g) + 0.5).cuda()
+    for bad in (float("nan"), float("inf"), -float("inf")):
+        announce("codes of", bad, dtype)
+        dy = torch.randn((M, N), generator=g).to({"f32": torch.float32, "bf16": torch.bfloat16}[dtype])
+        dy[3, 7] = dy[40, 100] = dy[41, 100] = bad
+        dy = dy.cuda()
+        q1, s1, q2, s2, _ = qlin.qlin_quantize_grad(dy, sw, sx)
+        c1, c2 = qlin.qlin_quantize_grad_scaled(dy, sw, sx, s1, s2)
+        assert torch.equal(c1, q1) and torch.equal(c2, q2)

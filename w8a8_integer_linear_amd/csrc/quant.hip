@@ -617,6 +617,13 @@ __device__ __forceinline__ i32x2 quant8_each(const float g[8], const float s[8],
     return i32x2{pack(0), pack(4)};
 }
 
+// g within +-127.25 s, where codes of scale s end; a NaN stays one, as it reaches the
+// codes of a gradient's own scales (a median of three would make it the lower bound).
+__device__ __forceinline__ float saturated(float g, float s)
+{
+    return __builtin_elementwise_minimum(__builtin_elementwise_maximum(g, -127.25f * s), 127.25f * s);
+}
+
 // Pass 2: each thread owns 8 columns (their weight scales, column scales and
 // reciprocals stay in registers) and walks kCodeRows rows, writing the row
 // codes rne(fl(fl(dY * sw) / s1[r])) to q1 and the column codes
@@ -667,7 +674,7 @@ __device__ __forceinline__ void grad_codes(
             if constexpr (SATURATE) {
 #pragma unroll
                 for (int e = 0; e < 8; e++)
-                    g[e] = __builtin_amdgcn_fmed3f(g[e], -127.25f * sr, 127.25f * sr);
+                    g[e] = saturated(g[e], sr);
             }
             o = quant8(g, sr, recip_refined(sr));
         }
@@ -680,7 +687,7 @@ __device__ __forceinline__ void grad_codes(
             if constexpr (SATURATE) {
 #pragma unroll
                 for (int e = 0; e < 8; e++)
-                    g[e] = __builtin_amdgcn_fmed3f(g[e], -127.25f * sc[e], 127.25f * sc[e]);
+                    g[e] = saturated(g[e], sc[e]);
             }
             o = quant8_each(g, sc, inv);
         } else {
